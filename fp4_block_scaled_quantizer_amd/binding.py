@@ -8,9 +8,10 @@ this module raises -- there is no fallback path.
 from __future__ import annotations
 
 import ctypes
+import math
 import os
 import re
-from typing import Optional, Tuple
+from typing import NamedTuple, Optional, Tuple
 
 import torch
 
@@ -25,6 +26,8 @@ RNE, SR = 0, 1
 NV_GLOBAL, NV_TILE128 = 0, 1
 LAYOUT_LINEAR, LAYOUT_TILED = 0, 1
 OUT_F32, OUT_BF16 = 0, 1
+NORM_LAYER, NORM_RMS = 0, 1
+ROTARY_HALF, ROTARY_INTERLEAVED = 0, 1
 
 _lib = None
 
@@ -72,6 +75,17 @@ def lib() -> ctypes.CDLL:
     L.fp4_quantize_nv_noalloc.argtypes = [vp, i64, i64, i64, i32, i32, u64, u32, i32, vp, vp, vp, i32, vp]
     L.fp4_hadamard32_quantize_nv.argtypes = [vp, i64, i64, i64, i32, u32, i32, u64, u32, i32, vp, vp, vp, vp,
                                              ctypes.c_size_t, i32, vp]
+    L.fp4_dropout.argtypes = [vp, i64, i64, i64, i32, vp, i64, f32, u64, u32, vp, i64, vp]
+    L.fp4_norm.argtypes = [vp, i64, i64, i64, i32, vp, i64, f32, u64, u32, vp, i64, i32, vp, vp, i32, f32, vp, i64, vp,
+                           vp, vp, vp, i32, vp]
+    L.fp4q_norm_grad_workspace_bytes.argtypes = [i64, i64]
+    L.fp4q_norm_grad_workspace_bytes.restype = ctypes.c_size_t
+    L.fp4_norm_grad.argtypes = [vp, i64, i64, i64, i32, vp, i64, vp, i64, i32, vp, i32, vp, vp, f32, u64, u32, vp, i64,
+                                vp, i64, vp, vp, vp, ctypes.c_size_t, vp]
+    L.fp4_swiglu_grad_bf16.argtypes = [vp, i64, vp, i64, i64, i64, i64, vp, i64, vp, i64, vp]
+    L.fp4_rotary.argtypes = [vp, i64, i64, i64, i64, i64, i32, vp, i32, vp, i64, i32, i32, f32, vp, i64, i64, vp]
+    for fn in ("fp4_dropout", "fp4_norm", "fp4_norm_grad", "fp4_swiglu_grad_bf16", "fp4_rotary"):
+        getattr(L, fn).restype = i32
     for fn in ("fp4_quantize_mx", "fp4_hadamard32_quantize", "fp4_quantize_mx_dual", "fp4_quantize_nv",
                "fp4_quantize_nv_noalloc",
                "fp4_quantize_nv_amax", "fp4_hadamard32_quantize_nv", "fp4_gemm_mx", "fp4_gemm_nv",
@@ -428,3 +442,247 @@ def fp4_gemm_nv(a_codes: torch.Tensor, a_scales: torch.Tensor, a_tensor_scale: t
                                             domain, M, N, K, float(alpha), layout, c.data_ptr(), ctype, ldc,
                                             _stream(stream)))
     return c
+
+
+# ---- the row-wise operators between the GEMMs
+
+_TYPES = {torch.float32: OUT_F32, torch.bfloat16: OUT_BF16}
+
+
+def _matrix(t: torch.Tensor, name: str, like: Optional[torch.Tensor] = None) -> int:
+    """Leading dimension of a 2-D fp32 or bf16 matrix with unit column stride,
+    of `like`'s shape, type and device where that is given."""
+    if t.dim() != 2 or t.dtype not in _TYPES or (t.stride(1) != 1 and t.shape[1] > 1):
+        raise ValueError(f"{name} must be a 2-D fp32 or bf16 tensor with unit column stride")
+    if like is not None and (t.shape != like.shape or t.dtype != like.dtype or t.device != like.device):
+        raise ValueError(f"{name} must be a {tuple(like.shape)} {like.dtype} tensor on {like.device}, not "
+                         f"{tuple(t.shape)} {t.dtype} on {t.device}")
+    rows, cols = t.shape
+    if rows <= 1:
+        return cols
+    if t.stride(0) < cols:
+        raise ValueError(f"{name}'s rows overlap (row stride below their width)")
+    return t.stride(0)
+
+
+def _vector(t: Optional[torch.Tensor], name: str, n: int, device, dtype=None) -> Optional[int]:
+    if t is None:
+        return None
+    if t.dim() != 1 or t.shape[0] != n or t.device != device or not t.is_contiguous() or (
+            t.dtype != dtype if dtype is not None else t.dtype not in _TYPES):
+        raise ValueError(f"{name} must be a contiguous vector of {n} {dtype or 'fp32 or bf16'} elements on {device}")
+    return t.data_ptr()
+
+
+def _weights(gamma, beta, cols: int, device) -> Tuple[Optional[int], Optional[int], int]:
+    if gamma is not None and beta is not None and gamma.dtype != beta.dtype:
+        raise ValueError("gamma and beta must have the same type")
+    g, b = _vector(gamma, "gamma", cols, device), _vector(beta, "beta", cols, device)
+    w = gamma if gamma is not None else beta
+    return g, b, OUT_F32 if w is None else _TYPES[w.dtype]
+
+
+def fp4_dropout(x: torch.Tensor, p: float, *, seed: int, stream_id: int = 0, residual: Optional[torch.Tensor] = None,
+                y: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """[residual +] dropout(x): each element is kept with probability 1 - p
+    (from 16 random bits of (seed, stream_id, row, column)) and scaled. The
+    gradient is the same call on the gradient. y may be x or residual."""
+    ld_x = _matrix(x, "x")
+    rows, cols = x.shape
+    ld_r = 0 if residual is None else _matrix(residual, "residual", x)
+    if y is None:
+        y = torch.empty((rows, cols), dtype=x.dtype, device=x.device)
+    ld_y = _matrix(y, "y", x)
+    _check("fp4_dropout", lib().fp4_dropout(x.data_ptr(), rows, cols, ld_x, _TYPES[x.dtype], _ptr(residual), ld_r, p,
+                                            seed, stream_id, y.data_ptr(), ld_y, _stream(stream)))
+    return y
+
+
+class Norm(NamedTuple):
+    """fp4_norm's outputs; those not asked for are None."""
+    y: Optional[torch.Tensor]
+    h: Optional[torch.Tensor]
+    mean: Optional[torch.Tensor]
+    rstd: Optional[torch.Tensor]
+    codes: Optional[torch.Tensor]
+    scales: Optional[torch.Tensor]
+
+
+def fp4_norm(x: torch.Tensor, gamma: Optional[torch.Tensor] = None, beta: Optional[torch.Tensor] = None, *,
+             kind: int = NORM_LAYER, eps: float = 1e-5, residual: Optional[torch.Tensor] = None, p: float = 0.0,
+             seed: int = 0, stream_id: int = 0, save: bool = False, want_y: bool = True, mx: bool = False,
+             layout: int = LAYOUT_LINEAR, y: Optional[torch.Tensor] = None, h: Optional[torch.Tensor] = None,
+             mean: Optional[torch.Tensor] = None, rstd: Optional[torch.Tensor] = None,
+             codes: Optional[torch.Tensor] = None, scales: Optional[torch.Tensor] = None, stream=None) -> Norm:
+    """h = [residual +] dropout(x); y = norm(h) * gamma + beta, with kind
+    NORM_LAYER or NORM_RMS. h comes out where there is a residual or dropout
+    (else it is x); `save` asks for the row statistics that fp4_norm_grad
+    takes; `mx` for the MXFP4 operand of a bf16 y in `layout` (with want_y
+    False, instead of y). h and y may each be x or residual."""
+    ld_x = _matrix(x, "x")
+    rows, cols = x.shape
+    dev = x.device
+    ld_r = ld_h = ld_y = 0
+    if residual is not None:
+        ld_r = _matrix(residual, "residual", x)
+    if h is None and (residual is not None or p > 0):
+        h = torch.empty((rows, cols), dtype=x.dtype, device=dev)
+    if h is not None:
+        ld_h = _matrix(h, "h", x)
+    if y is None and want_y:
+        y = torch.empty((rows, cols), dtype=x.dtype, device=dev)
+    if y is not None:
+        ld_y = _matrix(y, "y", x)
+    if save and mean is None and kind == NORM_LAYER:
+        mean = torch.empty((rows,), dtype=torch.float32, device=dev)
+    if save and rstd is None:
+        rstd = torch.empty((rows,), dtype=torch.float32, device=dev)
+    if mx or codes is not None or scales is not None:
+        codes, scales = _mx_outputs(rows, cols, layout, codes, scales, dev)
+    g, b, wt = _weights(gamma, beta, cols, dev)
+    _check("fp4_norm",
+           lib().fp4_norm(x.data_ptr(), rows, cols, ld_x, _TYPES[x.dtype], _ptr(residual), ld_r, p, seed, stream_id,
+                          _ptr(h), ld_h, kind, g, b, wt, eps, _ptr(y), ld_y,
+                          _vector(mean, "mean", rows, dev, torch.float32),
+                          _vector(rstd, "rstd", rows, dev, torch.float32), _ptr(codes), _ptr(scales), layout,
+                          _stream(stream)))
+    return Norm(y, h, mean, rstd, codes, scales)
+
+
+class NormGrad(NamedTuple):
+    """fp4_norm_grad's outputs; those not asked for are None."""
+    dh: torch.Tensor
+    dx: Optional[torch.Tensor]
+    dgamma: Optional[torch.Tensor]
+    dbeta: Optional[torch.Tensor]
+
+
+def fp4_norm_grad(dy: torch.Tensor, h: torch.Tensor, gamma: Optional[torch.Tensor] = None, *, rstd: torch.Tensor,
+                  mean: Optional[torch.Tensor] = None, kind: int = NORM_LAYER, dres: Optional[torch.Tensor] = None,
+                  p: float = 0.0, seed: int = 0, stream_id: int = 0, weights: bool = True,
+                  dh: Optional[torch.Tensor] = None, dx: Optional[torch.Tensor] = None,
+                  dgamma: Optional[torch.Tensor] = None, dbeta: Optional[torch.Tensor] = None,
+                  workspace: Optional[torch.Tensor] = None, stream=None) -> NormGrad:
+    """The gradient of fp4_norm: dh of the normed rows (plus `dres`, what
+    reaches them along the residual stream), dx of fp4_norm's x where p > 0
+    (dx equals dh otherwise and is None), and with `weights` dgamma and, for
+    NORM_LAYER, dbeta in fp32. dh and dx may each be dy, h or dres."""
+    ld_dy = _matrix(dy, "dy")
+    rows, cols = dy.shape
+    dev = dy.device
+    ld_h = _matrix(h, "h", dy)
+    ld_dres = 0 if dres is None else _matrix(dres, "dres", dy)
+    if dh is None:
+        dh = torch.empty((rows, cols), dtype=dy.dtype, device=dev)
+    ld_dh, ld_dx = _matrix(dh, "dh", dy), 0
+    if dx is None and p > 0:
+        dx = torch.empty((rows, cols), dtype=dy.dtype, device=dev)
+    if dx is not None:
+        ld_dx = _matrix(dx, "dx", dy)
+    if weights and dgamma is None:
+        dgamma = torch.empty((cols,), dtype=torch.float32, device=dev)
+    if weights and dbeta is None and kind == NORM_LAYER:
+        dbeta = torch.empty((cols,), dtype=torch.float32, device=dev)
+    need = lib().fp4q_norm_grad_workspace_bytes(rows, cols) if dgamma is not None or dbeta is not None else 0
+    if workspace is None and need > 0:
+        workspace = torch.empty((need,), dtype=torch.uint8, device=dev)
+    if workspace is not None and (workspace.device != dev or not workspace.is_contiguous()):
+        raise ValueError("workspace must be a contiguous tensor on dy's device")
+    wbytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    g, _, wt = _weights(gamma, None, cols, dev)
+    _check("fp4_norm_grad",
+           lib().fp4_norm_grad(dy.data_ptr(), rows, cols, ld_dy, _TYPES[dy.dtype], h.data_ptr(), ld_h, _ptr(dres),
+                               ld_dres, kind, g, wt, _vector(mean, "mean", rows, dev, torch.float32),
+                               _vector(rstd, "rstd", rows, dev, torch.float32), p, seed, stream_id, dh.data_ptr(),
+                               ld_dh, _ptr(dx), ld_dx, _vector(dgamma, "dgamma", cols, dev, torch.float32),
+                               _vector(dbeta, "dbeta", cols, dev, torch.float32), _ptr(workspace), wbytes,
+                               _stream(stream)))
+    return NormGrad(dh, dx, dgamma, dbeta)
+
+
+def fp4_swiglu_grad_bf16(dh: torch.Tensor, c: torch.Tensor, *, pair: int = 32, want_h: bool = False,
+                         dc: Optional[torch.Tensor] = None, h: Optional[torch.Tensor] = None,
+                         stream=None) -> Tuple[torch.Tensor, Optional[torch.Tensor]]:
+    """The gradient of fp4_swiglu_bf16: (dc, h) from dh [M x F] and the bf16
+    C [M x >= 2F] whose columns interleave gate and up in groups of `pair`;
+    h (with `want_h`) is the forward's output again. dc may be c, h may be dh."""
+    if dh.dtype != torch.bfloat16 or c.dtype != torch.bfloat16:
+        raise ValueError("dh and c must be bf16")
+    M, f = dh.shape
+    ld_dh, ldc, ldh = _matrix(dh, "dh"), _matrix(c, "c"), 0
+    if c.shape[0] != M or c.shape[1] < 2 * f or c.device != dh.device:
+        raise ValueError(f"c must be a bf16 [{M} x >= {2 * f}] tensor on {dh.device}")
+    if dc is None:
+        dc = torch.empty((M, 2 * f), dtype=torch.bfloat16, device=c.device)
+    if dc.shape[0] != M or dc.shape[1] < 2 * f or dc.dtype != torch.bfloat16 or dc.device != dh.device:
+        raise ValueError(f"dc must be a bf16 [{M} x >= {2 * f}] tensor on {dh.device}")
+    if h is None and want_h:
+        h = torch.empty((M, f), dtype=torch.bfloat16, device=c.device)
+    if h is not None:
+        ldh = _matrix(h, "h", dh)
+    _check("fp4_swiglu_grad_bf16",
+           lib().fp4_swiglu_grad_bf16(dh.data_ptr(), ld_dh, c.data_ptr(), M, f, ldc, pair, dc.data_ptr(),
+                                      _matrix(dc, "dc"), _ptr(h), ldh, _stream(stream)))
+    return dc, h
+
+
+def _heads(t: torch.Tensor, name: str) -> Tuple[int, int]:
+    """(token stride, head stride) of a [tokens, heads, dim] view."""
+    if t.dim() != 3 or t.dtype not in _TYPES or (t.stride(2) != 1 and t.shape[2] > 1):
+        raise ValueError(f"{name} must be a [tokens, heads, dim] fp32 or bf16 tensor with unit stride along dim")
+    n, heads, dim = t.shape
+    head = t.stride(1) if heads > 1 else dim
+    return (t.stride(0) if n > 1 else max(1, heads) * head), head
+
+
+def fp4_rotary(x: torch.Tensor, positions: torch.Tensor, inv_freq: torch.Tensor, *, style: int = ROTARY_HALF,
+               scale: float = 1.0, inverse: bool = False, y: Optional[torch.Tensor] = None,
+               stream=None) -> torch.Tensor:
+    """Rotary positions of x [tokens, heads, dim] (any token and head
+    strides, so a slice of a fused QKV output serves): pair i of each head
+    turns by positions[t] * inv_freq[i], the first 2 len(inv_freq) elements
+    of the head taking part. `inverse` turns back: the gradient. y may be x."""
+    xt, xh = _heads(x, "x")
+    n, heads, dim = x.shape
+    if y is None:
+        y = torch.empty((n, heads, dim), dtype=x.dtype, device=x.device)
+    if y.shape != x.shape or y.dtype != x.dtype or y.device != x.device:
+        raise ValueError(f"y must be a {tuple(x.shape)} {x.dtype} tensor on {x.device}")
+    yt, yh = _heads(y, "y")
+    if positions.dtype not in (torch.int32, torch.int64):
+        raise ValueError("positions must be int32 or int64")
+    pos = _vector(positions, "positions", n, x.device, positions.dtype)
+    freq = _vector(inv_freq, "inv_freq", inv_freq.shape[0], x.device, torch.float32)
+    _check("fp4_rotary",
+           lib().fp4_rotary(x.data_ptr(), n, heads, dim, xt, xh, _TYPES[x.dtype], pos,
+                            64 if positions.dtype == torch.int64 else 32, freq, 2 * inv_freq.shape[0], style,
+                            int(bool(inverse)), scale, y.data_ptr(), yt, yh, _stream(stream)))
+    return y
+
+
+def rotary_frequencies(rot: int, base: float = 10000.0, *, factor: float = 1.0, method: str = "none",
+                       original_length: int = 8192, slow_turns: float = 1.0, fast_turns: float = 32.0,
+                       device=None) -> Tuple[torch.Tensor, float]:
+    """(inv_freq, scale) for fp4_rotary: rot / 2 frequencies base^(-2i/rot),
+    stretched for a context `factor` times the trained `original_length`:
+      "linear"  every frequency divided by factor (positions interpolated);
+      "base"    the base raised to base * factor^(rot / (rot - 2)), so that the
+                lowest frequency is divided by factor and the highest kept;
+      "turns"   by the turns a pair makes over the trained length: below
+                slow_turns divided by factor, above fast_turns kept, linear in
+                the turns between; scale = 1 + 0.1 ln factor.
+    A layout of constants made once, like pair_gate_up."""
+    if rot < 2 or rot % 2 or factor < 1 or method not in ("none", "linear", "base", "turns"):
+        raise ValueError("rot must be even and >= 2, factor >= 1, method none, linear, base or turns")
+    if method == "base" and rot > 2:
+        base = base * factor ** (rot / (rot - 2))
+    freq = base ** (-torch.arange(0, rot, 2, dtype=torch.float64) / rot)
+    scale = 1.0
+    if method == "linear":
+        freq = freq / factor
+    elif method == "turns":
+        turns = freq * original_length / (2 * math.pi)
+        keep = ((turns - slow_turns) / (fast_turns - slow_turns)).clamp(0, 1)
+        freq = freq * (keep + (1 - keep) / factor)
+        scale = 1 + 0.1 * math.log(factor)
+    return freq.to(torch.float32).to(device or "cpu"), scale

@@ -364,6 +364,39 @@ fp4q_status run_quantize_nv(const void *x, int64_t rows, int64_t cols, int64_t l
     return launched(fp4q::launch_quant_nv(a, domain, tensor_scale, workspace, given_amax, as_stream(stream)));
 }
 
+// ---- the row-wise operators between the GEMMs
+
+// A row-major [rows x cols] argument: its leading dimension and byte range.
+struct Matrix {
+    const void *p;
+    int64_t ld;
+    Range r;
+};
+Matrix matrix(const void *p, int64_t rows, int64_t cols, int64_t ld, uint64_t esize)
+{
+    return Matrix{p, ld, bytes(p, p ? ((uint64_t)(rows - 1) * (uint64_t)ld + (uint64_t)cols) * esize : 0)};
+}
+bool meet(Range a, Range b) { return a.lo != a.hi && b.lo != b.hi && overlap(a, b); }
+// An output and an input that share memory must be the same matrix.
+bool same_or_apart(const Matrix &out, const Matrix &in)
+{
+    return !meet(out.r, in.r) || (out.p == in.p && out.ld == in.ld);
+}
+
+bool type_ok(int type) { return type == FP4Q_OUT_F32 || type == FP4Q_OUT_BF16; }
+uint64_t type_size(int type) { return type == FP4Q_OUT_F32 ? 4 : 2; }
+bool p_ok(float p) { return p >= 0.0f && p <= 1.0f; }  // false for NaN
+bool ld_ok(const void *p, int64_t ld, int64_t cols) { return !p || (ld >= cols && ld <= kMaxDim); }
+
+constexpr int64_t kMaxNormCols = 32768;
+
+// Sizes of a [rows x cols] operator whose dropout counters are 32-bit.
+bool rows_cols_ok(int64_t rows, int64_t cols)
+{
+    return rows >= 0 && cols >= 0 && rows <= kMaxDim && cols <= kMaxDim &&
+           (uint64_t)rows * (uint64_t)((cols + 7) / 8) < (1ull << 32);
+}
+
 }  // namespace
 
 extern "C" {
@@ -532,6 +565,261 @@ fp4q_status fp4_quantize_nv_amax(const void *x, int64_t rows, int64_t cols, int6
     if (!aligned(amax, 4)) return FP4Q_EALIGN;
     return run_quantize_nv(x, rows, cols, ld_x, FP4Q_ALONG_ROWS, round, seed, stream_id, FP4Q_NV_GLOBAL, codes,
                            scales, tensor_scale, nullptr, 0, FP4Q_LAYOUT_LINEAR, amax, false, 0u, stream);
+}
+
+fp4q_status fp4_dropout(const void *x, int64_t rows, int64_t cols, int64_t ld_x, int type, const void *residual,
+                        int64_t ld_r, float p, uint64_t seed, uint32_t stream_id, void *y, int64_t ld_y, void *stream)
+{
+    if (!type_ok(type) || !p_ok(p)) return FP4Q_EINVAL;
+    if (!rows_cols_ok(rows, cols)) return FP4Q_ESHAPE;
+    if (ld_x < cols || ld_x > kMaxDim || ld_y < cols || ld_y > kMaxDim || !ld_ok(residual, ld_r, cols))
+        return FP4Q_ESHAPE;
+    if (rows == 0 || cols == 0) return FP4Q_OK;
+    if (!x || !y) return FP4Q_EINVAL;
+    const uint64_t es = type_size(type);
+    if (!aligned(x, es) || !aligned(y, es) || !aligned(residual, es)) return FP4Q_EALIGN;
+    const Matrix out = matrix(y, rows, cols, ld_y, es);
+    if (!same_or_apart(out, matrix(x, rows, cols, ld_x, es)) ||
+        !same_or_apart(out, matrix(residual, rows, cols, ld_r, es)))
+        return FP4Q_EINVAL;
+    fp4q::DropoutArgs a{};
+    a.x = x;
+    a.residual = residual;
+    a.rows = rows;
+    a.cols = cols;
+    a.ld_x = ld_x;
+    a.ld_r = ld_r;
+    a.ld_y = ld_y;
+    a.bf16 = type == FP4Q_OUT_BF16;
+    a.p = p;
+    a.seed = seed;
+    a.stream_id = stream_id;
+    a.y = y;
+    (void)hipGetLastError();
+    return launched(fp4q::launch_dropout(a, as_stream(stream)));
+}
+
+fp4q_status fp4_norm(const void *x, int64_t rows, int64_t cols, int64_t ld_x, int type, const void *residual,
+                     int64_t ld_r, float p, uint64_t seed, uint32_t stream_id, void *h, int64_t ld_h, int kind,
+                     const void *gamma, const void *beta, int w_type, float eps, void *y, int64_t ld_y, float *mean,
+                     float *rstd, void *codes, void *scales, int layout, void *stream)
+{
+    if (!type_ok(type) || !type_ok(w_type) || !p_ok(p) || (kind != FP4Q_NORM_LAYER && kind != FP4Q_NORM_RMS) ||
+        (layout != FP4Q_LAYOUT_LINEAR && layout != FP4Q_LAYOUT_TILED) || !(eps >= 0.0f))
+        return FP4Q_EINVAL;
+    if ((codes == nullptr) != (scales == nullptr) || (mean && kind == FP4Q_NORM_RMS)) return FP4Q_EINVAL;
+    if (!rows_cols_ok(rows, cols)) return FP4Q_ESHAPE;
+    if (ld_x < cols || ld_x > kMaxDim || !ld_ok(residual, ld_r, cols) || !ld_ok(h, ld_h, cols) || !ld_ok(y, ld_y, cols))
+        return FP4Q_ESHAPE;
+    const bool tiled = codes && layout == FP4Q_LAYOUT_TILED;
+    if (codes && cols % (tiled ? 128 : 32) != 0) return FP4Q_ESHAPE;
+    if (cols > kMaxNormCols || (codes && type != FP4Q_OUT_BF16)) return FP4Q_EUNSUPPORTED;
+    if (rows == 0 || cols == 0) return FP4Q_OK;
+    if (!x || (!y && !codes)) return FP4Q_EINVAL;
+    const uint64_t es = type_size(type), ws = type_size(w_type);
+    if (!aligned(x, es) || !aligned(residual, es) || !aligned(h, es) || !aligned(y, es) || !aligned(gamma, ws) ||
+        !aligned(beta, ws) || !aligned(mean, 4) || !aligned(rstd, 4) || !aligned(codes, 16) ||
+        (tiled && !aligned(scales, 16)))
+        return FP4Q_EALIGN;
+    const int64_t rows_out = tiled ? (rows + 31) / 32 * 32 : rows;
+    const Matrix in[2] = {matrix(x, rows, cols, ld_x, es), matrix(residual, rows, cols, ld_r, es)};
+    const Matrix mh = matrix(h, rows, cols, ld_h, es), my = matrix(y, rows, cols, ld_y, es);
+    const Range weights[2] = {bytes(gamma, gamma ? cols * ws : 0), bytes(beta, beta ? cols * ws : 0)};
+    const Range outs[6] = {mh.r, my.r, bytes(mean, mean ? rows * 4 : 0), bytes(rstd, rstd ? rows * 4 : 0),
+                           bytes(codes, codes ? (uint64_t)rows_out * cols / 2 : 0),
+                           bytes(scales, scales ? (uint64_t)rows_out * cols / 32 : 0)};
+    for (int i = 0; i < 6; ++i) {
+        for (int j = i + 1; j < 6; ++j)
+            if (meet(outs[i], outs[j])) return FP4Q_EINVAL;
+        for (const Range &w : weights)
+            if (meet(outs[i], w)) return FP4Q_EINVAL;
+        for (const Matrix &m : in) {
+            if (i >= 2 && meet(outs[i], m.r)) return FP4Q_EINVAL;
+        }
+    }
+    for (const Matrix &m : in)
+        if (!same_or_apart(mh, m) || !same_or_apart(my, m)) return FP4Q_EINVAL;
+    fp4q::NormArgs a{};
+    a.x = x;
+    a.residual = residual;
+    a.rows = rows;
+    a.cols = cols;
+    a.ld_x = ld_x;
+    a.ld_r = ld_r;
+    a.ld_h = ld_h;
+    a.ld_y = ld_y;
+    a.rows_out = rows_out;
+    a.bf16 = type == FP4Q_OUT_BF16;
+    a.layer = kind == FP4Q_NORM_LAYER;
+    a.gamma = gamma;
+    a.beta = beta;
+    a.w_bf16 = w_type == FP4Q_OUT_BF16;
+    a.eps = eps;
+    a.p = p;
+    a.seed = seed;
+    a.stream_id = stream_id;
+    a.h = h;
+    a.y = y;
+    a.mean = mean;
+    a.rstd = rstd;
+    a.codes = codes;
+    a.scales = scales;
+    a.tiled = tiled;
+    (void)hipGetLastError();
+    return launched(fp4q::launch_norm(a, as_stream(stream)));
+}
+
+size_t fp4q_norm_grad_workspace_bytes(int64_t rows, int64_t cols)
+{
+    return rows_cols_ok(rows, cols) && cols <= kMaxNormCols ? fp4q::norm_grad_workspace_bytes(rows, cols) : 0;
+}
+
+fp4q_status fp4_norm_grad(const void *dy, int64_t rows, int64_t cols, int64_t ld_dy, int type, const void *h,
+                          int64_t ld_h, const void *dres, int64_t ld_dres, int kind, const void *gamma, int w_type,
+                          const float *mean, const float *rstd, float p, uint64_t seed, uint32_t stream_id, void *dh,
+                          int64_t ld_dh, void *dx, int64_t ld_dx, float *dgamma, float *dbeta, void *workspace,
+                          size_t workspace_bytes, void *stream)
+{
+    if (!type_ok(type) || !type_ok(w_type) || !p_ok(p) || (kind != FP4Q_NORM_LAYER && kind != FP4Q_NORM_RMS))
+        return FP4Q_EINVAL;
+    if (!rows_cols_ok(rows, cols)) return FP4Q_ESHAPE;
+    if (ld_dy < cols || ld_dy > kMaxDim || ld_h < cols || ld_h > kMaxDim || !ld_ok(dres, ld_dres, cols) ||
+        !ld_ok(dh, ld_dh, cols) || !ld_ok(dx, ld_dx, cols))
+        return FP4Q_ESHAPE;
+    if (cols > kMaxNormCols) return FP4Q_EUNSUPPORTED;
+    if (cols == 0) return FP4Q_OK;
+    if (!aligned(dgamma, 4) || !aligned(dbeta, 4)) return FP4Q_EALIGN;
+    const bool sums = dgamma || dbeta;
+    if (rows == 0 && !sums) return FP4Q_OK;
+    const uint64_t es = type_size(type), ws = type_size(w_type);
+    if (rows > 0) {
+        if (!dy || !h || !rstd || (kind == FP4Q_NORM_LAYER && !mean) || (!dh && !dx && !sums)) return FP4Q_EINVAL;
+        const size_t need = sums ? fp4q::norm_grad_workspace_bytes(rows, cols) : 0;
+        if (need > 0 && (!workspace || workspace_bytes < need)) return FP4Q_EINVAL;
+        if (!aligned(dy, es) || !aligned(h, es) || !aligned(dres, es) || !aligned(dh, es) || !aligned(dx, es) ||
+            !aligned(gamma, ws) || !aligned(mean, 4) || !aligned(rstd, 4) || (need > 0 && !aligned(workspace, 16)))
+            return FP4Q_EALIGN;
+        const Matrix in[3] = {matrix(dy, rows, cols, ld_dy, es), matrix(h, rows, cols, ld_h, es),
+                              matrix(dres, rows, cols, ld_dres, es)};
+        const Matrix mo[2] = {matrix(dh, rows, cols, ld_dh, es), matrix(dx, rows, cols, ld_dx, es)};
+        const Range small[3] = {bytes(gamma, gamma ? cols * ws : 0), bytes(mean, mean ? rows * 4 : 0),
+                                bytes(rstd, rows * 4)};
+        const Range outs[5] = {mo[0].r, mo[1].r, bytes(dgamma, dgamma ? cols * 4 : 0),
+                               bytes(dbeta, dbeta ? cols * 4 : 0), bytes(workspace, need)};
+        for (int i = 0; i < 5; ++i) {
+            for (int j = i + 1; j < 5; ++j)
+                if (meet(outs[i], outs[j])) return FP4Q_EINVAL;
+            for (const Range &r : small)
+                if (meet(outs[i], r)) return FP4Q_EINVAL;
+            for (const Matrix &m : in) {
+                if (i < 2 ? !same_or_apart(mo[i], m) : meet(outs[i], m.r)) return FP4Q_EINVAL;
+            }
+        }
+    }
+    fp4q::NormGradArgs a{};
+    a.dy = dy;
+    a.h = h;
+    a.dres = dres;
+    a.rows = rows;
+    a.cols = cols;
+    a.ld_dy = ld_dy;
+    a.ld_h = ld_h;
+    a.ld_dres = ld_dres;
+    a.ld_dh = ld_dh;
+    a.ld_dx = ld_dx;
+    a.bf16 = type == FP4Q_OUT_BF16;
+    a.layer = kind == FP4Q_NORM_LAYER;
+    a.gamma = gamma;
+    a.w_bf16 = w_type == FP4Q_OUT_BF16;
+    a.mean = mean;
+    a.rstd = rstd;
+    a.p = p;
+    a.seed = seed;
+    a.stream_id = stream_id;
+    a.dh = dh;
+    a.dx = dx;
+    a.parts = reinterpret_cast<float *>(workspace);
+    (void)hipGetLastError();
+    return launched(fp4q::launch_norm_grad(a, dgamma, dbeta, as_stream(stream)));
+}
+
+fp4q_status fp4_swiglu_grad_bf16(const void *dh, int64_t ld_dh, const void *c, int64_t M, int64_t F, int64_t ldc,
+                                 int64_t pair, void *dc, int64_t ld_dc, void *h, int64_t ldh, void *stream)
+{
+    if (M < 0 || F < 0 || M > kMaxDim || F > kMaxDim) return FP4Q_ESHAPE;
+    if (F % 8 != 0 || pair <= 0 || pair % 8 != 0 || (F > 0 && F % pair != 0) || ldc < 2 * F || ld_dc < 2 * F ||
+        ld_dh < F || ldc % 8 != 0 || ld_dc % 8 != 0 || ld_dh % 8 != 0 || ldc > kMaxDim * 2 || ld_dc > kMaxDim * 2 ||
+        ld_dh > kMaxDim || (h && (ldh < F || ldh % 8 != 0 || ldh > kMaxDim)))
+        return FP4Q_ESHAPE;
+    if (M == 0 || F == 0) return FP4Q_OK;
+    if (!dh || !c || !dc) return FP4Q_EINVAL;
+    if (!aligned(dh, 16) || !aligned(c, 16) || !aligned(dc, 16) || !aligned(h, 16)) return FP4Q_EALIGN;
+    const Matrix mi = matrix(dh, M, F, ld_dh, 2), mc = matrix(c, M, 2 * F, ldc, 2);
+    const Matrix mo = matrix(dc, M, 2 * F, ld_dc, 2), mh = matrix(h, M, F, ldh, 2);
+    if (meet(mo.r, mi.r) || !same_or_apart(mo, mc) || meet(mh.r, mc.r) || meet(mh.r, mo.r) || !same_or_apart(mh, mi))
+        return FP4Q_EINVAL;
+    fp4q::SwigluGradArgs a{};
+    a.dh = dh;
+    a.c = c;
+    a.M = M;
+    a.F = F;
+    a.ld_dh = ld_dh;
+    a.ldc = ldc;
+    a.ld_dc = ld_dc;
+    a.ldh = ldh;
+    a.pair = pair;
+    a.dc = dc;
+    a.h = h;
+    (void)hipGetLastError();
+    return launched(fp4q::launch_swiglu_grad(a, as_stream(stream)));
+}
+
+fp4q_status fp4_rotary(const void *x, int64_t tokens, int64_t heads, int64_t dim, int64_t x_token, int64_t x_head,
+                       int type, const void *positions, int position_bits, const float *inv_freq, int64_t rot,
+                       int style, int inverse, float scale, void *y, int64_t y_token, int64_t y_head, void *stream)
+{
+    if (!type_ok(type) || (position_bits != 32 && position_bits != 64) ||
+        (style != FP4Q_ROTARY_HALF && style != FP4Q_ROTARY_INTERLEAVED) || (inverse != 0 && inverse != 1))
+        return FP4Q_EINVAL;
+    if (tokens < 0 || heads < 0 || dim < 0 || tokens > kMaxDim || heads > 65536 || dim > 1024 || rot < 2 ||
+        rot % 2 != 0 || rot > dim)
+        return FP4Q_ESHAPE;
+    // the heads of a token lie side by side or apart, and so do the tokens
+    if (x_head < dim || y_head < dim || x_head > kMaxDim || y_head > kMaxDim || x_token > kMaxDim || y_token > kMaxDim ||
+        (heads > 0 && (x_token < (heads - 1) * x_head + dim || y_token < (heads - 1) * y_head + dim)))
+        return FP4Q_ESHAPE;
+    if (tokens == 0 || heads == 0) return FP4Q_OK;
+    if (!x || !y || !positions || !inv_freq) return FP4Q_EINVAL;
+    const uint64_t es = type_size(type);
+    if (!aligned(x, es) || !aligned(y, es) || !aligned(positions, position_bits / 8) || !aligned(inv_freq, 4))
+        return FP4Q_EALIGN;
+    const Range rx = bytes(x, ((uint64_t)(tokens - 1) * x_token + (uint64_t)(heads - 1) * x_head + dim) * es);
+    const Range ry = bytes(y, ((uint64_t)(tokens - 1) * y_token + (uint64_t)(heads - 1) * y_head + dim) * es);
+    const bool in_place = x == y && x_token == y_token && x_head == y_head;
+    if ((meet(rx, ry) && !in_place) || meet(ry, bytes(positions, (uint64_t)tokens * position_bits / 8)) ||
+        meet(ry, bytes(inv_freq, (uint64_t)rot / 2 * 4)))
+        return FP4Q_EINVAL;
+    fp4q::RotaryArgs a{};
+    a.x = x;
+    a.tokens = tokens;
+    a.x_token = x_token;
+    a.x_head = x_head;
+    a.y_token = y_token;
+    a.y_head = y_head;
+    a.heads = (uint32_t)heads;
+    a.dim = (uint32_t)dim;
+    a.rot = (uint32_t)rot;
+    a.bf16 = type == FP4Q_OUT_BF16;
+    a.interleaved = style == FP4Q_ROTARY_INTERLEAVED;
+    a.inverse = inverse != 0;
+    a.pos64 = position_bits == 64;
+    a.copy = !in_place && rot < dim;
+    a.positions = positions;
+    a.inv_freq = inv_freq;
+    a.scale = scale;
+    a.y = y;
+    (void)hipGetLastError();
+    return launched(fp4q::launch_rotary(a, as_stream(stream)));
 }
 
 const char *fp4q_status_str(int status)

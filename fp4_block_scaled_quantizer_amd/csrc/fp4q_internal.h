@@ -47,6 +47,68 @@ struct GemmArgs {
     bool q_swiglu;
 };
 
+struct DropoutArgs {
+    const void *x, *residual;  // residual: optional
+    int64_t rows, cols, ld_x, ld_r, ld_y;
+    bool bf16;  // elements, else binary32
+    float p;
+    uint64_t seed;
+    uint32_t stream_id;
+    void *y;
+};
+
+struct NormArgs {
+    const void *x, *residual;  // residual: optional
+    int64_t rows, cols, ld_x, ld_r, ld_h, ld_y;
+    int64_t rows_out;  // rows, or in the tiled MX layout rows rounded up to 32
+    bool bf16;
+    bool layer;  // else RMS
+    const void *gamma, *beta;  // optional
+    bool w_bf16;
+    float eps, p;
+    uint64_t seed;
+    uint32_t stream_id;
+    void *h, *y;         // optional
+    float *mean, *rstd;  // optional
+    void *codes, *scales;  // optional: the MXFP4 operand of a bf16 y
+    bool tiled;
+};
+
+struct NormGradArgs {
+    const void *dy, *h, *dres;  // dres: optional
+    int64_t rows, cols, ld_dy, ld_h, ld_dres, ld_dh, ld_dx;
+    bool bf16;
+    bool layer;
+    const void *gamma;  // optional
+    bool w_bf16;
+    const float *mean, *rstd;
+    float p;
+    uint64_t seed;
+    uint32_t stream_id;
+    void *dh, *dx;  // one of them optional
+    float *parts;   // workspace: the workgroups' weight sums
+    bool layer_beta;  // dbeta is asked for
+};
+
+struct SwigluGradArgs {
+    const void *dh, *c;
+    int64_t M, F, ld_dh, ldc, ld_dc, ldh, pair;
+    void *dc, *h;  // h: optional
+};
+
+struct RotaryArgs {
+    const void *x;
+    int64_t tokens, x_token, x_head, y_token, y_head;
+    uint32_t heads, dim, rot;
+    bool bf16, interleaved, inverse, pos64;
+    bool copy;  // the elements past rot have to be copied (y is not x)
+    const void *positions;
+    const float *inv_freq;
+    float scale;
+    void *y;
+    uint32_t tokens_at_once;
+};
+
 // Compute units of the current device (the persistent GEMMs' grid), looked
 // up once per device; <= 0 if the device cannot be queried.
 int device_cu_count();
@@ -63,5 +125,11 @@ int launch_gemm_nv(const GemmArgs &g, hipStream_t st);
 // and up in groups of `pair` (a multiple of 8 dividing F)
 int launch_swiglu(const void *c, int64_t M, int64_t F, int64_t ldc, int64_t pair, void *h, int64_t ldh,
                   hipStream_t st);
+int launch_dropout(const DropoutArgs &a, hipStream_t st);
+int launch_norm(const NormArgs &a, hipStream_t st);
+size_t norm_grad_workspace_bytes(int64_t rows, int64_t cols);
+int launch_norm_grad(NormGradArgs a, float *dgamma, float *dbeta, hipStream_t st);
+int launch_swiglu_grad(const SwigluGradArgs &a, hipStream_t st);
+int launch_rotary(RotaryArgs a, hipStream_t st);
 
 }  // namespace fp4q

@@ -144,6 +144,8 @@ typedef enum { FP4Q_RNE = 0, FP4Q_SR = 1 } fp4q_round;
 typedef enum { FP4Q_NV_GLOBAL = 0, FP4Q_NV_TILE128 = 1 } fp4q_nv_domain;
 typedef enum { FP4Q_LAYOUT_LINEAR = 0, FP4Q_LAYOUT_TILED = 1 } fp4q_layout;
 typedef enum { FP4Q_OUT_F32 = 0, FP4Q_OUT_BF16 = 1 } fp4q_out;
+typedef enum { FP4Q_NORM_LAYER = 0, FP4Q_NORM_RMS = 1 } fp4q_norm;
+typedef enum { FP4Q_ROTARY_HALF = 0, FP4Q_ROTARY_INTERLEAVED = 1 } fp4q_rotary;
 
 /* MXFP4 producer ("native mxfp", [Fusion] section "The Design Philosophy of
  * Format-Aware Fusion"; steps of [Stack] section "The first change").
@@ -344,6 +346,104 @@ FP4Q_API fp4q_status fp4_gemm_nv_amax(const void *a_codes, const void *a_scales,
 FP4Q_API fp4q_status fp4_quantize_nv_amax(const void *x, int64_t rows, int64_t cols, int64_t ld_x, int round,
                                  uint64_t seed, uint32_t stream_id, const float *amax, void *codes, void *scales,
                                  float *tensor_scale, void *stream);
+
+/* ------------------------------------------------------------------------
+ * The row-wise operators between a transformer block's GEMMs: what turns one
+ * GEMM's output into the next one's input, forward and backward.
+ *
+ * Elements are binary32 or bf16 (`type`, `w_type`: the values of fp4q_out),
+ * one type for a call's matrices; everything is computed in binary32 and
+ * rounded once to that type.  Matrices are row-major with leading dimensions
+ * in elements; widths, leading dimensions and pointers need only the
+ * element's alignment (rows whose width, pitch and start are multiples of
+ * eight elements are the fast ones).  An output may be one of the inputs
+ * named at the call, with the same leading dimension, or must not overlap
+ * any.  NaN and Inf follow the formulas; they stay within their row, and
+ * within their column of the weight gradients.  Errors as above, plus
+ * FP4Q_ESHAPE where rows * ceil(cols / 8) reaches 2^32.
+ * ------------------------------------------------------------------------ */
+
+/* Dropout with a mask that is never stored, and an optional residual add:
+ * y = [residual +] (kept ? x * scale : 0).  Element (r, k) draws 16 bits as
+ * FP4Q_SR does, under the counter {k/8, r, stream_id, 1} (the last word keeps
+ * the two apart), and is kept iff they are >= D = rint(65536 p); scale =
+ * 65536 / (65536 - D).  p in [0, 1] (FP4Q_EINVAL otherwise); p = 1 drops
+ * everything.  A dropped element is 0 whatever x holds.  The gradient of x is
+ * the same call on the gradient of y, without residual.  y may be x or
+ * residual. */
+FP4Q_API fp4q_status fp4_dropout(const void *x, int64_t rows, int64_t cols, int64_t ld_x, int type,
+                                 const void *residual, int64_t ld_r, float p, uint64_t seed, uint32_t stream_id,
+                                 void *y, int64_t ld_y, void *stream);
+
+/* Layer norm or RMS norm of each row, after an optional dropout and residual
+ * add, before an optional MXFP4 producer:
+ *   h    = [residual +] dropout(x, p, seed, stream_id), rounded to `type`;
+ *   mean = sum h / cols (RMS: 0),  rstd = 1 / sqrt(sum (h - mean)^2 / cols + eps);
+ *   y    = (h - mean) * rstd * gamma + beta.
+ * Optional (null): residual, gamma (1), beta (0), and of the outputs h, mean
+ * (must be null for RMS), rstd, and y if codes are asked for.  With codes and
+ * scales (bf16 only: FP4Q_EUNSUPPORTED for binary32) the MXFP4 operand of y
+ * leaves as well, byte for byte as fp4_quantize_mx (FP4Q_ALONG_ROWS, FP4Q_RNE,
+ * `layout`) makes it of y; then cols % 32 == 0 (linear) or % 128 == 0
+ * (tiled), codes 16-byte aligned (tiled: scales too).  cols <= 32768
+ * (FP4Q_EUNSUPPORTED above).  h and y may each be x or residual. */
+FP4Q_API fp4q_status fp4_norm(const void *x, int64_t rows, int64_t cols, int64_t ld_x, int type, const void *residual,
+                              int64_t ld_r, float p, uint64_t seed, uint32_t stream_id, void *h, int64_t ld_h,
+                              int kind, const void *gamma, const void *beta, int w_type, float eps, void *y,
+                              int64_t ld_y, float *mean, float *rstd, void *codes, void *scales, int layout,
+                              void *stream);
+
+/* Bytes of device workspace fp4_norm_grad needs for its weight gradients. */
+FP4Q_API size_t fp4q_norm_grad_workspace_bytes(int64_t rows, int64_t cols);
+
+/* The gradient of fp4_norm.  With xh = (h - mean) * rstd and g = dy * gamma:
+ *   dh     = [dres +] rstd * (g - sum g / cols - xh * sum(g xh) / cols)
+ *            (RMS: xh = h * rstd, and no sum g term);
+ *   dx     = kept ? dh * scale : 0, the mask that fp4_norm drew for the same
+ *            p, seed and stream_id (from dh before its rounding);
+ *   dgamma = sum over rows of dy * xh,  dbeta = sum over rows of dy, binary32.
+ * dres is the gradient that reaches h along the residual stream; dh is then
+ * also the gradient of `residual`.  h, mean and rstd as fp4_norm wrote them
+ * (h is x where there was neither dropout nor residual; mean is not read for
+ * RMS).  Optional (null): dres, gamma (1), dx, dgamma, dbeta, and dh where
+ * another output is asked for.  The weight gradients are summed in a fixed
+ * order (two calls give the same bits) and need `workspace` (16-byte
+ * aligned); with rows == 0 they are set to 0.  cols <= 32768.  dh and dx may
+ * each be dy, h or dres. */
+FP4Q_API fp4q_status fp4_norm_grad(const void *dy, int64_t rows, int64_t cols, int64_t ld_dy, int type, const void *h,
+                                   int64_t ld_h, const void *dres, int64_t ld_dres, int kind, const void *gamma,
+                                   int w_type, const float *mean, const float *rstd, float p, uint64_t seed,
+                                   uint32_t stream_id, void *dh, int64_t ld_dh, void *dx, int64_t ld_dx, float *dgamma,
+                                   float *dbeta, void *workspace, size_t workspace_bytes, void *stream);
+
+/* The gradient of fp4_swiglu_bf16 (h = SiLU(g) u, columns of c in groups of
+ * `pair` as there), sigma = 1 / (1 + e^-g):
+ *   dc at gate columns = dh * u * (sigma + g sigma (1 - sigma)),
+ *   dc at up columns   = dh * g sigma,
+ * bf16, in c's column order with pitch ld_dc.  h (optional): h itself again,
+ * bit for bit as fp4_swiglu_bf16 writes it, so that a training step need not
+ * keep it for the down projection's weight gradient.  Requirements as
+ * fp4_swiglu_bf16 (FP4Q_ESHAPE, FP4Q_EALIGN).  dc may be c, h may be dh. */
+FP4Q_API fp4q_status fp4_swiglu_grad_bf16(const void *dh, int64_t ld_dh, const void *c, int64_t M, int64_t F,
+                                          int64_t ldc, int64_t pair, void *dc, int64_t ld_dc, void *h, int64_t ldh,
+                                          void *stream);
+
+/* Rotary positions.  Element (t, head, d) of x lies at t * x_token + head *
+ * x_head + d, so the query and key heads can be rotated where a fused QKV
+ * GEMM left them.  Pair i of a head (elements i and i + rot/2 in the half
+ * style, 2i and 2i + 1 interleaved) turns by positions[t] * inv_freq[i]:
+ *   (a, b) -> scale * (a cos - b sin, b cos + a sin),
+ * by the opposite angle with inverse = 1 (the gradient: scale * R^T); the
+ * elements from rot on are copied.  positions: 32- or 64-bit integers
+ * (position_bits), any order, so packed sequences restart where they like;
+ * inv_freq: rot/2 binary32, scaled for a long context as its user wants.  The
+ * angle's whole turns are removed in binary64.  FP4Q_ESHAPE unless 2 <= rot
+ * <= dim <= 1024, rot even, heads <= 65536, heads and tokens not overlapping
+ * (x_head >= dim, x_token >= the span of a token's heads).  y may be x. */
+FP4Q_API fp4q_status fp4_rotary(const void *x, int64_t tokens, int64_t heads, int64_t dim, int64_t x_token,
+                                int64_t x_head, int type, const void *positions, int position_bits,
+                                const float *inv_freq, int64_t rot, int style, int inverse, float scale, void *y,
+                                int64_t y_token, int64_t y_head, void *stream);
 
 /* Human-readable text for a status code (static storage). */
 FP4Q_API const char *fp4q_status_str(int status);
