@@ -445,41 +445,65 @@ def fp4_gemm_nv(a_codes: torch.Tensor, a_scales: torch.Tensor, a_tensor_scale: t
 
 
 # ---- the row-wise operators between the GEMMs
+#
+# A decoding step makes these calls on a few kilobytes each, so what they
+# check is read from each tensor once.
 
 _TYPES = {torch.float32: OUT_F32, torch.bfloat16: OUT_BF16}
+_new = tuple.__new__  # of a NamedTuple, at a third of its own constructor's time
 
 
-def _matrix(t: torch.Tensor, name: str, like: Optional[torch.Tensor] = None) -> int:
-    """Leading dimension of a 2-D fp32 or bf16 matrix with unit column stride,
-    of `like`'s shape, type and device where that is given."""
-    if t.dim() != 2 or t.dtype not in _TYPES or (t.stride(1) != 1 and t.shape[1] > 1):
-        raise ValueError(f"{name} must be a 2-D fp32 or bf16 tensor with unit column stride")
-    if like is not None and (t.shape != like.shape or t.dtype != like.dtype or t.device != like.device):
-        raise ValueError(f"{name} must be a {tuple(like.shape)} {like.dtype} tensor on {like.device}, not "
-                         f"{tuple(t.shape)} {t.dtype} on {t.device}")
-    rows, cols = t.shape
-    if rows <= 1:
-        return cols
-    if t.stride(0) < cols:
-        raise ValueError(f"{name}'s rows overlap (row stride below their width)")
-    return t.stride(0)
+def _row_stream(stream, dev: int) -> int:
+    """The stream's handle; the tensors' GPU has to be the current one, which
+    the library launches on."""
+    if dev < 0 or dev != torch._C._cuda_getDevice():
+        raise ValueError("the tensors must be on the current GPU")
+    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
 
 
-def _vector(t: Optional[torch.Tensor], name: str, n: int, device, dtype=None) -> Optional[int]:
-    if t is None:
-        return None
-    if t.dim() != 1 or t.shape[0] != n or t.device != device or not t.is_contiguous() or (
-            t.dtype != dtype if dtype is not None else t.dtype not in _TYPES):
-        raise ValueError(f"{name} must be a contiguous vector of {n} {dtype or 'fp32 or bf16'} elements on {device}")
+def _first(t: torch.Tensor, name: str) -> Tuple[torch.Size, int, torch.dtype, int, int]:
+    """(shape, leading dimension, dtype, the library's type, device index) of
+    a call's first matrix: 2-D, fp32 or bf16, unit column stride."""
+    shape, dtype = t.shape, t.dtype
+    kind = _TYPES.get(dtype)
+    if kind is None or len(shape) != 2:
+        raise ValueError(f"{name} must be a 2-D fp32 or bf16 tensor")
+    ld, one = t.stride()
+    cols = shape[1]
+    if shape[0] <= 1:
+        ld = cols
+    if ld < cols or (one != 1 and cols > 1):
+        raise ValueError(f"{name} must have unit column stride and rows that do not overlap")
+    return shape, ld, dtype, kind, t.get_device()
+
+
+def _ld(t: torch.Tensor, name: str, shape: torch.Size, dtype: torch.dtype, dev: int) -> int:
+    """Leading dimension of another matrix, which has the first one's shape,
+    dtype and device."""
+    if t.shape != shape or t.dtype is not dtype or t.get_device() != dev:
+        raise ValueError(f"{name} must be a {tuple(shape)} {dtype} tensor on the same device, not {tuple(t.shape)} "
+                         f"{t.dtype} on {t.device}")
+    ld, one = t.stride()
+    cols = shape[1]
+    if shape[0] <= 1:
+        ld = cols
+    if ld < cols or (one != 1 and cols > 1):
+        raise ValueError(f"{name} must have unit column stride and rows that do not overlap")
+    return ld
+
+
+def _vector(t: torch.Tensor, name: str, n: int, dtype: torch.dtype, dev: int) -> int:
+    if t.numel() != n or t.dtype is not dtype or t.get_device() != dev or not t.is_contiguous():
+        raise ValueError(f"{name} must be {n} contiguous {dtype} elements on the same device")
     return t.data_ptr()
 
 
-def _weights(gamma, beta, cols: int, device) -> Tuple[Optional[int], Optional[int], int]:
-    if gamma is not None and beta is not None and gamma.dtype != beta.dtype:
-        raise ValueError("gamma and beta must have the same type")
-    g, b = _vector(gamma, "gamma", cols, device), _vector(beta, "beta", cols, device)
-    w = gamma if gamma is not None else beta
-    return g, b, OUT_F32 if w is None else _TYPES[w.dtype]
+def _weight(t: torch.Tensor, name: str, n: int, dev: int) -> Tuple[int, int]:
+    dtype = t.dtype
+    kind = _TYPES.get(dtype)
+    if kind is None:
+        raise ValueError(f"{name} must be fp32 or bf16")
+    return _vector(t, name, n, dtype, dev), kind
 
 
 def fp4_dropout(x: torch.Tensor, p: float, *, seed: int, stream_id: int = 0, residual: Optional[torch.Tensor] = None,
@@ -487,14 +511,16 @@ def fp4_dropout(x: torch.Tensor, p: float, *, seed: int, stream_id: int = 0, res
     """[residual +] dropout(x): each element is kept with probability 1 - p
     (from 16 random bits of (seed, stream_id, row, column)) and scaled. The
     gradient is the same call on the gradient. y may be x or residual."""
-    ld_x = _matrix(x, "x")
-    rows, cols = x.shape
-    ld_r = 0 if residual is None else _matrix(residual, "residual", x)
+    shape, ld_x, dtype, kind, dev = _first(x, "x")
+    res, ld_r = None, 0
+    if residual is not None:
+        res, ld_r = residual.data_ptr(), _ld(residual, "residual", shape, dtype, dev)
     if y is None:
-        y = torch.empty((rows, cols), dtype=x.dtype, device=x.device)
-    ld_y = _matrix(y, "y", x)
-    _check("fp4_dropout", lib().fp4_dropout(x.data_ptr(), rows, cols, ld_x, _TYPES[x.dtype], _ptr(residual), ld_r, p,
-                                            seed, stream_id, y.data_ptr(), ld_y, _stream(stream)))
+        y = torch.empty(shape, dtype=dtype, device=x.device)
+    status = lib().fp4_dropout(x.data_ptr(), shape[0], shape[1], ld_x, kind, res, ld_r, p, seed, stream_id,
+                               y.data_ptr(), _ld(y, "y", shape, dtype, dev), _row_stream(stream, dev))
+    if status:
+        raise Fp4qError("fp4_dropout", status)
     return y
 
 
@@ -519,34 +545,43 @@ def fp4_norm(x: torch.Tensor, gamma: Optional[torch.Tensor] = None, beta: Option
     (else it is x); `save` asks for the row statistics that fp4_norm_grad
     takes; `mx` for the MXFP4 operand of a bf16 y in `layout` (with want_y
     False, instead of y). h and y may each be x or residual."""
-    ld_x = _matrix(x, "x")
-    rows, cols = x.shape
-    dev = x.device
-    ld_r = ld_h = ld_y = 0
+    shape, ld_x, dtype, kt, dev = _first(x, "x")
+    rows, cols = shape
+    pr = ph = py = pm = ps = pg = pb = pc = pe = None
+    ld_r = ld_h = ld_y = wt = 0
     if residual is not None:
-        ld_r = _matrix(residual, "residual", x)
+        pr, ld_r = residual.data_ptr(), _ld(residual, "residual", shape, dtype, dev)
     if h is None and (residual is not None or p > 0):
-        h = torch.empty((rows, cols), dtype=x.dtype, device=dev)
+        h = torch.empty(shape, dtype=dtype, device=x.device)
     if h is not None:
-        ld_h = _matrix(h, "h", x)
+        ph, ld_h = h.data_ptr(), _ld(h, "h", shape, dtype, dev)
     if y is None and want_y:
-        y = torch.empty((rows, cols), dtype=x.dtype, device=dev)
+        y = torch.empty(shape, dtype=dtype, device=x.device)
     if y is not None:
-        ld_y = _matrix(y, "y", x)
+        py, ld_y = y.data_ptr(), _ld(y, "y", shape, dtype, dev)
     if save and mean is None and kind == NORM_LAYER:
-        mean = torch.empty((rows,), dtype=torch.float32, device=dev)
+        mean = torch.empty((rows,), dtype=torch.float32, device=x.device)
     if save and rstd is None:
-        rstd = torch.empty((rows,), dtype=torch.float32, device=dev)
+        rstd = torch.empty((rows,), dtype=torch.float32, device=x.device)
+    if mean is not None:
+        pm = _vector(mean, "mean", rows, torch.float32, dev)
+    if rstd is not None:
+        ps = _vector(rstd, "rstd", rows, torch.float32, dev)
     if mx or codes is not None or scales is not None:
-        codes, scales = _mx_outputs(rows, cols, layout, codes, scales, dev)
-    g, b, wt = _weights(gamma, beta, cols, dev)
-    _check("fp4_norm",
-           lib().fp4_norm(x.data_ptr(), rows, cols, ld_x, _TYPES[x.dtype], _ptr(residual), ld_r, p, seed, stream_id,
-                          _ptr(h), ld_h, kind, g, b, wt, eps, _ptr(y), ld_y,
-                          _vector(mean, "mean", rows, dev, torch.float32),
-                          _vector(rstd, "rstd", rows, dev, torch.float32), _ptr(codes), _ptr(scales), layout,
-                          _stream(stream)))
-    return Norm(y, h, mean, rstd, codes, scales)
+        codes, scales = _mx_outputs(rows, cols, layout, codes, scales, x.device)
+        pc, pe = codes.data_ptr(), scales.data_ptr()
+    if gamma is not None:
+        pg, wt = _weight(gamma, "gamma", cols, dev)
+    if beta is not None:
+        pb, bt = _weight(beta, "beta", cols, dev)
+        if gamma is not None and bt != wt:
+            raise ValueError("gamma and beta must have the same type")
+        wt = bt
+    status = lib().fp4_norm(x.data_ptr(), rows, cols, ld_x, kt, pr, ld_r, p, seed, stream_id, ph, ld_h, kind, pg, pb,
+                            wt, eps, py, ld_y, pm, ps, pc, pe, layout, _row_stream(stream, dev))
+    if status:
+        raise Fp4qError("fp4_norm", status)
+    return _new(Norm, (y, h, mean, rstd, codes, scales))
 
 
 class NormGrad(NamedTuple):
@@ -567,37 +602,48 @@ def fp4_norm_grad(dy: torch.Tensor, h: torch.Tensor, gamma: Optional[torch.Tenso
     reaches them along the residual stream), dx of fp4_norm's x where p > 0
     (dx equals dh otherwise and is None), and with `weights` dgamma and, for
     NORM_LAYER, dbeta in fp32. dh and dx may each be dy, h or dres."""
-    ld_dy = _matrix(dy, "dy")
-    rows, cols = dy.shape
-    dev = dy.device
-    ld_h = _matrix(h, "h", dy)
-    ld_dres = 0 if dres is None else _matrix(dres, "dres", dy)
+    shape, ld_dy, dtype, kt, dev = _first(dy, "dy")
+    rows, cols = shape
+    pr = px = pm = pg = pw = pdg = pdb = None
+    ld_r = ld_x = wt = wbytes = 0
+    ld_h = _ld(h, "h", shape, dtype, dev)
+    if dres is not None:
+        pr, ld_r = dres.data_ptr(), _ld(dres, "dres", shape, dtype, dev)
     if dh is None:
-        dh = torch.empty((rows, cols), dtype=dy.dtype, device=dev)
-    ld_dh, ld_dx = _matrix(dh, "dh", dy), 0
+        dh = torch.empty(shape, dtype=dtype, device=dy.device)
+    ld_dh = _ld(dh, "dh", shape, dtype, dev)
     if dx is None and p > 0:
-        dx = torch.empty((rows, cols), dtype=dy.dtype, device=dev)
+        dx = torch.empty(shape, dtype=dtype, device=dy.device)
     if dx is not None:
-        ld_dx = _matrix(dx, "dx", dy)
+        px, ld_x = dx.data_ptr(), _ld(dx, "dx", shape, dtype, dev)
     if weights and dgamma is None:
-        dgamma = torch.empty((cols,), dtype=torch.float32, device=dev)
+        dgamma = torch.empty((cols,), dtype=torch.float32, device=dy.device)
     if weights and dbeta is None and kind == NORM_LAYER:
-        dbeta = torch.empty((cols,), dtype=torch.float32, device=dev)
-    need = lib().fp4q_norm_grad_workspace_bytes(rows, cols) if dgamma is not None or dbeta is not None else 0
-    if workspace is None and need > 0:
-        workspace = torch.empty((need,), dtype=torch.uint8, device=dev)
-    if workspace is not None and (workspace.device != dev or not workspace.is_contiguous()):
-        raise ValueError("workspace must be a contiguous tensor on dy's device")
-    wbytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
-    g, _, wt = _weights(gamma, None, cols, dev)
-    _check("fp4_norm_grad",
-           lib().fp4_norm_grad(dy.data_ptr(), rows, cols, ld_dy, _TYPES[dy.dtype], h.data_ptr(), ld_h, _ptr(dres),
-                               ld_dres, kind, g, wt, _vector(mean, "mean", rows, dev, torch.float32),
-                               _vector(rstd, "rstd", rows, dev, torch.float32), p, seed, stream_id, dh.data_ptr(),
-                               ld_dh, _ptr(dx), ld_dx, _vector(dgamma, "dgamma", cols, dev, torch.float32),
-                               _vector(dbeta, "dbeta", cols, dev, torch.float32), _ptr(workspace), wbytes,
-                               _stream(stream)))
-    return NormGrad(dh, dx, dgamma, dbeta)
+        dbeta = torch.empty((cols,), dtype=torch.float32, device=dy.device)
+    if dgamma is not None:
+        pdg = _vector(dgamma, "dgamma", cols, torch.float32, dev)
+    if dbeta is not None:
+        pdb = _vector(dbeta, "dbeta", cols, torch.float32, dev)
+    if workspace is None and (pdg or pdb):
+        wbytes = lib().fp4q_norm_grad_workspace_bytes(rows, cols)
+        if wbytes:
+            workspace = torch.empty((wbytes,), dtype=torch.uint8, device=dy.device)
+            pw = workspace.data_ptr()
+    elif workspace is not None:
+        if workspace.get_device() != dev or not workspace.is_contiguous():
+            raise ValueError("workspace must be a contiguous tensor on dy's device")
+        pw, wbytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
+    if gamma is not None:
+        pg, wt = _weight(gamma, "gamma", cols, dev)
+    if mean is not None:
+        pm = _vector(mean, "mean", rows, torch.float32, dev)
+    ps = _vector(rstd, "rstd", rows, torch.float32, dev)
+    status = lib().fp4_norm_grad(dy.data_ptr(), rows, cols, ld_dy, kt, h.data_ptr(), ld_h, pr, ld_r, kind, pg, wt, pm,
+                                 ps, p, seed, stream_id, dh.data_ptr(), ld_dh, px, ld_x, pdg, pdb, pw, wbytes,
+                                 _row_stream(stream, dev))
+    if status:
+        raise Fp4qError("fp4_norm_grad", status)
+    return _new(NormGrad, (dh, dx, dgamma, dbeta))
 
 
 def fp4_swiglu_grad_bf16(dh: torch.Tensor, c: torch.Tensor, *, pair: int = 32, want_h: bool = False,
@@ -606,33 +652,37 @@ def fp4_swiglu_grad_bf16(dh: torch.Tensor, c: torch.Tensor, *, pair: int = 32, w
     """The gradient of fp4_swiglu_bf16: (dc, h) from dh [M x F] and the bf16
     C [M x >= 2F] whose columns interleave gate and up in groups of `pair`;
     h (with `want_h`) is the forward's output again. dc may be c, h may be dh."""
-    if dh.dtype != torch.bfloat16 or c.dtype != torch.bfloat16:
-        raise ValueError("dh and c must be bf16")
-    M, f = dh.shape
-    ld_dh, ldc, ldh = _matrix(dh, "dh"), _matrix(c, "c"), 0
-    if c.shape[0] != M or c.shape[1] < 2 * f or c.device != dh.device:
-        raise ValueError(f"c must be a bf16 [{M} x >= {2 * f}] tensor on {dh.device}")
+    shape, ld_dh, _, kind, dev = _first(dh, "dh")
+    M, f = shape
+    cs, ldc, _, ck, cd = _first(c, "c")
+    if kind != OUT_BF16 or ck != OUT_BF16 or cd != dev or cs[0] != M or cs[1] < 2 * f:
+        raise ValueError(f"dh must be bf16 and c a bf16 [{M} x >= {2 * f}] tensor on its device")
     if dc is None:
         dc = torch.empty((M, 2 * f), dtype=torch.bfloat16, device=c.device)
-    if dc.shape[0] != M or dc.shape[1] < 2 * f or dc.dtype != torch.bfloat16 or dc.device != dh.device:
-        raise ValueError(f"dc must be a bf16 [{M} x >= {2 * f}] tensor on {dh.device}")
+    os, ld_dc, _, ok, od = _first(dc, "dc")
+    if ok != OUT_BF16 or od != dev or os[0] != M or os[1] < 2 * f:
+        raise ValueError(f"dc must be a bf16 [{M} x >= {2 * f}] tensor on dh's device")
+    ph, ldh = None, 0
     if h is None and want_h:
         h = torch.empty((M, f), dtype=torch.bfloat16, device=c.device)
     if h is not None:
-        ldh = _matrix(h, "h", dh)
-    _check("fp4_swiglu_grad_bf16",
-           lib().fp4_swiglu_grad_bf16(dh.data_ptr(), ld_dh, c.data_ptr(), M, f, ldc, pair, dc.data_ptr(),
-                                      _matrix(dc, "dc"), _ptr(h), ldh, _stream(stream)))
+        ph, ldh = h.data_ptr(), _ld(h, "h", shape, torch.bfloat16, dev)
+    status = lib().fp4_swiglu_grad_bf16(dh.data_ptr(), ld_dh, c.data_ptr(), M, f, ldc, pair, dc.data_ptr(), ld_dc, ph,
+                                        ldh, _row_stream(stream, dev))
+    if status:
+        raise Fp4qError("fp4_swiglu_grad_bf16", status)
     return dc, h
 
 
-def _heads(t: torch.Tensor, name: str) -> Tuple[int, int]:
+def _heads(t: torch.Tensor, name: str, shape: torch.Size) -> Tuple[int, int]:
     """(token stride, head stride) of a [tokens, heads, dim] view."""
-    if t.dim() != 3 or t.dtype not in _TYPES or (t.stride(2) != 1 and t.shape[2] > 1):
-        raise ValueError(f"{name} must be a [tokens, heads, dim] fp32 or bf16 tensor with unit stride along dim")
-    n, heads, dim = t.shape
-    head = t.stride(1) if heads > 1 else dim
-    return (t.stride(0) if n > 1 else max(1, heads) * head), head
+    n, heads, dim = shape
+    token, head, one = t.stride()
+    if one != 1 and dim > 1:
+        raise ValueError(f"{name} must have unit stride along dim")
+    if heads <= 1:
+        head = dim
+    return (token if n > 1 else max(1, heads) * head), head
 
 
 def fp4_rotary(x: torch.Tensor, positions: torch.Tensor, inv_freq: torch.Tensor, *, style: int = ROTARY_HALF,
@@ -642,21 +692,23 @@ def fp4_rotary(x: torch.Tensor, positions: torch.Tensor, inv_freq: torch.Tensor,
     strides, so a slice of a fused QKV output serves): pair i of each head
     turns by positions[t] * inv_freq[i], the first 2 len(inv_freq) elements
     of the head taking part. `inverse` turns back: the gradient. y may be x."""
-    xt, xh = _heads(x, "x")
-    n, heads, dim = x.shape
+    shape, kind, dev = x.shape, _TYPES.get(x.dtype), x.get_device()
+    if kind is None or len(shape) != 3:
+        raise ValueError("x must be a [tokens, heads, dim] fp32 or bf16 tensor")
+    xt, xh = _heads(x, "x", shape)
     if y is None:
-        y = torch.empty((n, heads, dim), dtype=x.dtype, device=x.device)
-    if y.shape != x.shape or y.dtype != x.dtype or y.device != x.device:
-        raise ValueError(f"y must be a {tuple(x.shape)} {x.dtype} tensor on {x.device}")
-    yt, yh = _heads(y, "y")
-    if positions.dtype not in (torch.int32, torch.int64):
-        raise ValueError("positions must be int32 or int64")
-    pos = _vector(positions, "positions", n, x.device, positions.dtype)
-    freq = _vector(inv_freq, "inv_freq", inv_freq.shape[0], x.device, torch.float32)
-    _check("fp4_rotary",
-           lib().fp4_rotary(x.data_ptr(), n, heads, dim, xt, xh, _TYPES[x.dtype], pos,
-                            64 if positions.dtype == torch.int64 else 32, freq, 2 * inv_freq.shape[0], style,
-                            int(bool(inverse)), scale, y.data_ptr(), yt, yh, _stream(stream)))
+        y = torch.empty(shape, dtype=x.dtype, device=x.device)
+    elif y.shape != shape or y.dtype is not x.dtype or y.get_device() != dev:
+        raise ValueError(f"y must be a {tuple(shape)} {x.dtype} tensor on x's device")
+    yt, yh = _heads(y, "y", shape)
+    bits = 64 if positions.dtype is torch.int64 else 32
+    pos = _vector(positions, "positions", shape[0], torch.int64 if bits == 64 else torch.int32, dev)
+    pairs = inv_freq.numel()
+    status = lib().fp4_rotary(x.data_ptr(), shape[0], shape[1], shape[2], xt, xh, kind, pos, bits,
+                              _vector(inv_freq, "inv_freq", pairs, torch.float32, dev), 2 * pairs, style,
+                              1 if inverse else 0, scale, y.data_ptr(), yt, yh, _row_stream(stream, dev))
+    if status:
+        raise Fp4qError("fp4_rotary", status)
     return y
 
 

@@ -87,7 +87,7 @@ struct NormGradArgs {
     uint32_t stream_id;
     void *dh, *dx;  // one of them optional
     float *parts;   // workspace: the workgroups' weight sums
-    bool layer_beta;  // dbeta is asked for
+    uint32_t waves, groups, row_blocks;  // set by the launcher: waves of a row, rows of a workgroup, workgroups
 };
 
 struct SwigluGradArgs {

@@ -27,39 +27,69 @@ namespace fp4q {
 
 namespace {
 
-// The weights are read once per row from cache, in their own type.
-template <bool kTail>
-__device__ __forceinline__ void load_weight(const void *w, bool bf16, uint32_t c, uint32_t cols, float v[8])
+// Eight weights as stored, in either type: the loads are the same whatever
+// the type (bf16 reads its 16 bytes twice), so that nothing waits for them
+// under a branch; get() is where they have to be there.
+struct Weights {
+    u32x4v a, b;
+    __device__ __forceinline__ void get(bool bf16, float v[8]) const
+    {
+        Chunk<bf16_t> h;
+        Chunk<float> f;
+        h.q = a;
+        f.a = a;
+        f.b = b;
+        if (bf16)
+            h.get(v);
+        else
+            f.get(v);
+    }
+};
+template <Edge kEdge>
+__device__ __forceinline__ void load_weights(const void *w, bool bf16, const Span &s, uint32_t cols, Weights &q)
+{
+    if (kEdge != kTiny) {
+        const char *p = reinterpret_cast<const char *>(w) + (s.from << (bf16 ? 1 : 2));
+        q.a = *reinterpret_cast<const u32x4_a2 *>(p);
+        q.b = *reinterpret_cast<const u32x4_a2 *>(p + (bf16 ? 0 : 16));
+    } else if (bf16) {
+        Chunk<bf16_t> h;
+        load_chunk<bf16_t, kEdge>(reinterpret_cast<const bf16_t *>(w), s, cols, h);
+        q.a = q.b = h.q;
+    } else {
+        Chunk<float> f;
+        load_chunk<float, kEdge>(reinterpret_cast<const float *>(w), s, cols, f);
+        q.a = f.a;
+        q.b = f.b;
+    }
+}
+
+// ... and loaded where they are used, which takes fewer registers.
+template <Edge kEdge>
+__device__ __forceinline__ void weights_now(const void *w, bool bf16, const Span &s, uint32_t cols, float v[8])
 {
     if (bf16) {
         Chunk<bf16_t> q;
-        load_chunk<bf16_t, kTail>(reinterpret_cast<const bf16_t *>(w), c, cols, q);
+        load_chunk<bf16_t, kEdge>(reinterpret_cast<const bf16_t *>(w), s, cols, q);
         q.get(v);
     } else {
         Chunk<float> q;
-        load_chunk<float, kTail>(reinterpret_cast<const float *>(w), c, cols, q);
+        load_chunk<float, kEdge>(reinterpret_cast<const float *>(w), s, cols, q);
         q.get(v);
     }
 }
 
-// Sum over the kTpr threads of a row: a wave by itself, or the waves of the
-// row's group through LDS (`slot`: one float per wave of the workgroup, of
-// its own for each sum of a row).  kTpr > 64: every thread of the workgroup
-// must call it.
-template <int kTpr>
-__device__ __forceinline__ float row_sum(float v, float *slot)
+// Sum over the `waves` waves (at most 16) of a row that starts at wave
+// `first` of the workgroup, through LDS (`slot`: one float per wave, of its
+// own for each sum of a row).  Every thread of the workgroup must call it.
+__device__ __forceinline__ float row_sum(float v, float *slot, uint32_t wave, uint32_t first, uint32_t waves)
 {
     v = wave_sum(v);
-    if (kTpr <= 64) return v;
-    constexpr int kWaves = kTpr / 64 > 0 ? kTpr / 64 : 1;
-    const int wave = threadIdx.x >> 6;
-    if ((threadIdx.x & 63) == 0) slot[wave] = v;
+    const uint32_t lane = threadIdx.x & 63u;
+    if (lane == 0) slot[wave] = v;
     __syncthreads();
-    const int first = wave / kWaves * kWaves;
-    v = slot[first];
-#pragma unroll
-    for (int i = 1; i < kWaves; ++i) v += slot[first + i];
-    return v;
+    v = lane < waves ? slot[first + lane] : 0.0f;
+    return lane_value(sum16(v), 15);
 }
 
 template <int kMask>
@@ -100,285 +130,475 @@ __device__ __forceinline__ void store_mx(const NormArgs &a, int64_t row, uint32_
     }
 }
 
-// kTpr threads per row, kC chunks of eight elements per thread.
-template <typename T, int kTpr, int kC, bool kRes, bool kTail, bool kMx>
-__global__ __launch_bounds__(kTpr < 256 ? 256 : kTpr) void norm_kernel(const NormArgs a, const Dropout d,
-                                                                            const void *__restrict__ gamma,
-                                                                            const void *__restrict__ beta)
+// kC chunks of eight elements per thread.  kWave: a wave has a row to itself
+// (four rows to a workgroup, no barriers); otherwise a workgroup of as many
+// waves as the row needs has it.
+template <typename T, bool kWave, int kC, bool kRes, Edge kEdge, bool kMx>
+__global__ __launch_bounds__(kWave ? 256 : 1024) void norm_kernel(const NormArgs a, const Dropout d,
+                                                                  const void *__restrict__ gamma,
+                                                                  const void *__restrict__ beta)
 {
-    constexpr int kRows = kTpr < 256 ? 256 / kTpr : 1;  // rows of a workgroup at a time
-    static_assert(kTpr == 64 || kRows == 1, "a workgroup's waves share a row's barriers or need none");
-    __shared__ float red[2][2][kTpr / 64 * kRows];  // a row's slots stay apart from the next row's
-    const uint32_t t = threadIdx.x % kTpr, cols = (uint32_t)a.cols;
+    __shared__ float red[2][16];
+    constexpr bool kEarlyW = kC == 1;
+    const uint32_t tpr = kWave ? 64u : blockDim.x, t = kWave ? threadIdx.x & 63u : threadIdx.x;
+    const uint32_t cols = (uint32_t)a.cols, waves = blockDim.x >> 6;
+    const uint32_t wave = (uint32_t)__builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));  // rows in scalar registers
+    const auto sum_of = [&](float v, float *slot) { return kWave ? wave_sum(v) : row_sum(v, slot, wave, 0, waves); };
     const float inv_n = 1.0f / (float)cols;
-    int parity = 0;
-    // tiled output: the padding rows up to rows_out get zero codes and scales
-    for (int64_t row = (int64_t)blockIdx.x * kRows + threadIdx.x / kTpr; row < a.rows_out;
-         row += (int64_t)gridDim.x * kRows, parity ^= 1) {
-        if (kMx && row >= a.rows) {
-            Chunk<bf16_t> z;
-            z.q = (u32x4v){0u, 0u, 0u, 0u};
+    // whether each lane of the wave has a full chunk of its own in place i
+    const auto whole = [&](int i) { return (i * tpr + (kWave ? 64u : wave * 64u + 64u)) * 8u <= cols; };
+    // no loop over rows: what a loop would keep ready for its next turn
+    // (Philox's keys among it) spills
+    const int64_t block = (int64_t)blockIdx.y * gridDim.x + blockIdx.x, row = kWave ? block * 4 + wave : block;
+    if (row >= a.rows_out) return;
+    if (kMx && row >= a.rows) {  // tiled output's padding rows: zero codes and scales
+        Chunk<bf16_t> z;
+        z.q = (u32x4v){0u, 0u, 0u, 0u};
 #pragma unroll
-            for (int i = 0; i < kC; ++i) store_mx(a, row, i * kTpr + t, cols, z);
-            continue;
+        for (int i = 0; i < kC; ++i) store_mx(a, row, i * tpr + t, cols, z);
+        return;
+    }
+    Span sp[kC];
+    Chunk<T> q[kC], s[kRes ? kC : 1];
+    const T *px = reinterpret_cast<const T *>(a.x) + row * a.ld_x;
+    const T *res = reinterpret_cast<const T *>(a.residual) + row * a.ld_r;
+#pragma unroll
+    for (int i = 0; i < kC; ++i) {
+        sp[i] = span_of<kEdge>(i * tpr + t, cols);
+        load_chunk<T, kEdge, kStream<T>>(px, sp[i], cols, q[i]);
+        if (kRes) load_chunk<T, kEdge, kStream<T>>(res, sp[i], cols, s[i]);
+    }
+    // behind the row, so that they have come when its sums are done
+    Weights wg, wb;
+    if (kEarlyW) {
+        if (gamma) load_weights<kEdge>(gamma, a.w_bf16, sp[0], cols, wg);
+        if (beta) load_weights<kEdge>(beta, a.w_bf16, sp[0], cols, wb);
+    }
+    if (kRes || d.drop || a.h) {
+        // the random words are made while the row is on its way
+        __builtin_amdgcn_sched_barrier(0);
+        Draws x[kC];
+        if (d.drop) {
+#pragma unroll
+            for (int i = 0; i < kC; ++i) x[i] = draws_of<kEdge>(d, (uint32_t)row, i * tpr + t, sp[i]);
         }
-        Chunk<T> q[kC];
-        const T *x = reinterpret_cast<const T *>(a.x) + row * a.ld_x;
+        __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-        for (int i = 0; i < kC; ++i) load_chunk<T, kTail>(x, i * kTpr + t, cols, q[i]);
-        if (kRes || d.drop || a.h) {
-            Chunk<T> s[kRes ? kC : 1];
+        for (int i = 0; i < kC; ++i) {
+            float v[8];
+            q[i].get(v);
+            if (d.drop) apply_dropout(d, x[i], v);
             if (kRes) {
-                const T *res = reinterpret_cast<const T *>(a.residual) + row * a.ld_r;
+                float r[8];
+                s[i].get(r);
 #pragma unroll
-                for (int i = 0; i < kC; ++i) load_chunk<T, kTail>(res, i * kTpr + t, cols, s[i]);
+                for (int j = 0; j < 8; ++j) v[j] = r[j] + v[j];
             }
-#pragma unroll
-            for (int i = 0; i < kC; ++i) {
-                const uint32_t c = i * kTpr + t;
-                float v[8];
-                q[i].get(v);
-                if (d.drop) apply_dropout(d, (uint32_t)row, c, v);
-                if (kRes) {
-                    float r[8];
-                    s[i].get(r);
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) v[j] = r[j] + v[j];
-                }
-                q[i].set(v);
-                if (a.h) store_chunk<T, kTail>(reinterpret_cast<T *>(a.h) + row * a.ld_h, c, cols, q[i]);
-            }
+            q[i].set(v);
+            if (a.h) store_chunk<T, kEdge, kStream<T>>(reinterpret_cast<T *>(a.h) + row * a.ld_h, sp[i], q[i]);
         }
-        float mean = 0.0f;
-        if (a.layer) {
-            float sum = 0.0f;
-#pragma unroll
-            for (int i = 0; i < kC; ++i) {
-                float v[8];
-                q[i].get(v);
-                sum += ((v[0] + v[1]) + (v[2] + v[3])) + ((v[4] + v[5]) + (v[6] + v[7]));
-            }
-            mean = row_sum<kTpr>(sum, red[parity][0]) * inv_n;
-        }
-        float sq = 0.0f;
+    }
+    float mean = 0.0f;
+    if (a.layer) {
+        float sum = 0.0f;
 #pragma unroll
         for (int i = 0; i < kC; ++i) {
-            const uint32_t at = (i * kTpr + t) * 8u;
             float v[8];
             q[i].get(v);
+            if (kEdge != kWhole && !whole(i)) {
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                const bool in = kTail ? at + j < cols : at < cols;
-                const float e = in ? v[j] - mean : 0.0f;
-                sq = __builtin_fmaf(e, e, sq);
+                for (int j = 0; j < 8; ++j) v[j] = sp[i].own(j) ? v[j] : 0.0f;
             }
+            const float e = ((v[0] + v[1]) + (v[2] + v[3])) + ((v[4] + v[5]) + (v[6] + v[7]));
+            sum += kEdge != kWhole || sp[i].any() ? e : 0.0f;
         }
-        const float rstd = 1.0f / __builtin_sqrtf(row_sum<kTpr>(sq, red[parity][1]) * inv_n + a.eps);
-        if (t == 0) {
-            if (a.layer && a.mean) a.mean[row] = mean;
-            if (a.rstd) a.rstd[row] = rstd;
+        mean = sum_of(sum, red[0]) * inv_n;
+    }
+    float sq = 0.0f;
+#pragma unroll
+    for (int i = 0; i < kC; ++i) {
+        float v[8], e = 0.0f;
+        q[i].get(v);
+        if (kEdge != kWhole && !whole(i)) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) v[j] = sp[i].own(j) ? v[j] : mean;
         }
 #pragma unroll
-        for (int i = 0; i < kC; ++i) {
-            const uint32_t c = i * kTpr + t;
-            float v[8];
-            q[i].get(v);
-            float w[8], b[8];
-#pragma unroll
-            for (int j = 0; j < 8; ++j) w[j] = 1.0f, b[j] = 0.0f;
-            if (gamma) load_weight<kTail>(gamma, a.w_bf16, c, cols, w);
-            if (beta) load_weight<kTail>(beta, a.w_bf16, c, cols, b);
-#pragma unroll
-            for (int j = 0; j < 8; ++j) v[j] = __builtin_fmaf((v[j] - mean) * rstd, w[j], b[j]);
-            Chunk<T> out;
-            out.set(v);
-            if (a.y) store_chunk<T, kTail>(reinterpret_cast<T *>(a.y) + row * a.ld_y, c, cols, out);
-            if constexpr (kMx) {
-                out.mask(c * 8u < cols);
-                store_mx(a, row, c, cols, out);
-            }
+        for (int j = 0; j < 8; ++j) {
+            const float c = v[j] - mean;
+            e = __builtin_fmaf(c, c, e);
         }
+        sq += kEdge != kWhole || sp[i].any() ? e : 0.0f;
+    }
+    const float rstd = 1.0f / __builtin_sqrtf(sum_of(sq, red[1]) * inv_n + a.eps);
+    if (t == 0) {
+        if (a.layer && a.mean) a.mean[row] = mean;
+        if (a.rstd) a.rstd[row] = rstd;
+    }
+#pragma unroll
+    for (int i = 0; i < kC; ++i) {
+        float v[8], w[8], b[8];
+        q[i].get(v);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) w[j] = 1.0f, b[j] = 0.0f;
+        if (kEarlyW) {
+            if (gamma) wg.get(a.w_bf16, w);
+            if (beta) wb.get(a.w_bf16, b);
+        } else {
+            if (gamma) weights_now<kEdge>(gamma, a.w_bf16, sp[i], cols, w);
+            if (beta) weights_now<kEdge>(beta, a.w_bf16, sp[i], cols, b);
+        }
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[j] = __builtin_fmaf((v[j] - mean) * rstd, w[j], b[j]);
+        q[i].set(v);
+        if (a.y) store_chunk<T, kEdge, kStream<T>>(reinterpret_cast<T *>(a.y) + row * a.ld_y, sp[i], q[i]);
+        if constexpr (kMx) store_mx(a, row, i * tpr + t, cols, q[i]);
     }
 }
 
-template <typename T, int kTpr, int kC, bool kMx>
+template <typename T, bool kWave, int kC, bool kMx>
 void run_norm(const NormArgs &a, const Dropout &d, hipStream_t st)
 {
-    constexpr int kThreads = kTpr < 256 ? 256 : kTpr, kRows = kThreads / kTpr;
-    const int64_t need = (a.rows_out + kRows - 1) / kRows;
-    const dim3 grid((unsigned)(need < (1 << 20) ? need : (1 << 20))), block(kThreads);
-    const bool tail = a.cols % 8 != 0;
-    if constexpr (kMx) {  // cols % 32 == 0
-        if (a.residual)
-            hipLaunchKernelGGL((norm_kernel<T, kTpr, kC, true, false, true>), grid, block, 0, st, a, d, a.gamma, a.beta);
-        else
-            hipLaunchKernelGGL((norm_kernel<T, kTpr, kC, false, false, true>), grid, block, 0, st, a, d, a.gamma, a.beta);
-    } else {
-        if (a.residual) {
-            if (tail)
-                hipLaunchKernelGGL((norm_kernel<T, kTpr, kC, true, true, false>), grid, block, 0, st, a, d, a.gamma, a.beta);
-            else
-                hipLaunchKernelGGL((norm_kernel<T, kTpr, kC, true, false, false>), grid, block, 0, st, a, d, a.gamma, a.beta);
-        } else {
-            if (tail)
-                hipLaunchKernelGGL((norm_kernel<T, kTpr, kC, false, true, false>), grid, block, 0, st, a, d, a.gamma, a.beta);
-            else
-                hipLaunchKernelGGL((norm_kernel<T, kTpr, kC, false, false, false>), grid, block, 0, st, a, d, a.gamma, a.beta);
-        }
+    const int64_t chunks = (a.cols + 7) / 8, need = kWave ? (a.rows_out + 3) / 4 : a.rows_out;
+    const int64_t wide = 1 << 20;  // a launch's threads along x are below 2^32
+    const dim3 grid((unsigned)(need < wide ? need : wide), (unsigned)((need + wide - 1) / wide));
+    const dim3 block(kWave ? 256 : (unsigned)((chunks + 64 * kC - 1) / (64 * kC) * 64));
+#define FP4Q_NORM(EDGE)                                                                                           \
+    do {                                                                                                          \
+        if (a.residual)                                                                                           \
+            hipLaunchKernelGGL((norm_kernel<T, kWave, kC, true, EDGE, kMx>), grid, block, 0, st, a, d, a.gamma, a.beta);  \
+        else                                                                                                      \
+            hipLaunchKernelGGL((norm_kernel<T, kWave, kC, false, EDGE, kMx>), grid, block, 0, st, a, d, a.gamma, a.beta); \
+    } while (0)
+    const Edge edge = edge_of(a.cols);  // an operand's is kWhole, and only short rows are tiny
+    if constexpr (kWave && kC == 1 && !kMx) {
+        if (edge == kTiny) FP4Q_NORM(kTiny);
     }
+    if constexpr (!kMx) {
+        if (edge == kRagged) FP4Q_NORM(kRagged);
+    }
+    if (edge == kWhole) FP4Q_NORM(kWhole);
+#undef FP4Q_NORM
 }
 
 template <typename T, bool kMx>
 void pick_norm(const NormArgs &a, const Dropout &d, hipStream_t st)
 {
-    const int64_t chunks = (a.cols + 7) / 8;
-    if (chunks <= 64)
-        run_norm<T, 64, 1, kMx>(a, d, st);
-    else if (chunks <= 128)
-        run_norm<T, 64, 2, kMx>(a, d, st);
-    else if (chunks <= 256)
-        run_norm<T, 256, 1, kMx>(a, d, st);
-    else if (chunks <= 512)
-        run_norm<T, 256, 2, kMx>(a, d, st);
-    else if (chunks <= 1024)
-        run_norm<T, 256, 4, kMx>(a, d, st);
-    else if (chunks <= 2048)
-        run_norm<T, 512, 4, kMx>(a, d, st);
+    if (a.cols <= 512)
+        run_norm<T, true, 1, kMx>(a, d, st);
+    else if (a.cols <= 1024)
+        run_norm<T, true, 2, kMx>(a, d, st);
+    else if (a.cols <= 4096)
+        run_norm<T, false, 1, kMx>(a, d, st);
+    else if (a.cols <= 16384)
+        run_norm<T, false, 2, kMx>(a, d, st);
     else
-        run_norm<T, 1024, 4, kMx>(a, d, st);
+        run_norm<T, false, 4, kMx>(a, d, st);
 }
 
 // ------------------------------------------------------------------ gradient
 
-constexpr int kGradThreads = 1024;
 constexpr int kMaxParts = 256;  // workgroups that keep weight sums: one per compute unit
-
-// A workgroup of 1024 threads takes 1024 / kTpr rows at a time; its weight
-// sums are folded over those row groups in LDS at the end.
-template <typename T, int kTpr, int kC, bool kRes, bool kDx, bool kTail>
-__global__ __launch_bounds__(kGradThreads) void norm_grad_kernel(const NormGradArgs a, const Dropout d)
+// The weight sums of 64 columns over every `nslices`-th run of 128 rows, by
+// a workgroup of 1024 threads: eight lanes side by side take the columns,
+// the other 128 the rows.  They need the rows' statistics but not their
+// sums, so this part can run beside the rows' own work.
+template <typename T, Edge kEdge>
+__device__ __forceinline__ void weight_sums(const NormGradArgs &a, uint32_t block, uint32_t slice, uint32_t nslices,
+                                            float *dgamma, float *dbeta)
 {
-    constexpr int kGroups = kGradThreads / kTpr;
-    __shared__ float red[2][2][kGradThreads / 64];
-    __shared__ float fold[kGroups > 1 ? kC * 8 * kGradThreads : 1];
-    const uint32_t t = threadIdx.x % kTpr, g = threadIdx.x / kTpr, cols = (uint32_t)a.cols;
+    __shared__ float s[2][16][64];
+    const uint32_t lane = threadIdx.x & 63u, wave = threadIdx.x >> 6, cols = (uint32_t)a.cols;
+    const Span sp = span_of<kEdge>(block * 8u + (lane & 7u), cols);
+    float sum_w[8], sum_b[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) sum_w[j] = 0.0f, sum_b[j] = 0.0f;
+#pragma unroll 2
+    for (int64_t row = (int64_t)slice * 128 + (threadIdx.x >> 3); row < a.rows; row += (int64_t)nslices * 128) {
+        Chunk<T> dy, h;
+        load_chunk<T, kEdge, kStream<T>>(reinterpret_cast<const T *>(a.dy) + row * a.ld_dy, sp, cols, dy);
+        load_chunk<T, kEdge, kStream<T>>(reinterpret_cast<const T *>(a.h) + row * a.ld_h, sp, cols, h);
+        const float mean = a.layer ? a.mean[row] : 0.0f, rstd = a.rstd[row];
+        float e[8], v[8];
+        dy.get(e);
+        h.get(v);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            sum_w[j] = __builtin_fmaf(e[j], (v[j] - mean) * rstd, sum_w[j]);
+            sum_b[j] += e[j];
+        }
+    }
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+#pragma unroll
+        for (int m = 8; m < 64; m <<= 1) {
+            sum_w[j] += __shfl_xor(sum_w[j], m);
+            sum_b[j] += __shfl_xor(sum_b[j], m);
+        }
+    }
+    if (lane < 8) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            s[0][wave][lane * 8 + j] = sum_w[j];
+            s[1][wave][lane * 8 + j] = sum_b[j];
+        }
+    }
+    __syncthreads();
+    if (threadIdx.x < 128) {
+        const uint32_t which = threadIdx.x >> 6;
+        float v = s[which][0][lane];
+#pragma unroll
+        for (int i = 1; i < 16; ++i) v += s[which][i][lane];
+        // the last chunk's own columns start at its lo
+        const Span o = span_of<kEdge>(block * 8u + (lane >> 3), cols);
+        float *out = which ? dbeta : dgamma;
+        if (out && o.own(lane & 7u)) out[o.from + (lane & 7u)] = v;
+    }
+}
+
+// A workgroup takes a.groups rows at a time, a.waves waves each, and loads
+// the next ones before it works on those it has (kAhead).  Weight sums:
+// kInRegs and kInLds, each workgroup keeps those of its rows and leaves them
+// in the workspace; kNone, where they are asked for, the workgroups from
+// a.row_blocks on take them from all rows (weight_sums), 64 columns each.
+enum Sums { kNone, kInRegs, kInLds };
+template <typename T, int kC, bool kAhead, Sums kSums, bool kRes, bool kDx, Edge kEdge>
+__global__ __launch_bounds__(1024) void norm_grad_kernel(const NormGradArgs a, const Dropout d, float *dgamma,
+                                                         float *dbeta)
+{
+    const uint32_t block = blockIdx.y * gridDim.x + blockIdx.x;
+    if constexpr (kSums == kNone) {
+        if (block >= a.row_blocks) {
+            if (dgamma || dbeta) weight_sums<T, kEdge>(a, block - a.row_blocks, 0, 1, dgamma, dbeta);
+            return;
+        }
+    }
+    __shared__ float red[2][2][16];
+    // the sums in LDS, or folded there over the groups at the end; a
+    // thread's eight of a chunk are two groups of four, each wave-contiguous
+    __shared__ __attribute__((aligned(16))) float keep[kSums == kNone ? 1 : (kSums == kInLds ? 2 : 1) * kC * 8 * 1024];
+    const uint32_t wave = (uint32_t)__builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));  // rows in scalar registers
+    const uint32_t lane = threadIdx.x & 63u, cols = (uint32_t)a.cols;
+    const uint32_t g = (uint32_t)__builtin_amdgcn_readfirstlane((int)(wave / a.waves)), first = g * a.waves, tpr = a.waves * 64u, t = threadIdx.x - first * 64u;
     const float inv_n = 1.0f / (float)cols;
-    float w[kC][8], sum_w[kC][8], sum_b[kC][8];
+    // wide rows read the weights again for each row rather than hold them
+    constexpr bool kHoldW = kC <= 2;
+    constexpr int kRegs = kSums == kInRegs ? kC : 1;
+    float w[kHoldW ? kC : 1][8], sum_w[kRegs][8], sum_b[kRegs][8];
+    Span sp[kC];
+    const auto weight = [&](int i, float v[8]) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[j] = 1.0f;
+        if (a.gamma) weights_now<kEdge>(a.gamma, a.w_bf16, sp[i], cols, v);
+    };
+    const auto kept = [&](int which, int i, int half) {
+        return reinterpret_cast<float4 *>(keep) + ((which * kC + i) * 2 + half) * 1024 + threadIdx.x;
+    };
 #pragma unroll
     for (int i = 0; i < kC; ++i) {
+        sp[i] = span_of<kEdge>(i * tpr + t, cols);
+        if (kSums == kInRegs) {
 #pragma unroll
-        for (int j = 0; j < 8; ++j) w[i][j] = 1.0f, sum_w[i][j] = 0.0f, sum_b[i][j] = 0.0f;
-        if (a.gamma) load_weight<kTail>(a.gamma, a.w_bf16, i * kTpr + t, cols, w[i]);
+            for (int j = 0; j < 8; ++j) sum_w[kRegs > i ? i : 0][j] = 0.0f, sum_b[kRegs > i ? i : 0][j] = 0.0f;
+        }
+        if (kSums == kInLds) {
+#pragma unroll
+            for (int k = 0; k < 4; ++k) *kept(k >> 1, i, k & 1) = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        }
+        if (kHoldW) weight(i, w[i]);
     }
-    const int64_t stride = (int64_t)gridDim.x * kGroups;
-    int parity = 0;
-    for (int64_t base = (int64_t)blockIdx.x * kGroups; base < a.rows; base += stride, parity ^= 1) {
-        const bool live = base + g < a.rows;  // the same on every lane of a wave
-        const int64_t row = live ? base + g : a.rows - 1;
+    struct Row {
         Chunk<T> dy[kC], h[kC], res[kRes ? kC : 1];
+        float mean, rstd;
+    };
+    const uint32_t rows = (uint32_t)a.rows;
+    const float *means = a.layer ? a.mean : a.rstd;
+    const auto fetch = [&](uint32_t base, Row &r) {  // past the end: the last row again
+        const int64_t row = __builtin_amdgcn_readfirstlane((int)min(base + g, rows - 1u));
 #pragma unroll
         for (int i = 0; i < kC; ++i) {
-            load_chunk<T, kTail>(reinterpret_cast<const T *>(a.dy) + row * a.ld_dy, i * kTpr + t, cols, dy[i]);
-            load_chunk<T, kTail>(reinterpret_cast<const T *>(a.h) + row * a.ld_h, i * kTpr + t, cols, h[i]);
-            if (kRes)
-                load_chunk<T, kTail>(reinterpret_cast<const T *>(a.dres) + row * a.ld_dres, i * kTpr + t, cols, res[i]);
+            load_chunk<T, kEdge, kStream<T>>(reinterpret_cast<const T *>(a.dy) + row * a.ld_dy, sp[i], cols, r.dy[i]);
+            load_chunk<T, kEdge, kStream<T>>(reinterpret_cast<const T *>(a.h) + row * a.ld_h, sp[i], cols, r.h[i]);
+            if (kRes) load_chunk<T, kEdge, kStream<T>>(reinterpret_cast<const T *>(a.dres) + row * a.ld_dres, sp[i], cols, r.res[i]);
         }
-        const float mean = a.layer ? a.mean[row] : 0.0f, rstd = a.rstd[row];
+        r.mean = means[row];
+        r.rstd = a.rstd[row];
+    };
+    // rows < 2^31 and three strides (where there is a loop) < 2^16: below 2^32
+    const uint32_t stride = a.row_blocks * a.groups, base0 = block * a.groups;
+    // whether each lane of the wave has a full chunk of its own in place i
+    const auto whole = [&](int i) { return (i * tpr + (wave - first) * 64u + 64u) * 8u <= cols; };
+    int parity = 0;
+    const auto work = [&](uint32_t base, const Row &cur) {
+        const int64_t row = (uint32_t)__builtin_amdgcn_readfirstlane((int)(base + g));
+        // the same on every lane of a wave; waves past the last group (the
+        // workgroups beside this one need 1024 threads) have no row
+        const bool live = row < a.rows && g < a.groups;
+        Draws x[kC];
+        if (kDx && d.drop) {
+            // the key made anew for each row: the rounds' keys, kept over the
+            // loop, would spill
+            Dropout k = d;
+            asm volatile("" : "+s"(k.key0), "+s"(k.key1));
+#pragma unroll
+            for (int i = 0; i < kC; ++i) x[i] = draws_of<kEdge>(k, (uint32_t)row, i * tpr + t, sp[i]);
+        }
+        const float mean = a.layer ? cur.mean : 0.0f, rstd = cur.rstd;
         float s1 = 0.0f, s2 = 0.0f;
 #pragma unroll
         for (int i = 0; i < kC; ++i) {
-            float e[8], v[8];
-            dy[i].get(e);
-            h[i].get(v);
+            float e[8], v[8], wi[8], p1 = 0.0f, p2 = 0.0f;
+            cur.dy[i].get(e);
+            cur.h[i].get(v);
+            if (!kHoldW) weight(i, wi);
+            if (kEdge != kWhole && !whole(i)) {
+#pragma unroll
+                for (int j = 0; j < 8; ++j) e[j] = sp[i].own(j) ? e[j] : 0.0f, v[j] = sp[i].own(j) ? v[j] : mean;
+            }
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
-                const float xh = (v[j] - mean) * rstd, gj = e[j] * w[i][j];
-                s1 = __builtin_fmaf(gj, xh, s1);
-                s2 += gj;
-                if (live) {
-                    sum_w[i][j] = __builtin_fmaf(e[j], xh, sum_w[i][j]);
-                    sum_b[i][j] += e[j];
+                v[j] = (v[j] - mean) * rstd;
+                const float gj = e[j] * (kHoldW ? w[kHoldW ? i : 0][j] : wi[j]);
+                p1 = __builtin_fmaf(gj, v[j], p1);
+                p2 += gj;
+                if (kSums == kInRegs && live) {
+                    sum_w[kRegs > i ? i : 0][j] = __builtin_fmaf(e[j], v[j], sum_w[kRegs > i ? i : 0][j]);
+                    sum_b[kRegs > i ? i : 0][j] += e[j];
                 }
             }
+            if (kSums == kInLds && live) {
+#pragma unroll
+                for (int half = 0; half < 2; ++half) {
+                    const float *pe = e + 4 * half, *pv = v + 4 * half;
+                    float4 m = *kept(0, i, half);
+                    m.x = __builtin_fmaf(pe[0], pv[0], m.x);
+                    m.y = __builtin_fmaf(pe[1], pv[1], m.y);
+                    m.z = __builtin_fmaf(pe[2], pv[2], m.z);
+                    m.w = __builtin_fmaf(pe[3], pv[3], m.w);
+                    *kept(0, i, half) = m;
+                    m = *kept(1, i, half);
+                    m.x += pe[0], m.y += pe[1], m.z += pe[2], m.w += pe[3];
+                    *kept(1, i, half) = m;
+                }
+            }
+            s1 += kEdge != kWhole || sp[i].any() ? p1 : 0.0f;
+            s2 += kEdge != kWhole || sp[i].any() ? p2 : 0.0f;
         }
-        // both sums with one barrier; the two parities keep a row's slots
-        // apart from the next row's
+        // both sums with one barrier, lanes 0-15 the one and 16-31 the other;
+        // the two parities keep a row's slots apart from the next row's
         s1 = wave_sum(s1);
         s2 = wave_sum(s2);
-        if (kTpr > 64) {
-            constexpr int kWaves = kTpr / 64;
-            const int wave = threadIdx.x >> 6, first = wave / kWaves * kWaves;
-            if ((threadIdx.x & 63) == 0) red[parity][0][wave] = s1, red[parity][1][wave] = s2;
+        if (a.waves > 1) {
+            if (lane == 0) red[parity][0][wave] = s1, red[parity][1][wave] = s2;
             __syncthreads();
-            s1 = red[parity][0][first];
-            s2 = red[parity][1][first];
-#pragma unroll
-            for (int i = 1; i < kWaves; ++i) {
-                s1 += red[parity][0][first + i];
-                s2 += red[parity][1][first + i];
-            }
+            const uint32_t k = lane & 15u;
+            const float v = sum16(k < a.waves && g < a.groups ? red[parity][(lane >> 4) & 1u][first + k] : 0.0f);
+            s1 = lane_value(v, 15);
+            s2 = lane_value(v, 31);
         }
         const float c1 = s1 * inv_n, c2 = a.layer ? s2 * inv_n : 0.0f;
         if (live) {
 #pragma unroll
             for (int i = 0; i < kC; ++i) {
-                const uint32_t c = i * kTpr + t;
-                float e[8], v[8];
-                dy[i].get(e);
-                h[i].get(v);
+                float e[8], v[8], wi[8];
+                cur.dy[i].get(e);
+                cur.h[i].get(v);
+                if (!kHoldW) weight(i, wi);
 #pragma unroll
                 for (int j = 0; j < 8; ++j) {
-                    const float xh = (v[j] - mean) * rstd;
-                    v[j] = __builtin_fmaf(-xh, c1, __builtin_fmaf(e[j], w[i][j], -c2)) * rstd;
+                    const float xh = (v[j] - mean) * rstd, gj = kHoldW ? w[kHoldW ? i : 0][j] : wi[j];
+                    v[j] = __builtin_fmaf(-xh, c1, __builtin_fmaf(e[j], gj, -c2)) * rstd;
                 }
                 if (kRes) {
                     float r[8];
-                    res[i].get(r);
+                    cur.res[i].get(r);
 #pragma unroll
                     for (int j = 0; j < 8; ++j) v[j] = r[j] + v[j];
                 }
                 Chunk<T> out;
                 if (a.dh) {
                     out.set(v);
-                    store_chunk<T, kTail>(reinterpret_cast<T *>(a.dh) + row * a.ld_dh, c, cols, out);
+                    store_chunk<T, kEdge, kStream<T>>(reinterpret_cast<T *>(a.dh) + row * a.ld_dh, sp[i], out);
                 }
                 if (kDx) {
-                    if (d.drop) apply_dropout(d, (uint32_t)row, c, v);
+                    if (d.drop) apply_dropout(d, x[i], v);
                     out.set(v);
-                    store_chunk<T, kTail>(reinterpret_cast<T *>(a.dx) + row * a.ld_dx, c, cols, out);
+                    store_chunk<T, kEdge, kStream<T>>(reinterpret_cast<T *>(a.dx) + row * a.ld_dx, sp[i], out);
                 }
             }
         }
+        parity ^= 1;
+    };
+    // two rows in registers: the one after the next is asked for as soon as
+    // a row is done, before the next one has to be there
+    Row one, two;
+    fetch(base0, one);
+    if constexpr (kSums == kNone) {  // no sums to carry: a workgroup ends with its rows
+        work(base0, one);
+        return;
     }
-    if (!a.parts) return;
-    // parts[workgroup][gamma, beta][cols]
-#pragma unroll
-    for (int which = 0; which < 2; ++which) {
-        if (which == 1 && !a.layer_beta) break;
-        float *part = a.parts + ((size_t)blockIdx.x * 2 + which) * cols;
-        if (kGroups == 1) {
-#pragma unroll
-            for (int i = 0; i < kC; ++i)
-#pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    const uint32_t col = (i * kTpr + t) * 8u + j;
-                    if (col < cols) part[col] = which ? sum_b[i][j] : sum_w[i][j];
-                }
+    if (kAhead) fetch(base0 + stride, two);
+    for (uint32_t base = base0; base < rows; base += kAhead ? 2 * stride : stride) {
+        work(base, one);
+        if (kAhead) {
+            fetch(base + 2 * stride, one);
+            if (base + stride >= rows) break;
+            work(base + stride, two);
+            fetch(base + 3 * stride, two);
         } else {
-            __syncthreads();
+            fetch(base + stride, one);
+        }
+    }
+    if constexpr (kSums != kNone) {  // parts[workgroup][gamma, beta][cols]
 #pragma unroll
-            for (int i = 0; i < kC; ++i)
+        for (int which = 0; which < 2; ++which) {
+            if (which == 1 && !dbeta) break;
+            if (kSums == kInRegs && a.groups > 1) {
+                __syncthreads();
 #pragma unroll
-                for (int j = 0; j < 8; ++j) fold[(i * 8 + j) * kGradThreads + threadIdx.x] = which ? sum_b[i][j] : sum_w[i][j];
-            __syncthreads();
-            for (uint32_t col = threadIdx.x; col < cols; col += kGradThreads) {
-                const uint32_t c = col >> 3, at = ((c / kTpr) * 8u + (col & 7u)) * kGradThreads + c % kTpr;
-                float s = fold[at];
-                for (int k = 1; k < kGroups; ++k) s += fold[at + k * kTpr];
-                part[col] = s;
+                for (int i = 0; i < kC; ++i) {
+                    const float *v = which ? sum_b[kRegs > i ? i : 0] : sum_w[kRegs > i ? i : 0];
+#pragma unroll
+                    for (int half = 0; half < 2; ++half)
+                        *kept(0, i, half) = make_float4(v[4 * half], v[4 * half + 1], v[4 * half + 2], v[4 * half + 3]);
+                }
+            }
+            if (a.groups > 1) __syncthreads();
+            if (g == 0) {  // the first group's threads add the others' sums
+                float *part = a.parts + ((size_t)block * 2 + which) * cols;
+#pragma unroll
+                for (int i = 0; i < kC; ++i) {
+                    float v[8];
+#pragma unroll
+                    for (int half = 0; half < 2; ++half) {
+                        float4 m;
+                        if (kSums == kInLds) {
+                            m = *kept(which, i, half);
+                        } else {
+                            const float *r = (which ? sum_b[kRegs > i ? i : 0] : sum_w[kRegs > i ? i : 0]) + 4 * half;
+                            m = make_float4(r[0], r[1], r[2], r[3]);
+                        }
+                        for (uint32_t k = 1; k < a.groups; ++k) {
+                            const float4 o = kept(kSums == kInLds ? which : 0, i, half)[k * tpr];
+                            m.x += o.x, m.y += o.y, m.z += o.z, m.w += o.w;
+                        }
+                        v[4 * half] = m.x, v[4 * half + 1] = m.y, v[4 * half + 2] = m.z, v[4 * half + 3] = m.w;
+                    }
+                    Chunk<float> out;
+                    out.set(v);
+                    store_chunk<float, kEdge>(part, sp[i], out);
+                }
             }
         }
     }
+}
+
+// The weight sums of rows too wide to keep them beside the rows' own work.
+template <typename T, Edge kEdge>
+__global__ __launch_bounds__(1024) void norm_weight_sums_kernel(const NormGradArgs a)
+{
+    float *part = a.parts + (size_t)blockIdx.y * 2 * (uint32_t)a.cols;
+    weight_sums<T, kEdge>(a, blockIdx.x, blockIdx.y, gridDim.y, part, part + a.cols);
 }
 
 // out[which][col] = sum of the workgroups' parts.  64 columns of a workgroup
@@ -391,7 +611,7 @@ __global__ __launch_bounds__(1024) void norm_grad_weights_kernel(const float *__
     float *out = which ? dbeta : dgamma;
     float v = 0.0f;
     if (col < cols && out) {
-#pragma unroll 4
+#pragma unroll 16
         for (uint32_t p = slice; p < nparts; p += 16) v += parts[((size_t)p * 2 + which) * cols + col];
     }
     s[slice][threadIdx.x & 63u] = v;
@@ -403,45 +623,82 @@ __global__ __launch_bounds__(1024) void norm_grad_weights_kernel(const float *__
     }
 }
 
-int grad_rows_at_once(int64_t cols)
+// How a call is run.  Weight sums: in the rows' own kernel (kInRows), beside
+// it in workgroups of their own that read the rows again (kBeside: small
+// calls, where a second launch would cost more than the reading), or by a
+// kernel of their own (kApart: rows too wide to keep their sums).
+enum How { kNoSums, kInRows, kBeside, kApart };
+struct GradPlan {
+    How sums;
+    int chunks_per_thread;
+    uint32_t waves, groups;
+    int64_t row_blocks, parts;
+};
+GradPlan grad_plan(int64_t rows, int64_t cols, bool sums)
 {
-    const int64_t chunks = (cols + 7) / 8;
-    return chunks <= 128 ? 16 : chunks <= 256 ? 8 : chunks <= 512 ? 4 : chunks <= 1024 ? 2 : 1;
+    const int64_t waves1 = (cols + 511) / 512;  // waves of a row at one chunk per thread
+    GradPlan g{};
+    // 16 waves fit a workgroup
+    g.chunks_per_thread = waves1 > 32 ? 4 : waves1 > 16 ? 2 : 1;
+    g.waves = (uint32_t)((waves1 + g.chunks_per_thread - 1) / g.chunks_per_thread);
+    g.groups = 16 / g.waves;
+    const int64_t need = (rows + g.groups - 1) / g.groups;
+    g.sums = !sums ? kNoSums : g.chunks_per_thread == 4 ? kApart : rows <= 1024 && rows * cols <= (1 << 21) ? kBeside : kInRows;
+    g.row_blocks = g.sums == kInRows && need > kMaxParts ? kMaxParts : need;
+    const int64_t runs = (rows + 127) / 128;
+    g.parts = g.sums == kInRows ? g.row_blocks : g.sums == kApart ? (runs < 4 ? runs : 4) : 0;
+    return g;
 }
 
-template <typename T, int kTpr, int kC>
-void run_norm_grad(const NormGradArgs &a, const Dropout &d, unsigned grid, hipStream_t st)
+template <typename T, int kC, Sums kSums>
+void run_norm_grad(const NormGradArgs &a, const Dropout &d, How how, float *dgamma, float *dbeta, hipStream_t st)
 {
-    const bool tail = a.cols % 8 != 0;
-#define FP4Q_NORM_GRAD(RES, DX, TAIL)                                                                             \
-    hipLaunchKernelGGL((norm_grad_kernel<T, kTpr, kC, RES, DX, TAIL>), dim3(grid), dim3(kGradThreads), 0, st, a, d)
-#define FP4Q_NORM_GRAD_T(RES, DX) \
-    do { if (tail) FP4Q_NORM_GRAD(RES, DX, true); else FP4Q_NORM_GRAD(RES, DX, false); } while (0)
+    const unsigned blocks = a.row_blocks + (how == kBeside ? (unsigned)((a.cols + 63) / 64) : 0u);
+    const unsigned wide = 1u << 20;  // a launch's threads along x are below 2^32
+    const dim3 grid(blocks < wide ? blocks : wide, (blocks + wide - 1) / wide);
+    const dim3 block(how == kBeside ? 1024 : a.waves * a.groups * 64);
+    const Edge edge = edge_of(a.cols);
+#define FP4Q_NORM_GRAD(RES, DX, EDGE)                                                                          \
+    hipLaunchKernelGGL((norm_grad_kernel<T, kC, kC == 1 || (kC == 2 && (sizeof(T) == 2 || !RES)), kSums, RES, DX, EDGE>), \
+                       grid, block, 0, st, a, d, dgamma, dbeta)
+#define FP4Q_NORM_GRAD_E(RES, DX)                            \
+    do {                                                     \
+        if (edge == kWhole)                                  \
+            FP4Q_NORM_GRAD(RES, DX, kWhole);                 \
+        else if (edge == kRagged)                            \
+            FP4Q_NORM_GRAD(RES, DX, kRagged);                \
+        else if constexpr (kC == 1)                          \
+            FP4Q_NORM_GRAD(RES, DX, kTiny);                  \
+    } while (0)
     if (a.dres) {
-        if (a.dx) FP4Q_NORM_GRAD_T(true, true); else FP4Q_NORM_GRAD_T(true, false);
+        if (a.dx) FP4Q_NORM_GRAD_E(true, true); else FP4Q_NORM_GRAD_E(true, false);
     } else {
-        if (a.dx) FP4Q_NORM_GRAD_T(false, true); else FP4Q_NORM_GRAD_T(false, false);
+        if (a.dx) FP4Q_NORM_GRAD_E(false, true); else FP4Q_NORM_GRAD_E(false, false);
     }
-#undef FP4Q_NORM_GRAD_T
+#undef FP4Q_NORM_GRAD_E
 #undef FP4Q_NORM_GRAD
 }
 
 template <typename T>
-void pick_norm_grad(const NormGradArgs &a, const Dropout &d, unsigned grid, hipStream_t st)
+void pick_norm_grad(const NormGradArgs &a, const Dropout &d, const GradPlan &g, float *dgamma, float *dbeta,
+                    hipStream_t st)
 {
-    const int64_t chunks = (a.cols + 7) / 8;
-    if (chunks <= 128)
-        run_norm_grad<T, 64, 2>(a, d, grid, st);
-    else if (chunks <= 256)
-        run_norm_grad<T, 128, 2>(a, d, grid, st);
-    else if (chunks <= 512)
-        run_norm_grad<T, 256, 2>(a, d, grid, st);
-    else if (chunks <= 1024)
-        run_norm_grad<T, 512, 2>(a, d, grid, st);
-    else if (chunks <= 2048)
-        run_norm_grad<T, 1024, 2>(a, d, grid, st);
+    if (g.sums != kBeside && g.sums != kInRows) dgamma = dbeta = nullptr;  // not the row kernel's
+    if (g.chunks_per_thread == 4)
+        run_norm_grad<T, 4, kNone>(a, d, g.sums, dgamma, dbeta, st);
+    else if (g.sums != kInRows)
+        g.chunks_per_thread == 2 ? run_norm_grad<T, 2, kNone>(a, d, g.sums, dgamma, dbeta, st)
+                                 : run_norm_grad<T, 1, kNone>(a, d, g.sums, dgamma, dbeta, st);
     else
-        run_norm_grad<T, 1024, 4>(a, d, grid, st);
+        g.chunks_per_thread == 2 ? run_norm_grad<T, 2, kInLds>(a, d, g.sums, dgamma, dbeta, st)
+                                 : run_norm_grad<T, 1, kInRegs>(a, d, g.sums, dgamma, dbeta, st);
+    if (g.sums == kApart) {
+        const dim3 grid((unsigned)((a.cols + 63) / 64), (unsigned)g.parts);
+        if (a.cols % 8)
+            hipLaunchKernelGGL((norm_weight_sums_kernel<T, kRagged>), grid, dim3(1024), 0, st, a);
+        else
+            hipLaunchKernelGGL((norm_weight_sums_kernel<T, kWhole>), grid, dim3(1024), 0, st, a);
+    }
 }
 
 }  // namespace
@@ -458,35 +715,30 @@ int launch_norm(const NormArgs &a, hipStream_t st)
     return hipGetLastError() == hipSuccess ? 0 : 1;
 }
 
-// Workgroups of the gradient kernel, each of which keeps one row of sums.
-static int64_t grad_parts(int64_t rows, int64_t cols)
-{
-    const int at_once = grad_rows_at_once(cols);
-    const int64_t need = (rows + at_once - 1) / at_once;
-    return need < kMaxParts ? need : kMaxParts;
-}
-
 size_t norm_grad_workspace_bytes(int64_t rows, int64_t cols)
 {
-    return rows <= 0 || cols <= 0 ? 0 : (size_t)grad_parts(rows, cols) * 2u * (size_t)cols * sizeof(float);
+    return rows <= 0 || cols <= 0 ? 0 : (size_t)grad_plan(rows, cols, true).parts * 2u * (size_t)cols * sizeof(float);
 }
 
 int launch_norm_grad(NormGradArgs a, float *dgamma, float *dbeta, hipStream_t st)
 {
     const Dropout d = dropout_of(a.p, a.seed, a.stream_id);
-    const unsigned grid = (unsigned)grad_parts(a.rows, a.cols);
-    if (!dgamma && !dbeta) a.parts = nullptr;
-    a.layer_beta = dbeta != nullptr;
-    if (grid > 0) {
+    const bool sums = dgamma || dbeta;
+    const GradPlan g = grad_plan(a.rows, a.cols, sums);
+    a.waves = g.waves;
+    a.groups = g.groups;
+    a.row_blocks = (uint32_t)g.row_blocks;
+    if (a.rows > 0) {
         if (a.bf16)
-            pick_norm_grad<bf16_t>(a, d, grid, st);
+            pick_norm_grad<bf16_t>(a, d, g, dgamma, dbeta, st);
         else
-            pick_norm_grad<float>(a, d, grid, st);
+            pick_norm_grad<float>(a, d, g, dgamma, dbeta, st);
         if (hipGetLastError() != hipSuccess) return 1;
+        if (!sums || g.sums == kBeside) return 0;
     }
-    if (dgamma || dbeta)
-        hipLaunchKernelGGL(norm_grad_weights_kernel, dim3((unsigned)((a.cols + 63) / 64), dbeta ? 2 : 1), dim3(1024), 0,
-                           st, a.parts, grid, (uint32_t)a.cols, dgamma, dbeta);
+    // joins the parts, or with no rows writes zeros
+    hipLaunchKernelGGL(norm_grad_weights_kernel, dim3((unsigned)((a.cols + 63) / 64), dbeta ? 2 : 1), dim3(1024), 0, st,
+                       a.parts, (uint32_t)(a.rows > 0 ? g.parts : 0), (uint32_t)a.cols, dgamma, dbeta);
     return hipGetLastError() == hipSuccess ? 0 : 1;
 }
 

@@ -23,53 +23,88 @@ namespace fp4q {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kAngles = 1024;    // angles of a workgroup: tokens * pairs, pairs rounded up to 8
+constexpr int kAngles = 1024;  // angles of a workgroup: tokens * pairs, pairs rounded up to 8
 
-template <typename T>
-__device__ __forceinline__ void load8(const T *p, uint32_t n, float v[8])
+// Eight elements, or the first n where the head ends sooner (kRag).
+template <typename T, bool kRag, bool kNt>
+__device__ __forceinline__ void load8(const T *p, uint32_t n, Chunk<T> &q)
 {
-    Chunk<T> q;
-    if (n >= 8u) {
-        q.load(p);
-        q.get(v);
+    if (!kRag || n >= 8u) {
+        q.template load<kNt>(p);
     } else {
+        float v[8];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) v[j] = j < (int)n ? Chunk<T>::load1(p + j) : 0.0f;
+        for (int j = 0; j < 8; ++j) v[j] = j < (int)n ? as_float(p[j]) : 0.0f;
+        q.set(v);
     }
 }
-template <typename T>
+template <typename T, bool kRag>
 __device__ __forceinline__ void store8(T *p, uint32_t n, const float v[8])
 {
     Chunk<T> q;
     q.set(v);
-    if (n >= 8u)
-        q.store(p);
-    else
-        q.store_first(p, n);
+    if (!kRag || n >= 8u)
+        q.template store<false>(p);
+    else if (n != 0u)
+        q.store_own(p, 0u, n);
 }
 
-// grid.x: groups of a.tokens_at_once tokens.  An item is one chunk of one
-// head of one token: eight pairs, or eight elements to copy.
-template <typename T, bool kInter>
+// An item is one chunk of one head of one token: eight pairs (half style),
+// eight elements that are four pairs (interleaved), or eight elements to copy.
+struct Item {
+    int64_t x, y;       // the head's first element
+    uint32_t first, n;  // the chunk's first element and its size
+    uint32_t angle;     // of its first pair
+    bool copy;
+};
+
+// grid.x: groups of a.tokens_at_once tokens.
+template <typename T, bool kInter, bool kRag>
 __global__ __launch_bounds__(kThreads) void rotary_kernel(const RotaryArgs a, FastDiv per_token_div, FastDiv per_head_div)
 {
     __shared__ __attribute__((aligned(16))) float cs[kAngles], sn[kAngles];
-    const uint32_t half = a.rot >> 1, hc = (half + 7) / 8;  // chunks of pairs
-    const uint32_t cc = a.copy ? (a.dim - a.rot + 7) / 8 : 0;  // chunks to copy
-    const uint32_t per_head = hc + cc, per_token = per_head * a.heads;
-    for (int64_t tok0 = (int64_t)blockIdx.x * a.tokens_at_once; tok0 < a.tokens;
-         tok0 += (int64_t)gridDim.x * a.tokens_at_once) {
-    const uint32_t ntok = (uint32_t)min((int64_t)a.tokens_at_once, a.tokens - tok0);
-    for (uint32_t i = threadIdx.x; i < ntok * hc * 8; i += kThreads) {
-        const uint32_t tk = i / (hc * 8), k = i - tk * (hc * 8);
+    constexpr bool kNt = kStream<T>;
+    const uint32_t half = a.rot >> 1, angles = (half + 7u) & ~7u;  // of a token
+    const uint32_t turned = kInter ? (a.rot + 7u) >> 3 : angles >> 3;  // chunks of a head to turn
+    const uint32_t per_head = turned + (a.copy ? (a.dim - a.rot + 7u) >> 3 : 0u), per_token = per_head * a.heads;
+    const T *x = reinterpret_cast<const T *>(a.x);
+    T *y = reinterpret_cast<T *>(a.y);
+    const int64_t tok0 = (int64_t)(blockIdx.y * gridDim.x + blockIdx.x) * a.tokens_at_once;
+    if (tok0 >= a.tokens) return;
+    const uint32_t ntok = (uint32_t)min((int64_t)a.tokens_at_once, a.tokens - tok0), total = ntok * per_token;
+    const auto item = [&](uint32_t it) {
+        const uint32_t tk = fast_div(it, per_token_div), in_tok = it - tk * per_token;
+        const uint32_t head = fast_div(in_tok, per_head_div), ch = in_tok - head * per_head;
+        Item m;
+        m.x = (tok0 + tk) * a.x_token + (int64_t)head * a.x_head;
+        m.y = (tok0 + tk) * a.y_token + (int64_t)head * a.y_head;
+        m.copy = ch >= turned;
+        const uint32_t from = m.copy ? a.rot : 0u, to = m.copy ? a.dim : kInter ? a.rot : half;
+        // a part that eight does not divide: its last chunk is its last eight
+        // elements, some of them made twice; in place (kRag) it is what is left
+        m.first = kRag ? from + (ch - (m.copy ? turned : 0u)) * 8u : min(from + (ch - (m.copy ? turned : 0u)) * 8u, to - 8u);
+        m.n = min(8u, to - m.first);
+        m.angle = tk * angles + (kInter ? m.first >> 1 : m.first);
+        return m;
+    };
+    const auto fetch = [&](const Item &m, Chunk<T> &u, Chunk<T> &v) {
+        load8<T, kRag, kNt>(x + m.x + m.first, m.n, u);
+        if (!kInter) load8<T, kRag, kNt>(x + m.x + m.first + (m.copy ? 0u : half), m.n, v);
+    };
+    // the first item is on its way while the angles are made
+    uint32_t it = min(threadIdx.x, total - 1u);
+    Item m = item(it);
+    Chunk<T> u, v;
+    fetch(m, u, v);
+    for (uint32_t i = threadIdx.x; i < ntok * angles; i += kThreads) {
+        const uint32_t tk = i / angles, k = i - tk * angles;
         float c = 0.0f, s = 0.0f;
         if (k < half) {
             const int64_t pos = a.pos64 ? reinterpret_cast<const int64_t *>(a.positions)[tok0 + tk]
                                         : (int64_t) reinterpret_cast<const int32_t *>(a.positions)[tok0 + tk];
             double turns = (double)pos * ((double)a.inv_freq[k] * 0.15915494309189533577);
             turns -= __builtin_rint(turns);
-            const float f = 2.0f * (float)turns;
-            sincospif(f, &s, &c);
+            sincospif(2.0f * (float)turns, &s, &c);
             c *= a.scale;
             s *= a.inverse ? -a.scale : a.scale;
         }
@@ -77,53 +112,37 @@ __global__ __launch_bounds__(kThreads) void rotary_kernel(const RotaryArgs a, Fa
         sn[i] = s;
     }
     __syncthreads();
-    const T *x = reinterpret_cast<const T *>(a.x);
-    T *y = reinterpret_cast<T *>(a.y);
-    for (uint32_t it = threadIdx.x; it < ntok * per_token; it += kThreads) {
-        const uint32_t tk = fast_div(it, per_token_div), in_tok = it - tk * per_token;
-        const uint32_t head = fast_div(in_tok, per_head_div), ch = in_tok - head * per_head;
-        const T *px = x + (tok0 + tk) * a.x_token + (int64_t)head * a.x_head;
-        T *py = y + (tok0 + tk) * a.y_token + (int64_t)head * a.y_head;
-        if (ch < hc) {
-            const uint32_t k0 = ch * 8, n = min(8u, half - k0);
-            float c[8], s[8], u[8], v[8];
-            const uint32_t at = (tk * hc + ch) * 8;
+    for (it = threadIdx.x; it < total; it += kThreads) {
+        const Item next = item(min(it + kThreads, total - 1u));
+        Chunk<T> nu, nv;
+        fetch(next, nu, nv);  // in place: the last item again, after its store perhaps, but then it is not used
+        float p[8], q[8], o[8], r[8];
+        u.get(p);
+        T *out = y + m.y + m.first;
+        if (m.copy) {
+            store8<T, kRag>(out, m.n, p);
+        } else if (kInter) {
 #pragma unroll
-            for (int j = 0; j < 8; ++j) c[j] = cs[at + j], s[j] = sn[at + j];
-            if (kInter) {
-                const uint32_t n2 = 2 * n;
-                load8(px + 2 * k0, min(n2, 8u), u);
-                load8(px + 2 * k0 + 8, n2 > 8u ? n2 - 8u : 0u, v);
-                float p[8], q[8];
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    p[2 * j] = u[2 * j] * c[j] - u[2 * j + 1] * s[j];
-                    p[2 * j + 1] = u[2 * j + 1] * c[j] + u[2 * j] * s[j];
-                    q[2 * j] = v[2 * j] * c[4 + j] - v[2 * j + 1] * s[4 + j];
-                    q[2 * j + 1] = v[2 * j + 1] * c[4 + j] + v[2 * j] * s[4 + j];
-                }
-                store8(py + 2 * k0, min(n2, 8u), p);
-                store8(py + 2 * k0 + 8, n2 > 8u ? n2 - 8u : 0u, q);
-            } else {
-                load8(px + k0, n, u);
-                load8(px + half + k0, n, v);
-                float p[8], q[8];
-#pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    p[j] = u[j] * c[j] - v[j] * s[j];
-                    q[j] = v[j] * c[j] + u[j] * s[j];
-                }
-                store8(py + k0, n, p);
-                store8(py + half + k0, n, q);
+            for (int j = 0; j < 4; ++j) {
+                const float c = cs[m.angle + j], s = sn[m.angle + j];
+                o[2 * j] = p[2 * j] * c - p[2 * j + 1] * s;
+                o[2 * j + 1] = p[2 * j + 1] * c + p[2 * j] * s;
             }
+            store8<T, kRag>(out, m.n, o);
         } else {
-            const uint32_t e = a.rot + (ch - hc) * 8;
-            float u[8];
-            load8(px + e, min(8u, a.dim - e), u);
-            store8(py + e, min(8u, a.dim - e), u);
+            v.get(q);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const float c = cs[m.angle + j], s = sn[m.angle + j];
+                o[j] = p[j] * c - q[j] * s;
+                r[j] = q[j] * c + p[j] * s;
+            }
+            store8<T, kRag>(out, m.n, o);
+            store8<T, kRag>(out + half, m.n, r);
         }
-    }
-    __syncthreads();  // the next tokens' angles take the same place
+        m = next;
+        u = nu;
+        v = nv;
     }
 }
 
@@ -131,22 +150,35 @@ __global__ __launch_bounds__(kThreads) void rotary_kernel(const RotaryArgs a, Fa
 
 int launch_rotary(RotaryArgs a, hipStream_t st)
 {
-    const uint32_t half = a.rot / 2, hc = (half + 7) / 8;
-    const uint32_t cc = a.copy ? (a.dim - a.rot + 7) / 8 : 0;
-    const uint32_t per_head = hc + cc, per_token = per_head * a.heads;
-    int64_t at_once = kAngles / (hc * 8);
+    const uint32_t half = a.rot / 2, angles = (half + 7) / 8 * 8;
+    const uint32_t turned = a.interleaved ? (a.rot + 7) / 8 : angles / 8;
+    const uint32_t per_head = turned + (a.copy ? (a.dim - a.rot + 7) / 8 : 0), per_token = per_head * a.heads;
+    // four tokens to a workgroup, but at least about four workgroups to a
+    // compute unit
+    int64_t at_once = kAngles / angles;
     if (at_once > 4) at_once = 4;
     while (at_once > 1 && (a.tokens + at_once - 1) / at_once < 1024) at_once >>= 1;
     a.tokens_at_once = (uint32_t)at_once;
-    const int64_t groups = (a.tokens + at_once - 1) / at_once;
-    const dim3 grid((unsigned)(groups < (1 << 20) ? groups : (1 << 20)));
+    const int64_t groups = (a.tokens + at_once - 1) / at_once, wide = 1 << 20;  // a launch's threads along x are below 2^32
+    const dim3 grid((unsigned)(groups < wide ? groups : wide), (unsigned)((groups + wide - 1) / wide));
     const FastDiv dt = fast_div_for(per_token), dh = fast_div_for(per_head);
-#define FP4Q_ROTARY(T, INTER) hipLaunchKernelGGL((rotary_kernel<T, INTER>), grid, dim3(kThreads), 0, st, a, dt, dh)
-    if (a.bf16) {
-        if (a.interleaved) FP4Q_ROTARY(bf16_t, true); else FP4Q_ROTARY(bf16_t, false);
-    } else {
-        if (a.interleaved) FP4Q_ROTARY(float, true); else FP4Q_ROTARY(float, false);
-    }
+    const uint32_t part = a.interleaved ? a.rot : half, rest = a.copy ? a.dim - a.rot : 0;
+    const bool rag = (part % 8 != 0 && (part < 8 || a.x == a.y)) || (rest % 8 != 0 && rest < 8);
+#define FP4Q_ROTARY(T, INTER, RAG) \
+    hipLaunchKernelGGL((rotary_kernel<T, INTER, RAG>), grid, dim3(kThreads), 0, st, a, dt, dh)
+#define FP4Q_ROTARY_T(T)                                                                      \
+    do {                                                                                      \
+        if (a.interleaved) {                                                                  \
+            if (rag) FP4Q_ROTARY(T, true, true); else FP4Q_ROTARY(T, true, false);            \
+        } else {                                                                              \
+            if (rag) FP4Q_ROTARY(T, false, true); else FP4Q_ROTARY(T, false, false);          \
+        }                                                                                     \
+    } while (0)
+    if (a.bf16)
+        FP4Q_ROTARY_T(bf16_t);
+    else
+        FP4Q_ROTARY_T(float);
+#undef FP4Q_ROTARY_T
 #undef FP4Q_ROTARY
     return hipGetLastError() == hipSuccess ? 0 : 1;
 }

@@ -44,9 +44,9 @@ __global__ __launch_bounds__(256) void swiglu_grad_kernel(const uint16_t *__rest
     const int64_t gcol = (j / pair) * 2 * pair + (j % pair);
     for (int64_t m = blockIdx.y; m < M; m += gridDim.y) {
         const uint16_t *row = c + m * ldc + gcol;
-        const u32x4v g = __builtin_nontemporal_load(reinterpret_cast<const u32x4v *>(row));
-        const u32x4v u = __builtin_nontemporal_load(reinterpret_cast<const u32x4v *>(row + pair));
-        const u32x4v d = __builtin_nontemporal_load(reinterpret_cast<const u32x4v *>(dh + m * ld_dh + j));
+        const u32x4v g = *reinterpret_cast<const u32x4v *>(row);
+        const u32x4v u = *reinterpret_cast<const u32x4v *>(row + pair);
+        const u32x4v d = *reinterpret_cast<const u32x4v *>(dh + m * ld_dh + j);
         u32x4v og, ou, oh;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {

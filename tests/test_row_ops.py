@@ -69,11 +69,11 @@ def test_norm_refusals(L):
 
 
 def test_norm_grad_refusals(L):
-    need = L.fp4q_norm_grad_workspace_bytes(40, 128)
+    need = L.fp4q_norm_grad_workspace_bytes(4000, 128)
     assert need > 0 and L.fp4q_norm_grad_workspace_bytes(0, 128) == 0
     assert L.fp4q_norm_grad_workspace_bytes(10 ** 6, 4096) == 256 * 2 * 4096 * 4
 
-    def f(dy=A[0], rows=40, cols=128, ld=128, t=1, h=A[1], ldh=128, res=A[2], ldr=128, kind=0, g=A[3], wt=0, mean=A[4],
+    def f(dy=A[0], rows=4000, cols=128, ld=128, t=1, h=A[1], ldh=128, res=A[2], ldr=128, kind=0, g=A[3], wt=0, mean=A[4],
           rstd=A[5], p=0.1, dh=A[6], ldd=128, dx=A[7], ldx=128, dg=A[8], db=A[9], ws=A[10], wb=need):
         return L.fp4_norm_grad(dy, rows, cols, ld, t, h, ldh, res, ldr, kind, g, wt, mean, rstd, p, 1, 0, dh, ldd, dx, ldx,
                                dg, db, ws, wb, None)
@@ -143,8 +143,11 @@ def test_binding_refusals():
                  lambda: B.fp4_rotary(x[:, None], torch.zeros(4, dtype=torch.int64), f.double()),
                  lambda: B.rotary_frequencies(63), lambda: B.rotary_frequencies(64, method="other"),
                  lambda: B.rotary_frequencies(64, method="linear", factor=0.5)):
-        with pytest.raises(ValueError):
+        with pytest.raises(ValueError) as e:
             call()
+        assert "current GPU" not in str(e.value)
+    with pytest.raises(ValueError, match="current GPU"):  # nothing wrong but the place
+        B.fp4_dropout(x, 0.1, seed=1)
 
 
 def test_reference_draws_the_oracles_philox():
