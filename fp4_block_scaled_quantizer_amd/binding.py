@@ -629,6 +629,8 @@ def fp4_norm_grad(dy: torch.Tensor, h: torch.Tensor, gamma: Optional[torch.Tenso
         if wbytes:
             workspace = torch.empty((wbytes,), dtype=torch.uint8, device=dy.device)
             pw = workspace.data_ptr()
+            if stream is not None:  # freed here, on the current stream, while `stream` may still use it
+                workspace.record_stream(stream)
     elif workspace is not None:
         if workspace.get_device() != dev or not workspace.is_contiguous():
             raise ValueError("workspace must be a contiguous tensor on dy's device")

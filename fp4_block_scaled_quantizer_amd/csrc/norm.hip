@@ -117,16 +117,27 @@ __device__ __forceinline__ void store_mx(const NormArgs &a, int64_t row, uint32_
     code = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(code, __builtin_bit_cast(bf16x2v, w[1]), scale, 1);
     code = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(code, __builtin_bit_cast(bf16x2v, w[2]), scale, 2);
     code = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(code, __builtin_bit_cast(bf16x2v, w[3]), scale, 3);
+    // the scale bytes of four blocks, 16 lanes, as one word in the first lane
+    uint32_t word = sbyte;
+    word |= (uint32_t)__builtin_amdgcn_update_dpp(0, (int)sbyte, 0x104, 0xF, 0xF, true) << 8;   // row_shl:4
+    word |= (uint32_t)__builtin_amdgcn_update_dpp(0, (int)sbyte, 0x108, 0xF, 0xF, true) << 16;  // row_shl:8
+    word |= (uint32_t)__builtin_amdgcn_update_dpp(0, (int)sbyte, 0x10C, 0xF, 0xF, true) << 24;  // row_shl:12
     if (c * 8u >= cols) return;
     uint8_t *codes = reinterpret_cast<uint8_t *>(a.codes), *scales = reinterpret_cast<uint8_t *>(a.scales);
     const uint64_t r = (uint64_t)row;
-    if (a.tiled) {
+    if (a.tiled) {  // cols % 128 == 0
         *reinterpret_cast<uint32_t *>(codes + ((r >> 5) * (cols >> 6) + (c >> 3)) * 1024u +
                                       ((r & 31u) + 32u * ((c >> 2) & 1u)) * 16u + (c & 3u) * 4u) = code;
-        if ((c & 3u) == 0) scales[((uint64_t)(c >> 4) * (uint64_t)a.rows_out + r) * 4u + ((c >> 2) & 3u)] = (uint8_t)sbyte;
+        if ((c & 15u) == 0)
+            *reinterpret_cast<uint32_t *>(scales + ((uint64_t)(c >> 4) * (uint64_t)a.rows_out + r) * 4u) = word;
     } else {
         *reinterpret_cast<uint32_t *>(codes + r * (cols >> 1) + c * 4u) = code;
-        if ((c & 3u) == 0) scales[r * (cols >> 5) + (c >> 2)] = (uint8_t)sbyte;
+        uint8_t *to = scales + r * (cols >> 5) + (c >> 2);
+        if (cols % 128u == 0) {
+            if ((c & 15u) == 0) *reinterpret_cast<u32_a1 *>(to) = word;
+        } else if ((c & 3u) == 0) {
+            *to = (uint8_t)sbyte;
+        }
     }
 }
 
@@ -149,7 +160,15 @@ __global__ __launch_bounds__(kWave ? 256 : 1024) void norm_kernel(const NormArgs
     const auto whole = [&](int i) { return (i * tpr + (kWave ? 64u : wave * 64u + 64u)) * 8u <= cols; };
     // no loop over rows: what a loop would keep ready for its next turn
     // (Philox's keys among it) spills
-    const int64_t block = (int64_t)blockIdx.y * gridDim.x + blockIdx.x, row = kWave ? block * 4 + wave : block;
+    int64_t block = (int64_t)blockIdx.y * gridDim.x + blockIdx.x;
+    if (kMx && a.tiled) {
+        // 32 rows share the tiled operand's cache lines, 16 bytes each:
+        // workgroup b runs on XCD b mod 8, and of 256 rows each XCD gets 32
+        // together, so that its L2 puts the lines together
+        constexpr int64_t kRun = kWave ? 8 : 32;
+        block = block / (8 * kRun) * (8 * kRun) + block % 8 * kRun + block / 8 % kRun;
+    }
+    const int64_t row = kWave ? block * 4 + wave : block;
     if (row >= a.rows_out) return;
     if (kMx && row >= a.rows) {  // tiled output's padding rows: zero codes and scales
         Chunk<bf16_t> z;
@@ -251,7 +270,10 @@ __global__ __launch_bounds__(kWave ? 256 : 1024) void norm_kernel(const NormArgs
 #pragma unroll
         for (int j = 0; j < 8; ++j) v[j] = __builtin_fmaf((v[j] - mean) * rstd, w[j], b[j]);
         q[i].set(v);
-        if (a.y) store_chunk<T, kEdge, kStream<T>>(reinterpret_cast<T *>(a.y) + row * a.ld_y, sp[i], q[i]);
+        // y is left to the caches for the GEMM's producer that reads it next
+        // (norm and producer 8192 x 4096: 56.9 us; with y streamed past them
+        // 59.6); h is read a sub-block later
+        if (a.y) store_chunk<T, kEdge>(reinterpret_cast<T *>(a.y) + row * a.ld_y, sp[i], q[i]);
         if constexpr (kMx) store_mx(a, row, i * tpr + t, cols, q[i]);
     }
 }
@@ -259,7 +281,8 @@ __global__ __launch_bounds__(kWave ? 256 : 1024) void norm_kernel(const NormArgs
 template <typename T, bool kWave, int kC, bool kMx>
 void run_norm(const NormArgs &a, const Dropout &d, hipStream_t st)
 {
-    const int64_t chunks = (a.cols + 7) / 8, need = kWave ? (a.rows_out + 3) / 4 : a.rows_out;
+    const int64_t chunks = (a.cols + 7) / 8, rows = kMx && a.tiled ? (a.rows_out + 255) / 256 * 256 : a.rows_out;
+    const int64_t need = kWave ? (rows + 3) / 4 : rows;
     const int64_t wide = 1 << 20;  // a launch's threads along x are below 2^32
     const dim3 grid((unsigned)(need < wide ? need : wide), (unsigned)((need + wide - 1) / wide));
     const dim3 block(kWave ? 256 : (unsigned)((chunks + 64 * kC - 1) / (64 * kC) * 64));

@@ -34,8 +34,8 @@ __device__ __forceinline__ void sigmoid_pair(float x, float &s, float &c)
 
 // grid.x covers F / 8 column chunks, grid.y strides over rows
 template <bool kH>
-__global__ __launch_bounds__(256) void swiglu_grad_kernel(const uint16_t *__restrict__ dh, const uint16_t *c,
-                                                          uint16_t *dc, uint16_t *__restrict__ h, int64_t M, int64_t F,
+__global__ __launch_bounds__(256) void swiglu_grad_kernel(const uint16_t *dh, const uint16_t *c,
+                                                          uint16_t *dc, uint16_t *h, int64_t M, int64_t F,
                                                           int64_t ld_dh, int64_t ldc, int64_t ld_dc, int64_t ldh,
                                                           int64_t pair)
 {
