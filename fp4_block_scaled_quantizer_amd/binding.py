@@ -1,7 +1,7 @@
 """ctypes binding of ``libfp4q.so`` with the C ABI's entry-point names.
 
-Argument marshalling only: every step of the quantizers and GEMMs runs in the
-library's HIP kernels.  PyTorch supplies device memory (``data_ptr()``) and the
+Argument marshalling only: every step of the quantizers, GEMMs and row-wise
+operators runs in the library's HIP kernels.  PyTorch supplies device memory (``data_ptr()``) and the
 stream (``torch.cuda.current_stream()``).  If the library has not been built
 this module raises -- there is no fallback path.
 """
@@ -17,6 +17,7 @@ import torch
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libfp4q.so")
+ROW_CALLS_PATH = os.path.join(_HERE, "_row_calls.so")
 HEADER = os.path.join(os.path.dirname(_HERE), "include", "fp4q.h")
 
 # enums of include/fp4q.h
@@ -446,64 +447,31 @@ def fp4_gemm_nv(a_codes: torch.Tensor, a_scales: torch.Tensor, a_tensor_scale: t
 
 # ---- the row-wise operators between the GEMMs
 #
-# A decoding step makes these calls on a few kilobytes each, so what they
-# check is read from each tensor once.
+# A decoding step makes these calls on a few kilobytes each, where reading
+# tensors' attributes from Python would cost more than the launch: their
+# arguments are checked and marshalled in csrc/row_calls.cpp.
 
-_TYPES = {torch.float32: OUT_F32, torch.bfloat16: OUT_BF16}
+_row_calls = None
+_row_lib = None  # the library whose addresses _row_calls holds
 _new = tuple.__new__  # of a NamedTuple, at a third of its own constructor's time
 
 
-def _row_stream(stream, dev: int) -> int:
-    """The stream's handle; the tensors' GPU has to be the current one, which
-    the library launches on."""
-    if dev < 0 or dev != torch._C._cuda_getDevice():
-        raise ValueError("the tensors must be on the current GPU")
-    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
-
-
-def _first(t: torch.Tensor, name: str) -> Tuple[torch.Size, int, torch.dtype, int, int]:
-    """(shape, leading dimension, dtype, the library's type, device index) of
-    a call's first matrix: 2-D, fp32 or bf16, unit column stride."""
-    shape, dtype = t.shape, t.dtype
-    kind = _TYPES.get(dtype)
-    if kind is None or len(shape) != 2:
-        raise ValueError(f"{name} must be a 2-D fp32 or bf16 tensor")
-    ld, one = t.stride()
-    cols = shape[1]
-    if shape[0] <= 1:
-        ld = cols
-    if ld < cols or (one != 1 and cols > 1):
-        raise ValueError(f"{name} must have unit column stride and rows that do not overlap")
-    return shape, ld, dtype, kind, t.get_device()
-
-
-def _ld(t: torch.Tensor, name: str, shape: torch.Size, dtype: torch.dtype, dev: int) -> int:
-    """Leading dimension of another matrix, which has the first one's shape,
-    dtype and device."""
-    if t.shape != shape or t.dtype is not dtype or t.get_device() != dev:
-        raise ValueError(f"{name} must be a {tuple(shape)} {dtype} tensor on the same device, not {tuple(t.shape)} "
-                         f"{t.dtype} on {t.device}")
-    ld, one = t.stride()
-    cols = shape[1]
-    if shape[0] <= 1:
-        ld = cols
-    if ld < cols or (one != 1 and cols > 1):
-        raise ValueError(f"{name} must have unit column stride and rows that do not overlap")
-    return ld
-
-
-def _vector(t: torch.Tensor, name: str, n: int, dtype: torch.dtype, dev: int) -> int:
-    if t.numel() != n or t.dtype is not dtype or t.get_device() != dev or not t.is_contiguous():
-        raise ValueError(f"{name} must be {n} contiguous {dtype} elements on the same device")
-    return t.data_ptr()
-
-
-def _weight(t: torch.Tensor, name: str, n: int, dev: int) -> Tuple[int, int]:
-    dtype = t.dtype
-    kind = _TYPES.get(dtype)
-    if kind is None:
-        raise ValueError(f"{name} must be fp32 or bf16")
-    return _vector(t, name, n, dtype, dev), kind
+def _rows():
+    global _row_calls, _row_lib
+    if _lib is None or _row_lib is not _lib:
+        L = lib()
+        try:
+            from fp4_block_scaled_quantizer_amd import _row_calls as calls
+        except ImportError as e:
+            raise FileNotFoundError(
+                f"{ROW_CALLS_PATH} cannot be loaded ({e}): build it with "
+                "`python -c 'import __graft_entry__ as g; g.build()'`") from e
+        at = [ctypes.cast(getattr(L, f), ctypes.c_void_p).value for f in
+              ("fp4_dropout", "fp4_norm", "fp4q_norm_grad_workspace_bytes", "fp4_norm_grad", "fp4_swiglu_grad_bf16",
+               "fp4_rotary")]
+        calls.bind(*at, Fp4qError, torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream)
+        _row_calls, _row_lib = calls, L
+    return _row_calls
 
 
 def fp4_dropout(x: torch.Tensor, p: float, *, seed: int, stream_id: int = 0, residual: Optional[torch.Tensor] = None,
@@ -511,17 +479,7 @@ def fp4_dropout(x: torch.Tensor, p: float, *, seed: int, stream_id: int = 0, res
     """[residual +] dropout(x): each element is kept with probability 1 - p
     (from 16 random bits of (seed, stream_id, row, column)) and scaled. The
     gradient is the same call on the gradient. y may be x or residual."""
-    shape, ld_x, dtype, kind, dev = _first(x, "x")
-    res, ld_r = None, 0
-    if residual is not None:
-        res, ld_r = residual.data_ptr(), _ld(residual, "residual", shape, dtype, dev)
-    if y is None:
-        y = torch.empty(shape, dtype=dtype, device=x.device)
-    status = lib().fp4_dropout(x.data_ptr(), shape[0], shape[1], ld_x, kind, res, ld_r, p, seed, stream_id,
-                               y.data_ptr(), _ld(y, "y", shape, dtype, dev), _row_stream(stream, dev))
-    if status:
-        raise Fp4qError("fp4_dropout", status)
-    return y
+    return _rows().dropout(x, p, seed, stream_id, residual, y, stream)
 
 
 class Norm(NamedTuple):
@@ -545,42 +503,10 @@ def fp4_norm(x: torch.Tensor, gamma: Optional[torch.Tensor] = None, beta: Option
     (else it is x); `save` asks for the row statistics that fp4_norm_grad
     takes; `mx` for the MXFP4 operand of a bf16 y in `layout` (with want_y
     False, instead of y). h and y may each be x or residual."""
-    shape, ld_x, dtype, kt, dev = _first(x, "x")
-    rows, cols = shape
-    pr = ph = py = pm = ps = pg = pb = pc = pe = None
-    ld_r = ld_h = ld_y = wt = 0
-    if residual is not None:
-        pr, ld_r = residual.data_ptr(), _ld(residual, "residual", shape, dtype, dev)
-    if h is None and (residual is not None or p > 0):
-        h = torch.empty(shape, dtype=dtype, device=x.device)
-    if h is not None:
-        ph, ld_h = h.data_ptr(), _ld(h, "h", shape, dtype, dev)
-    if y is None and want_y:
-        y = torch.empty(shape, dtype=dtype, device=x.device)
-    if y is not None:
-        py, ld_y = y.data_ptr(), _ld(y, "y", shape, dtype, dev)
-    if save and mean is None and kind == NORM_LAYER:
-        mean = torch.empty((rows,), dtype=torch.float32, device=x.device)
-    if save and rstd is None:
-        rstd = torch.empty((rows,), dtype=torch.float32, device=x.device)
-    if mean is not None:
-        pm = _vector(mean, "mean", rows, torch.float32, dev)
-    if rstd is not None:
-        ps = _vector(rstd, "rstd", rows, torch.float32, dev)
     if mx or codes is not None or scales is not None:
-        codes, scales = _mx_outputs(rows, cols, layout, codes, scales, x.device)
-        pc, pe = codes.data_ptr(), scales.data_ptr()
-    if gamma is not None:
-        pg, wt = _weight(gamma, "gamma", cols, dev)
-    if beta is not None:
-        pb, bt = _weight(beta, "beta", cols, dev)
-        if gamma is not None and bt != wt:
-            raise ValueError("gamma and beta must have the same type")
-        wt = bt
-    status = lib().fp4_norm(x.data_ptr(), rows, cols, ld_x, kt, pr, ld_r, p, seed, stream_id, ph, ld_h, kind, pg, pb,
-                            wt, eps, py, ld_y, pm, ps, pc, pe, layout, _row_stream(stream, dev))
-    if status:
-        raise Fp4qError("fp4_norm", status)
+        codes, scales = _mx_outputs(x.shape[0], x.shape[1], layout, codes, scales, x.device)
+    y, h, mean, rstd = _rows().norm(x, gamma, beta, kind, eps, residual, p, seed, stream_id, save, want_y, layout, y, h,
+                                    mean, rstd, codes, scales, stream)
     return _new(Norm, (y, h, mean, rstd, codes, scales))
 
 
@@ -602,50 +528,12 @@ def fp4_norm_grad(dy: torch.Tensor, h: torch.Tensor, gamma: Optional[torch.Tenso
     reaches them along the residual stream), dx of fp4_norm's x where p > 0
     (dx equals dh otherwise and is None), and with `weights` dgamma and, for
     NORM_LAYER, dbeta in fp32. dh and dx may each be dy, h or dres."""
-    shape, ld_dy, dtype, kt, dev = _first(dy, "dy")
-    rows, cols = shape
-    pr = px = pm = pg = pw = pdg = pdb = None
-    ld_r = ld_x = wt = wbytes = 0
-    ld_h = _ld(h, "h", shape, dtype, dev)
-    if dres is not None:
-        pr, ld_r = dres.data_ptr(), _ld(dres, "dres", shape, dtype, dev)
-    if dh is None:
-        dh = torch.empty(shape, dtype=dtype, device=dy.device)
-    ld_dh = _ld(dh, "dh", shape, dtype, dev)
-    if dx is None and p > 0:
-        dx = torch.empty(shape, dtype=dtype, device=dy.device)
-    if dx is not None:
-        px, ld_x = dx.data_ptr(), _ld(dx, "dx", shape, dtype, dev)
-    if weights and dgamma is None:
-        dgamma = torch.empty((cols,), dtype=torch.float32, device=dy.device)
-    if weights and dbeta is None and kind == NORM_LAYER:
-        dbeta = torch.empty((cols,), dtype=torch.float32, device=dy.device)
-    if dgamma is not None:
-        pdg = _vector(dgamma, "dgamma", cols, torch.float32, dev)
-    if dbeta is not None:
-        pdb = _vector(dbeta, "dbeta", cols, torch.float32, dev)
-    if workspace is None and (pdg or pdb):
-        wbytes = lib().fp4q_norm_grad_workspace_bytes(rows, cols)
-        if wbytes:
-            workspace = torch.empty((wbytes,), dtype=torch.uint8, device=dy.device)
-            pw = workspace.data_ptr()
-            if stream is not None:  # freed here, on the current stream, while `stream` may still use it
-                workspace.record_stream(stream)
-    elif workspace is not None:
-        if workspace.get_device() != dev or not workspace.is_contiguous():
-            raise ValueError("workspace must be a contiguous tensor on dy's device")
-        pw, wbytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
-    if gamma is not None:
-        pg, wt = _weight(gamma, "gamma", cols, dev)
-    if mean is not None:
-        pm = _vector(mean, "mean", rows, torch.float32, dev)
-    ps = _vector(rstd, "rstd", rows, torch.float32, dev)
-    status = lib().fp4_norm_grad(dy.data_ptr(), rows, cols, ld_dy, kt, h.data_ptr(), ld_h, pr, ld_r, kind, pg, wt, pm,
-                                 ps, p, seed, stream_id, dh.data_ptr(), ld_dh, px, ld_x, pdg, pdb, pw, wbytes,
-                                 _row_stream(stream, dev))
-    if status:
-        raise Fp4qError("fp4_norm_grad", status)
-    return _new(NormGrad, (dh, dx, dgamma, dbeta))
+    if workspace is None and stream is not None and (weights or dgamma is not None or dbeta is not None):
+        # freed here, on the current stream, while `stream` may still use it
+        workspace = torch.empty((lib().fp4q_norm_grad_workspace_bytes(*dy.shape),), dtype=torch.uint8, device=dy.device)
+        workspace.record_stream(stream)
+    return _new(NormGrad, _rows().norm_grad(dy, h, gamma, kind, mean, rstd, dres, p, seed, stream_id, weights, dh, dx,
+                                            dgamma, dbeta, workspace, stream))
 
 
 def fp4_swiglu_grad_bf16(dh: torch.Tensor, c: torch.Tensor, *, pair: int = 32, want_h: bool = False,
@@ -654,37 +542,7 @@ def fp4_swiglu_grad_bf16(dh: torch.Tensor, c: torch.Tensor, *, pair: int = 32, w
     """The gradient of fp4_swiglu_bf16: (dc, h) from dh [M x F] and the bf16
     C [M x >= 2F] whose columns interleave gate and up in groups of `pair`;
     h (with `want_h`) is the forward's output again. dc may be c, h may be dh."""
-    shape, ld_dh, _, kind, dev = _first(dh, "dh")
-    M, f = shape
-    cs, ldc, _, ck, cd = _first(c, "c")
-    if kind != OUT_BF16 or ck != OUT_BF16 or cd != dev or cs[0] != M or cs[1] < 2 * f:
-        raise ValueError(f"dh must be bf16 and c a bf16 [{M} x >= {2 * f}] tensor on its device")
-    if dc is None:
-        dc = torch.empty((M, 2 * f), dtype=torch.bfloat16, device=c.device)
-    os, ld_dc, _, ok, od = _first(dc, "dc")
-    if ok != OUT_BF16 or od != dev or os[0] != M or os[1] < 2 * f:
-        raise ValueError(f"dc must be a bf16 [{M} x >= {2 * f}] tensor on dh's device")
-    ph, ldh = None, 0
-    if h is None and want_h:
-        h = torch.empty((M, f), dtype=torch.bfloat16, device=c.device)
-    if h is not None:
-        ph, ldh = h.data_ptr(), _ld(h, "h", shape, torch.bfloat16, dev)
-    status = lib().fp4_swiglu_grad_bf16(dh.data_ptr(), ld_dh, c.data_ptr(), M, f, ldc, pair, dc.data_ptr(), ld_dc, ph,
-                                        ldh, _row_stream(stream, dev))
-    if status:
-        raise Fp4qError("fp4_swiglu_grad_bf16", status)
-    return dc, h
-
-
-def _heads(t: torch.Tensor, name: str, shape: torch.Size) -> Tuple[int, int]:
-    """(token stride, head stride) of a [tokens, heads, dim] view."""
-    n, heads, dim = shape
-    token, head, one = t.stride()
-    if one != 1 and dim > 1:
-        raise ValueError(f"{name} must have unit stride along dim")
-    if heads <= 1:
-        head = dim
-    return (token if n > 1 else max(1, heads) * head), head
+    return _rows().swiglu_grad(dh, c, pair, want_h, dc, h, stream)
 
 
 def fp4_rotary(x: torch.Tensor, positions: torch.Tensor, inv_freq: torch.Tensor, *, style: int = ROTARY_HALF,
@@ -694,24 +552,7 @@ def fp4_rotary(x: torch.Tensor, positions: torch.Tensor, inv_freq: torch.Tensor,
     strides, so a slice of a fused QKV output serves): pair i of each head
     turns by positions[t] * inv_freq[i], the first 2 len(inv_freq) elements
     of the head taking part. `inverse` turns back: the gradient. y may be x."""
-    shape, kind, dev = x.shape, _TYPES.get(x.dtype), x.get_device()
-    if kind is None or len(shape) != 3:
-        raise ValueError("x must be a [tokens, heads, dim] fp32 or bf16 tensor")
-    xt, xh = _heads(x, "x", shape)
-    if y is None:
-        y = torch.empty(shape, dtype=x.dtype, device=x.device)
-    elif y.shape != shape or y.dtype is not x.dtype or y.get_device() != dev:
-        raise ValueError(f"y must be a {tuple(shape)} {x.dtype} tensor on x's device")
-    yt, yh = _heads(y, "y", shape)
-    bits = 64 if positions.dtype is torch.int64 else 32
-    pos = _vector(positions, "positions", shape[0], torch.int64 if bits == 64 else torch.int32, dev)
-    pairs = inv_freq.numel()
-    status = lib().fp4_rotary(x.data_ptr(), shape[0], shape[1], shape[2], xt, xh, kind, pos, bits,
-                              _vector(inv_freq, "inv_freq", pairs, torch.float32, dev), 2 * pairs, style,
-                              1 if inverse else 0, scale, y.data_ptr(), yt, yh, _row_stream(stream, dev))
-    if status:
-        raise Fp4qError("fp4_rotary", status)
-    return y
+    return _rows().rotary(x, positions, inv_freq, style, scale, inverse, y, stream)
 
 
 def rotary_frequencies(rot: int, base: float = 10000.0, *, factor: float = 1.0, method: str = "none",

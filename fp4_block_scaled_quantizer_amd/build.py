@@ -1,4 +1,5 @@
-"""Build ``libfp4q.so`` (hand-written HIP for gfx950) in-tree with hipcc.
+"""Build ``libfp4q.so`` (hand-written HIP for gfx950) in-tree with hipcc, and
+``_row_calls.so``, the binding's compiled argument marshalling (host C++).
 
 Every source is compiled for gfx950 only, with FMA contraction off (the
 quantizers' binary32 steps must round exactly as written), packed-fp32
@@ -11,6 +12,7 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
@@ -34,6 +36,9 @@ HIPCC_FLAGS = [
 ]
 
 
+ROW_CALLS_OUT = os.path.join(HERE, "_row_calls.so")
+
+
 def hipcc() -> str:
     for cand in (shutil.which("hipcc"), "/opt/rocm/bin/hipcc"):
         if cand and os.path.exists(cand):
@@ -52,10 +57,30 @@ def _compile(src: str, verbose: bool) -> str:
     return obj
 
 
+def _row_calls(verbose: bool) -> None:
+    import torch
+    from torch.utils import cpp_extension
+
+    libs = os.path.join(os.path.dirname(torch.__file__), "lib")
+    includes = [sysconfig.get_paths()["include"], *cpp_extension.include_paths()]
+    tmp = ROW_CALLS_OUT + ".tmp"
+    cmd = [shutil.which("g++") or "g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden", "-Wall",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", *(f"-I{i}" for i in includes),
+           os.path.join(CSRC, "row_calls.cpp"), "-o", tmp, f"-L{libs}", "-ltorch_python", "-ltorch_cpu", "-lc10"]
+    if verbose:
+        print(" ".join(cmd), flush=True)
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed on row_calls.cpp:\n{r.stderr}")
+    os.replace(tmp, ROW_CALLS_OUT)
+
+
 def build(verbose: bool = False) -> str:
     os.makedirs(BUILD_DIR, exist_ok=True)
-    with cf.ThreadPoolExecutor(max_workers=min(4, len(SOURCES))) as ex:
+    with cf.ThreadPoolExecutor(max_workers=min(4, len(SOURCES) + 1)) as ex:
+        rows = ex.submit(_row_calls, verbose)
         objs = list(ex.map(lambda s: _compile(s, verbose), SOURCES))
+        rows.result()
     tmp = OUT + ".tmp"
     cmd = [hipcc(), "--offload-arch=gfx950", "-shared", "-fPIC", *objs, "-o", tmp]
     if verbose:

@@ -481,3 +481,27 @@ def test_side_stream_and_graph():
         got = [t.clone() for t in out]
         assert all(torch.equal(a, b) for a, b in zip(got, step())), k
         torch.cuda.synchronize()
+
+
+def test_refusals_reach_the_caller():
+    dev = device()
+    announce("row operators' refusals through the binding (nothing is launched)")
+    x = torch.zeros((4, 64), dtype=BF, device=dev)
+    v = torch.zeros((4,), device=dev)
+    for call, status in ((lambda: B.fp4_dropout(x, 1.5, seed=1), B.EINVAL), (lambda: B.fp4_norm(x, kind=7), B.EINVAL),
+                         (lambda: B.fp4_norm(x, kind=B.NORM_RMS, mean=v), B.EINVAL),
+                         (lambda: B.fp4_norm_grad(x, x, rstd=v), B.EINVAL),  # a layer norm without its means
+                         (lambda: B.fp4_swiglu_grad_bf16(x, torch.zeros((4, 128), dtype=BF, device=dev), pair=12), B.ESHAPE),
+                         (lambda: B.fp4_rotary(x[:, None], torch.zeros((4,), dtype=torch.int32, device=dev),
+                                               torch.zeros((40,), device=dev)), B.ESHAPE)):
+        with pytest.raises(B.Fp4qError) as e:
+            call()
+        assert e.value.status == status
+    for call in (lambda: B.fp4_dropout(x, 0.1, seed=1, y=x.cpu()), lambda: B.fp4_dropout(x, 0.1, seed=1, residual=x[:3]),
+                 lambda: B.fp4_norm(x, v), lambda: B.fp4_norm_grad(x, x, rstd=v.double()),
+                 lambda: B.fp4_rotary(x[:, None], v, v)):
+        with pytest.raises(ValueError):
+            call()
+    with pytest.raises(TypeError):
+        B.fp4_dropout(x, "half", seed=1)
+    torch.cuda.synchronize()
