@@ -93,16 +93,15 @@ __device__ __forceinline__ void weights_now(const void *w, bool bf16, const Span
     }
 }
 
-// Sum over the `waves` waves (at most 16) of a row that starts at wave
-// `first` of the workgroup, through LDS (`slot`: one float per wave, of its
-// own for each sum of a row).  Every thread of the workgroup must call it.
-__device__ __forceinline__ float row_sum(float v, float *slot, uint32_t wave, uint32_t first, uint32_t waves)
+// Sum over the `waves` waves (at most 16) of a workgroup, through LDS
+// (`slot`: a float per wave, for this sum alone).  Every thread must call it.
+__device__ __forceinline__ float row_sum(float v, float *slot, uint32_t wave, uint32_t waves)
 {
     v = wave_sum(v);
     const uint32_t lane = threadIdx.x & 63u;
     if (lane == 0) slot[wave] = v;
     __syncthreads();
-    v = lane < waves ? slot[first + lane] : 0.0f;
+    v = lane < waves ? slot[lane] : 0.0f;
     return lane_value(sum16(v), 15);
 }
 
@@ -168,7 +167,7 @@ __global__ __launch_bounds__(kWave ? 256 : 1024) void norm_kernel(const NormArgs
     const uint32_t tpr = kWave ? 64u : blockDim.x, t = kWave ? threadIdx.x & 63u : threadIdx.x;
     const uint32_t cols = (uint32_t)a.cols, waves = blockDim.x >> 6;
     const uint32_t wave = (uint32_t)__builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));  // rows in scalar registers
-    const auto sum_of = [&](float v, float *slot) { return kWave ? wave_sum(v) : row_sum(v, slot, wave, 0, waves); };
+    const auto sum_of = [&](float v, float *slot) { return kWave ? wave_sum(v) : row_sum(v, slot, wave, waves); };
     const float inv_n = 1.0f / (float)cols;
     // whether each lane of the wave has a full chunk of its own in place i
     const auto whole = [&](int i) { return (i * tpr + (kWave ? 64u : wave * 64u + 64u)) * 8u <= cols; };
@@ -336,6 +335,7 @@ void pick_norm(const NormArgs &a, const Dropout &d, hipStream_t st)
 // ------------------------------------------------------------------ gradient
 
 constexpr int kMaxParts = 256;  // workgroups that keep weight sums: one per compute unit
+
 // The weight sums of 64 columns over every `nslices`-th run of 128 rows, by
 // a workgroup of 1024 threads: eight lanes side by side take the columns,
 // the other 128 the rows.  They need the rows' statistics but not their
@@ -416,7 +416,8 @@ __global__ __launch_bounds__(1024) void norm_grad_kernel(const NormGradArgs a, c
     __shared__ __attribute__((aligned(16))) float keep[kSums == kNone ? 1 : (kSums == kInLds ? 2 : 1) * kC * 8 * 1024];
     const uint32_t wave = (uint32_t)__builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));  // rows in scalar registers
     const uint32_t lane = threadIdx.x & 63u, cols = (uint32_t)a.cols;
-    const uint32_t g = (uint32_t)__builtin_amdgcn_readfirstlane((int)(wave / a.waves)), first = g * a.waves, tpr = a.waves * 64u, t = threadIdx.x - first * 64u;
+    const uint32_t g = (uint32_t)__builtin_amdgcn_readfirstlane((int)(wave / a.waves)), first = g * a.waves;
+    const uint32_t tpr = a.waves * 64u, t = threadIdx.x - first * 64u;
     const float inv_n = 1.0f / (float)cols;
     // wide rows read the weights again for each row rather than hold them
     constexpr bool kHoldW = kC <= 2;
@@ -456,7 +457,9 @@ __global__ __launch_bounds__(1024) void norm_grad_kernel(const NormGradArgs a, c
         for (int i = 0; i < kC; ++i) {
             load_chunk<T, kEdge, kStream<T>>(reinterpret_cast<const T *>(a.dy) + row * a.ld_dy, sp[i], cols, r.dy[i]);
             load_chunk<T, kEdge, kStream<T>>(reinterpret_cast<const T *>(a.h) + row * a.ld_h, sp[i], cols, r.h[i]);
-            if (kRes) load_chunk<T, kEdge, kStream<T>>(reinterpret_cast<const T *>(a.dres) + row * a.ld_dres, sp[i], cols, r.res[i]);
+            if (kRes)
+                load_chunk<T, kEdge, kStream<T>>(reinterpret_cast<const T *>(a.dres) + row * a.ld_dres, sp[i], cols,
+                                                 r.res[i]);
         }
         r.mean = means[row];
         r.rstd = a.rstd[row];
@@ -630,12 +633,17 @@ __global__ __launch_bounds__(1024) void norm_grad_kernel(const NormGradArgs a, c
     }
 }
 
-// The weight sums of rows too wide to keep them beside the rows' own work.
+// The weight sums by themselves: into the workspace in gridDim.y slices, or
+// as one slice into their place (parts null).
 template <typename T, Edge kEdge>
-__global__ __launch_bounds__(1024) void norm_weight_sums_kernel(const NormGradArgs a)
+__global__ __launch_bounds__(1024) void norm_weight_sums_kernel(const NormGradArgs a, float *parts, float *dgamma,
+                                                                float *dbeta)
 {
-    float *part = a.parts + (size_t)blockIdx.y * 2 * (uint32_t)a.cols;
-    weight_sums<T, kEdge>(a, blockIdx.x, blockIdx.y, gridDim.y, part, part + a.cols);
+    if (parts) {
+        dgamma = parts + (size_t)blockIdx.y * 2 * (uint32_t)a.cols;
+        dbeta = dgamma + (uint32_t)a.cols;
+    }
+    weight_sums<T, kEdge>(a, blockIdx.x, blockIdx.y, gridDim.y, dgamma, dbeta);
 }
 
 // out[which][col] = sum of the workgroups' parts.  64 columns of a workgroup
@@ -665,8 +673,9 @@ __global__ __launch_bounds__(1024) void norm_grad_weights_kernel(const float *__
 // calls, where a second launch costs more than the reading; a bf16 call
 // beside / in rows: 96 x 1024 4.3 / 7.9 us, 512 x 4096 10.1 / 12.7, 300 x
 // 7000 11.1 / 18.1, but 1000 x 1000 12.9 / 10.6 and 1024 x 4096 17.4 /
-// 15.8), or by a kernel of their own (kApart: rows too wide for a workgroup
-// to keep their sums).
+// 15.8), or by a kernel of their own before the rows' (kApart: rows too wide
+// for a workgroup to keep their sums; and in place of kBeside where the rows'
+// results overwrite what it reads).
 enum How { kNoSums, kInRows, kBeside, kApart };
 struct GradPlan {
     How sums;
@@ -723,22 +732,33 @@ template <typename T>
 void pick_norm_grad(const NormGradArgs &a, const Dropout &d, const GradPlan &g, float *dgamma, float *dbeta,
                     hipStream_t st)
 {
-    if (g.sums != kBeside && g.sums != kInRows) dgamma = dbeta = nullptr;  // not the row kernel's
-    if (g.chunks_per_thread == 4)
-        run_norm_grad<T, 4, kNone>(a, d, g.sums, dgamma, dbeta, st);
-    else if (g.sums != kInRows)
-        g.chunks_per_thread == 2 ? run_norm_grad<T, 2, kNone>(a, d, g.sums, dgamma, dbeta, st)
-                                 : run_norm_grad<T, 1, kNone>(a, d, g.sums, dgamma, dbeta, st);
-    else
-        g.chunks_per_thread == 2 ? run_norm_grad<T, 2, kInLds>(a, d, g.sums, dgamma, dbeta, st)
-                                 : run_norm_grad<T, 1, kInRegs>(a, d, g.sums, dgamma, dbeta, st);
-    if (g.sums == kApart) {
-        const dim3 grid((unsigned)((a.cols + 63) / 64), (unsigned)g.parts);
-        if (a.cols % 8)
-            hipLaunchKernelGGL((norm_weight_sums_kernel<T, kRagged>), grid, dim3(1024), 0, st, a);
-        else
-            hipLaunchKernelGGL((norm_weight_sums_kernel<T, kWhole>), grid, dim3(1024), 0, st, a);
+    How how = g.sums;
+    const bool overwritten = (a.dh && (a.dh == a.dy || a.dh == a.h)) || (a.dx && (a.dx == a.dy || a.dx == a.h));
+    if (how == kApart || (how == kBeside && overwritten)) {
+        float *parts = how == kApart ? a.parts : nullptr;
+        const dim3 grid((unsigned)((a.cols + 63) / 64), how == kApart ? (unsigned)g.parts : 1u);
+        switch (edge_of(a.cols)) {
+        case kWhole:
+            hipLaunchKernelGGL((norm_weight_sums_kernel<T, kWhole>), grid, dim3(1024), 0, st, a, parts, dgamma, dbeta);
+            break;
+        case kRagged:
+            hipLaunchKernelGGL((norm_weight_sums_kernel<T, kRagged>), grid, dim3(1024), 0, st, a, parts, dgamma, dbeta);
+            break;
+        case kTiny:
+            hipLaunchKernelGGL((norm_weight_sums_kernel<T, kTiny>), grid, dim3(1024), 0, st, a, parts, dgamma, dbeta);
+            break;
+        }
+        how = kNoSums;
     }
+    if (how == kNoSums) dgamma = dbeta = nullptr;  // not the rows' kernel's
+    if (g.chunks_per_thread == 4)
+        run_norm_grad<T, 4, kNone>(a, d, how, dgamma, dbeta, st);
+    else if (how != kInRows)
+        g.chunks_per_thread == 2 ? run_norm_grad<T, 2, kNone>(a, d, how, dgamma, dbeta, st)
+                                 : run_norm_grad<T, 1, kNone>(a, d, how, dgamma, dbeta, st);
+    else
+        g.chunks_per_thread == 2 ? run_norm_grad<T, 2, kInLds>(a, d, how, dgamma, dbeta, st)
+                                 : run_norm_grad<T, 1, kInRegs>(a, d, how, dgamma, dbeta, st);
 }
 
 }  // namespace

@@ -212,8 +212,8 @@ __device__ __forceinline__ Span span_of(uint32_t c, uint32_t cols)
 template <typename T>
 __device__ __forceinline__ T *in_row(T *row, uint32_t from)
 {
-    typedef typename std::conditional<std::is_const<T>::value, const char, char>::type byte;
-    return reinterpret_cast<T *>(reinterpret_cast<byte *>(row) + (uint32_t)(from * (uint32_t)sizeof(T)));
+    typedef typename std::conditional<std::is_const<T>::value, const char, char>::type Byte;
+    return reinterpret_cast<T *>(reinterpret_cast<Byte *>(row) + (uint32_t)(from * (uint32_t)sizeof(T)));
 }
 template <typename T, Edge kEdge, bool kNt = false>
 __device__ __forceinline__ void load_chunk(const T *row, const Span &s, uint32_t cols, Chunk<T> &q)
@@ -237,14 +237,14 @@ __device__ __forceinline__ void store_chunk(T *row, const Span &s, const Chunk<T
     }
 }
 
-// Sum over the 64 lanes of a wave, the same on every lane: DPP shifts inside
-// the rows of 16, then two broadcasts across rows (a fixed order, no LDS).
+// Sums by DPP, in a fixed order and without LDS: shifts inside the rows of 16
+// lanes, then for the whole wave two broadcasts across rows.
 template <int kCtrl, int kRowMask>
 __device__ __forceinline__ float dpp_add(float v)
 {
     return v + u2f((uint32_t)__builtin_amdgcn_update_dpp(0, (int)f2u(v), kCtrl, kRowMask, 0xF, true));
 }
-// ... inside each row of 16 lanes: the row's lane 15 holds its sum
+// The sum of each row of 16 lanes, in its lane 15.
 __device__ __forceinline__ float sum16(float v)
 {
     v = dpp_add<0x111, 0xF>(v);  // row_shr:1
@@ -256,6 +256,7 @@ __device__ __forceinline__ float lane_value(float v, int lane)
 {
     return u2f((uint32_t)__builtin_amdgcn_readlane((int)f2u(v), lane));
 }
+// The sum of all 64 lanes, on every lane.
 __device__ __forceinline__ float wave_sum(float v)
 {
     v = sum16(v);

@@ -272,6 +272,27 @@ def test_norm_grad(rows, cols, dtype, layer):
                 assert q.dgamma is None and q.dbeta is None
 
 
+@pytest.mark.parametrize("rows,cols", [(50, 5), (300, 1000), (700, 2048), (1500, 1032), (300, 9000), (260, 20000)])
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_norm_grad_in_place_with_weights(rows, cols, dtype):
+    """dh or dx in the place of an input that the weight gradients are made
+    from: every way of making them, small, in rows, and wide."""
+    dev = device()
+    announce(f"norm gradient in place with weights {rows}x{cols} {dtype}")
+    t = [draw((rows, cols), i, dtype).to(dev) for i in range(3)]  # dy, h, dres
+    g = (1 + draw((cols,), 4, F32, 0.2)).to(dev)
+    f = B.fp4_norm(t[1], g, save=True)
+    args = dict(mean=f.mean, rstd=f.rstd, p=0.1, seed=3)
+    want = B.fp4_norm_grad(t[0], t[1], g, dres=t[2], **args)
+    for i in range(3):
+        for j in range(3):
+            if i != j:
+                u = [v.clone() for v in t]
+                o = B.fp4_norm_grad(u[0], u[1], g, dres=u[2], dh=u[i], dx=u[j], **args)
+                for a, b, what in zip(o, want, ("dh", "dx", "dgamma", "dbeta")):
+                    same(a, b, f"{what}, dh in place {i}, dx in place {j}")
+
+
 def test_norm_grad_no_rows():
     dev = device()
     announce("norm gradient of no rows")
