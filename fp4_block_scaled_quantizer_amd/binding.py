@@ -528,10 +528,6 @@ def fp4_norm_grad(dy: torch.Tensor, h: torch.Tensor, gamma: Optional[torch.Tenso
     reaches them along the residual stream), dx of fp4_norm's x where p > 0
     (dx equals dh otherwise and is None), and with `weights` dgamma and, for
     NORM_LAYER, dbeta in fp32. dh and dx may each be dy, h or dres."""
-    if workspace is None and stream is not None and (weights or dgamma is not None or dbeta is not None):
-        # freed here, on the current stream, while `stream` may still use it
-        workspace = torch.empty((lib().fp4q_norm_grad_workspace_bytes(*dy.shape),), dtype=torch.uint8, device=dy.device)
-        workspace.record_stream(stream)
     return _new(NormGrad, _rows().norm_grad(dy, h, gamma, kind, mean, rstd, dres, p, seed, stream_id, weights, dh, dx,
                                             dgamma, dbeta, workspace, stream))
 
@@ -567,8 +563,10 @@ def rotary_frequencies(rot: int, base: float = 10000.0, *, factor: float = 1.0, 
                 slow_turns divided by factor, above fast_turns kept, linear in
                 the turns between; scale = 1 + 0.1 ln factor.
     A layout of constants made once, like pair_gate_up."""
-    if rot < 2 or rot % 2 or factor < 1 or method not in ("none", "linear", "base", "turns"):
-        raise ValueError("rot must be even and >= 2, factor >= 1, method none, linear, base or turns")
+    if (rot < 2 or rot % 2 or not factor >= 1 or not fast_turns > slow_turns
+            or method not in ("none", "linear", "base", "turns")):
+        raise ValueError("rot must be even and >= 2, factor >= 1, fast_turns > slow_turns, "
+                         "method none, linear, base or turns")
     if method == "base" and rot > 2:
         base = base * factor ** (rot / (rot - 2))
     freq = base ** (-torch.arange(0, rot, 2, dtype=torch.float64) / rot)

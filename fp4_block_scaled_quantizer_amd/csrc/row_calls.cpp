@@ -183,6 +183,18 @@ void *stream_of(PyObject *stream, const at::Tensor &t)
     return s;
 }
 
+// Memory made here for a call on a `stream` of the user's, and let go of when
+// the call returns: not given out again before that stream is through with it.
+void used_on(PyObject *stream, const at::Tensor &t)
+{
+    if (stream == Py_None || !t.defined()) return;
+    PyObject *o = THPVariable_Wrap(t);
+    PyObject *r = o ? PyObject_CallMethod(o, "record_stream", "O", stream) : nullptr;
+    Py_XDECREF(o);
+    if (!r) throw PythonError();
+    Py_DECREF(r);
+}
+
 void done(const char *fn, fp4q_status status)
 {
     if (status == FP4Q_OK) return;
@@ -270,6 +282,7 @@ PyObject *norm_grad(PyObject *const *a)
     const void *gamma = x.weight(a[GAMMA], "gamma", wt);
     const float *pm = x.floats(a[MEAN], "mean", x.rows, false, mean);
     const float *ps = static_cast<float *>(x.vector(tensor(a[RSTD], "rstd"), "rstd", x.rows, at::kFloat));
+    void *st = stream_of(a[STREAM], x.t);
     size_t bytes = 0;
     if (const at::Tensor *w = tensor_or_null(a[WORKSPACE], "workspace")) {
         if (w->device() != x.t.device() || !w->is_contiguous())
@@ -279,8 +292,8 @@ PyObject *norm_grad(PyObject *const *a)
     } else if (pg || pb) {
         bytes = lib.norm_grad_workspace(x.rows, x.cols);
         if (bytes) ws = at::empty({(int64_t)bytes}, x.t.options().dtype(at::kByte));
+        used_on(a[STREAM], ws);
     }
-    void *st = stream_of(a[STREAM], x.t);
     done("fp4_norm_grad",
          lib.norm_grad(my.p, x.rows, x.cols, my.ld, x.type, mh.p, mh.ld, mr.p, mr.ld, kind, gamma,
                        wt < 0 ? FP4Q_OUT_F32 : wt, pm, ps, (float)p, bits64(a[SEED]), (uint32_t)bits64(a[STREAM_ID]),

@@ -504,6 +504,36 @@ def test_side_stream_and_graph():
         torch.cuda.synchronize()
 
 
+@pytest.mark.parametrize("rows", [100, 1200])
+def test_named_stream(rows):
+    """`stream`: every operator on it, its outputs, workspace (the larger size
+    needs one) and results as on the current one."""
+    dev = device()
+    announce(f"row operators on a stream of their own, {rows} rows")
+    side, cols = torch.cuda.Stream(), 1024
+    x, r, dy = (draw((rows, cols), i, BF).to(dev) for i in range(3))
+    c = draw((rows, 2 * cols), 3, BF).to(dev)
+    gamma = (1 + draw((cols,), 4, F32, 0.2)).to(dev)
+    pos = torch.arange(rows, device=dev)
+    freq = B.rotary_frequencies(64, device=dev)[0]
+
+    def step(**s):
+        d = B.fp4_dropout(x, 0.2, seed=3, residual=r, **s)
+        f = B.fp4_norm(x, gamma, residual=r, p=0.2, seed=4, save=True, mx=True, **s)
+        g = B.fp4_norm_grad(dy, f.h, gamma, mean=f.mean, rstd=f.rstd, p=0.2, seed=4, **s)
+        return [d, *f, *g, *B.fp4_swiglu_grad_bf16(dy, c, want_h=True, **s),
+                B.fp4_rotary(x.view(rows, 8, 128), pos, freq, **s)]
+
+    want = step()
+    torch.cuda.synchronize()
+    got = step(stream=side)
+    side.synchronize()
+    for i, (a, b) in enumerate(zip(got, want)):
+        assert torch.equal(a, b), f"output {i}"
+    with pytest.raises(ValueError, match="2-D"):
+        B.fp4_norm_grad(dy[0], x[0], rstd=gamma, stream=side)
+
+
 def test_refusals_reach_the_caller():
     dev = device()
     announce("row operators' refusals through the binding (nothing is launched)")

@@ -150,6 +150,19 @@ def test_binding_refusals():
         B.fp4_dropout(x, 0.1, seed=1)
 
 
+def test_norm_grad_refusals_with_a_stream():
+    x, one = torch.zeros((4, 64)), torch.ones(4)
+    with pytest.raises(ValueError, match="2-D"):
+        B.fp4_norm_grad(x[0], x[0], rstd=one, stream=object())
+    with pytest.raises(ValueError, match="current GPU"):
+        B.fp4_norm_grad(x, x, rstd=one, mean=one, stream=object())
+
+
+def test_rotary_frequencies_refuses_an_empty_ramp():
+    with pytest.raises(ValueError):
+        B.rotary_frequencies(64, factor=4, method="turns", slow_turns=8, fast_turns=8)
+
+
 def test_reference_draws_the_oracles_philox():
     k, r = np.meshgrid(np.arange(5), np.arange(7))
     w = R.philox_words(k, r, 9, 1, 0x123456789ABCDEF)
