@@ -334,7 +334,7 @@ void pick_norm(const NormArgs &a, const Dropout &d, hipStream_t st)
 
 // ------------------------------------------------------------------ gradient
 
-constexpr int kMaxParts = 256;  // workgroups that keep weight sums: one per compute unit
+constexpr int kMaxParts = 256;  // workgroups that walk the rows (and keep weight sums): one per compute unit
 
 // The weight sums of 64 columns over every `nslices`-th run of 128 rows, by
 // a workgroup of 1024 threads: eight lanes side by side take the columns,
@@ -397,8 +397,10 @@ __device__ __forceinline__ void weight_sums(const NormGradArgs &a, uint32_t bloc
 // the next ones before it works on those it has (kAhead).  Weight sums:
 // kInRegs and kInLds, each workgroup keeps those of its rows and leaves them
 // in the workspace; kNone, where they are asked for, the workgroups from
-// a.row_blocks on take them from all rows (weight_sums), 64 columns each.
-enum Sums { kNone, kInRegs, kInLds };
+// a.row_blocks on take them from all rows (weight_sums), 64 columns each, and
+// a workgroup ends with its first rows; kWalk has no sums and walks the rows
+// like kInRegs.
+enum Sums { kNone, kWalk, kInRegs, kInLds };
 template <typename T, int kC, bool kAhead, Sums kSums, bool kRes, bool kDx, Edge kEdge>
 __global__ __launch_bounds__(1024) void norm_grad_kernel(const NormGradArgs a, const Dropout d, float *dgamma,
                                                          float *dbeta)
@@ -413,7 +415,7 @@ __global__ __launch_bounds__(1024) void norm_grad_kernel(const NormGradArgs a, c
     __shared__ float red[2][2][16];
     // the sums in LDS, or folded there over the groups at the end; a
     // thread's eight of a chunk are two groups of four, each wave-contiguous
-    __shared__ __attribute__((aligned(16))) float keep[kSums == kNone ? 1 : (kSums == kInLds ? 2 : 1) * kC * 8 * 1024];
+    __shared__ __attribute__((aligned(16))) float keep[kSums <= kWalk ? 1 : (kSums == kInLds ? 2 : 1) * kC * 8 * 1024];
     const uint32_t wave = (uint32_t)__builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));  // rows in scalar registers
     const uint32_t lane = threadIdx.x & 63u, cols = (uint32_t)a.cols;
     const uint32_t g = (uint32_t)__builtin_amdgcn_readfirstlane((int)(wave / a.waves)), first = g * a.waves;
@@ -573,7 +575,7 @@ __global__ __launch_bounds__(1024) void norm_grad_kernel(const NormGradArgs a, c
     // a row is done, before the next one has to be there
     Row one, two;
     fetch(base0, one);
-    if constexpr (kSums == kNone) {  // no sums to carry: a workgroup ends with its rows
+    if constexpr (kSums == kNone) {
         work(base0, one);
         return;
     }
@@ -589,7 +591,7 @@ __global__ __launch_bounds__(1024) void norm_grad_kernel(const NormGradArgs a, c
             fetch(base + stride, one);
         }
     }
-    if constexpr (kSums != kNone) {  // parts[workgroup][gamma, beta][cols]
+    if constexpr (kSums > kWalk) {  // parts[workgroup][gamma, beta][cols]
 #pragma unroll
         for (int which = 0; which < 2; ++which) {
             if (which == 1 && !dbeta) break;
@@ -675,8 +677,12 @@ __global__ __launch_bounds__(1024) void norm_grad_weights_kernel(const float *__
 // 7000 11.1 / 18.1, but 1000 x 1000 12.9 / 10.6 and 1024 x 4096 17.4 /
 // 15.8), or by a kernel of their own before the rows' (kApart: rows too wide
 // for a workgroup to keep their sums; and in place of kBeside where the rows'
-// results overwrite what it reads).
-enum How { kNoSums, kInRows, kBeside, kApart };
+// results overwrite what it reads).  Without weight sums a workgroup per
+// compute unit walks the rows as for kInRows (kRowsWalked), whose loads then
+// never pause: 8192 x 4096 34.9 us, a workgroup to every two rows 47.5 (2047
+// x 14336 binary32 68 / 75, 65536 x 128 19.4 / 34.5); no difference up to
+// 2^21 elements, where the latter has the shorter code (kNoSums).
+enum How { kNoSums, kRowsWalked, kInRows, kBeside, kApart };
 struct GradPlan {
     How sums;
     int chunks_per_thread;
@@ -692,8 +698,14 @@ GradPlan grad_plan(int64_t rows, int64_t cols, bool sums)
     g.waves = (uint32_t)((waves1 + g.chunks_per_thread - 1) / g.chunks_per_thread);
     g.groups = 16 / g.waves;
     const int64_t need = (rows + g.groups - 1) / g.groups;
-    g.sums = !sums ? kNoSums : g.chunks_per_thread == 4 ? kApart : rows <= 768 && rows * cols <= (3 << 20) ? kBeside : kInRows;
-    g.row_blocks = g.sums == kInRows && need > kMaxParts ? kMaxParts : need;
+    const bool small = rows * cols <= (3 << 20);
+    if (g.chunks_per_thread == 4)
+        g.sums = sums ? kApart : kNoSums;
+    else if (sums)
+        g.sums = small && rows <= 768 ? kBeside : kInRows;
+    else
+        g.sums = small ? kNoSums : kRowsWalked;
+    g.row_blocks = (g.sums == kInRows || g.sums == kRowsWalked) && need > kMaxParts ? kMaxParts : need;
     const int64_t runs = (rows + 127) / 128;
     g.parts = g.sums == kInRows ? g.row_blocks : g.sums == kApart ? (runs < 4 ? runs : 4) : 0;
     return g;
@@ -751,14 +763,18 @@ void pick_norm_grad(const NormGradArgs &a, const Dropout &d, const GradPlan &g, 
         how = kNoSums;
     }
     if (how == kNoSums) dgamma = dbeta = nullptr;  // not the rows' kernel's
+    const bool two = g.chunks_per_thread == 2;
     if (g.chunks_per_thread == 4)
         run_norm_grad<T, 4, kNone>(a, d, how, dgamma, dbeta, st);
-    else if (how != kInRows)
-        g.chunks_per_thread == 2 ? run_norm_grad<T, 2, kNone>(a, d, how, dgamma, dbeta, st)
-                                 : run_norm_grad<T, 1, kNone>(a, d, how, dgamma, dbeta, st);
+    else if (how == kNoSums || how == kBeside)
+        two ? run_norm_grad<T, 2, kNone>(a, d, how, dgamma, dbeta, st)
+            : run_norm_grad<T, 1, kNone>(a, d, how, dgamma, dbeta, st);
+    else if (how == kRowsWalked)
+        two ? run_norm_grad<T, 2, kWalk>(a, d, how, dgamma, dbeta, st)
+            : run_norm_grad<T, 1, kWalk>(a, d, how, dgamma, dbeta, st);
     else
-        g.chunks_per_thread == 2 ? run_norm_grad<T, 2, kInLds>(a, d, how, dgamma, dbeta, st)
-                                 : run_norm_grad<T, 1, kInRegs>(a, d, how, dgamma, dbeta, st);
+        two ? run_norm_grad<T, 2, kInLds>(a, d, how, dgamma, dbeta, st)
+            : run_norm_grad<T, 1, kInRegs>(a, d, how, dgamma, dbeta, st);
 }
 
 }  // namespace

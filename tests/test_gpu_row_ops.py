@@ -293,6 +293,30 @@ def test_norm_grad_in_place_with_weights(rows, cols, dtype):
                     same(a, b, f"{what}, dh in place {i}, dx in place {j}")
 
 
+@pytest.mark.parametrize("rows,cols", [(650000, 5), (70001, 48), (3500, 1000), (1700, 2048), (1601, 2056), (400, 9000),
+                                       (257, 14336), (170, 20000)])
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_norm_grad_without_weight_gradients(rows, cols, dtype):
+    """Large calls without weight gradients: the rows' gradients are those of
+    the call with them, bit for bit, in place too."""
+    dev = device()
+    announce(f"norm gradient without weight gradients {rows}x{cols} {dtype}")
+    dy, h, dres = (draw((rows, cols), i, dtype).to(dev) for i in range(3))
+    g = (1 + draw((cols,), 4, F32, 0.2)).to(dev)
+    f = B.fp4_norm(h, g, save=True)
+    for res, p in ((None, 0.0), (dres, 0.1)):
+        args = dict(mean=f.mean, rstd=f.rstd, dres=res, p=p, seed=3)
+        want = B.fp4_norm_grad(dy, h, g, **args)
+        got = B.fp4_norm_grad(dy, h, g, weights=False, **args)
+        assert got.dgamma is None and got.dbeta is None
+        u = dy.clone()
+        B.fp4_norm_grad(u, h, g, weights=False, dh=u, **args)
+        same(got.dh, want.dh, "dh")
+        same(u, want.dh, "dh in place")
+        if p > 0:
+            same(got.dx, want.dx, "dx")
+
+
 def test_norm_grad_no_rows():
     dev = device()
     announce("norm gradient of no rows")
