@@ -11,10 +11,13 @@
 // centred values, so that a large mean costs no precision), and each input
 // is read and each output written once: HBM-bound.  One workgroup per row, a
 // chunk of eight elements per thread (two above 4096 columns, four above
-// 16384; at 1024 and below a wave per row), many workgroups to a compute
-// unit, so that one row's loads run under another's sums and stores.
+// 16384; at 1024 and below a wave per row, at 256 half a wave and at 128, the
+// norms of single heads, a quarter), many workgroups to a compute unit, so
+// that one row's loads run under another's sums and stores.
 // Measured on rows that do not fit the caches, of a copy's 6.3 TB/s:
 //   8192 x 4096 bf16, layer norm, dropout, residual: 44.5 us, 6.0 TB/s;
+//   327680 x 128 bf16, layer norm: 30.0 us, 5.6 TB/s (a wave per row 80; 32768
+//   x 256: half a wave 9.1, a wave 12.6);
 //   1537 x 5003 binary32, layer norm: 13.4 us, 4.6 TB/s (all rows resident
 //   at once: the loads of all, then the stores of all);
 //   1 x 4096 bf16: 4.5 us a call, launch and latency.
@@ -30,7 +33,8 @@
 //   8192 x 4096 bf16, layer norm, dropout, dres: 63.9 us, 5.3 TB/s (59 us
 //   the rows, 5 the second kernel); 2047 x 14336 binary32: 77.9 us, 4.5 TB/s
 //   (eight rows to a compute unit, of which the first one's loads and the
-//   sums' 59 MB are not hidden); 96 x 1024: 4.6 us a call.
+//   sums' 59 MB are not hidden); 327680 x 128 bf16, dres: 64.0 us, 5.3 TB/s (a
+//   wave per row 94); 96 x 1024: 4.6 us a call.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -154,23 +158,30 @@ __device__ __forceinline__ void store_mx(const NormArgs &a, int64_t row, uint32_
     }
 }
 
-// kC chunks of eight elements per thread.  kWave: a wave has a row to itself
-// (four rows to a workgroup, no barriers); otherwise a workgroup of as many
-// waves as the row needs has it.
-template <typename T, bool kWave, int kC, bool kRes, Edge kEdge, bool kMx>
-__global__ __launch_bounds__(kWave ? 256 : 1024) void norm_kernel(const NormArgs a, const Dropout d,
+// kC chunks of eight elements per thread.  kLanes > 0: that many lanes of a
+// wave have a row to themselves (256 / kLanes rows to a workgroup, no
+// barriers); 0: a workgroup of as many waves as the row needs has it.
+template <typename T, int kLanes, int kC, bool kRes, Edge kEdge, bool kMx>
+__global__ __launch_bounds__(kLanes ? 256 : 1024) void norm_kernel(const NormArgs a, const Dropout d,
                                                                   const void *__restrict__ gamma,
                                                                   const void *__restrict__ beta)
 {
     __shared__ float red[2][16];
     constexpr bool kEarlyW = kC == 1;
-    const uint32_t tpr = kWave ? 64u : blockDim.x, t = kWave ? threadIdx.x & 63u : threadIdx.x;
+    constexpr bool kGroup = kLanes == 0;
+    constexpr int kRows = kGroup ? 1 : 256 / kLanes;  // of a workgroup
+    const uint32_t tpr = kGroup ? blockDim.x : kLanes, t = kGroup ? threadIdx.x : threadIdx.x % tpr;
     const uint32_t cols = (uint32_t)a.cols, waves = blockDim.x >> 6;
     const uint32_t wave = (uint32_t)__builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));  // rows in scalar registers
-    const auto sum_of = [&](float v, float *slot) { return kWave ? wave_sum(v) : row_sum(v, slot, wave, waves); };
+    const auto sum_of = [&](float v, float *slot) {
+        if constexpr (kGroup)
+            return row_sum(v, slot, wave, waves);
+        else
+            return lanes_sum<kLanes>(v);
+    };
     const float inv_n = 1.0f / (float)cols;
     // whether each lane of the wave has a full chunk of its own in place i
-    const auto whole = [&](int i) { return (i * tpr + (kWave ? 64u : wave * 64u + 64u)) * 8u <= cols; };
+    const auto whole = [&](int i) { return (i * tpr + (kGroup ? wave * 64u + 64u : tpr)) * 8u <= cols; };
     // no loop over rows: what a loop would keep ready for its next turn
     // (Philox's keys among it) spills
     int64_t block = (int64_t)blockIdx.y * gridDim.x + blockIdx.x;
@@ -178,10 +189,10 @@ __global__ __launch_bounds__(kWave ? 256 : 1024) void norm_kernel(const NormArgs
         // 32 rows share the tiled operand's cache lines, 16 bytes each:
         // workgroup b runs on XCD b mod 8, and of 256 rows each XCD gets 32
         // together, so that its L2 puts the lines together
-        constexpr int64_t kRun = kWave ? 8 : 32;
+        constexpr int64_t kRun = 32 / kRows;
         block = block / (8 * kRun) * (8 * kRun) + block % 8 * kRun + block / 8 % kRun;
     }
-    const int64_t row = kWave ? block * 4 + wave : block;
+    const int64_t row = block * kRows + (kGroup ? 0u : kLanes == 64 ? wave : threadIdx.x / tpr);
     if (row >= a.rows_out) return;
     if (kMx && row >= a.rows) {  // tiled output's padding rows: zero codes and scales
         Chunk<bf16_t> z;
@@ -291,23 +302,24 @@ __global__ __launch_bounds__(kWave ? 256 : 1024) void norm_kernel(const NormArgs
     }
 }
 
-template <typename T, bool kWave, int kC, bool kMx>
+template <typename T, int kLanes, int kC, bool kMx>
 void run_norm(const NormArgs &a, const Dropout &d, hipStream_t st)
 {
     const int64_t chunks = (a.cols + 7) / 8, rows = kMx && a.tiled ? (a.rows_out + 255) / 256 * 256 : a.rows_out;
-    const int64_t need = kWave ? (rows + 3) / 4 : rows;
+    constexpr int kRows = kLanes ? 256 / kLanes : 1;
+    const int64_t need = (rows + kRows - 1) / kRows;
     const int64_t wide = 1 << 20;  // a launch's threads along x are below 2^32
     const dim3 grid((unsigned)(need < wide ? need : wide), (unsigned)((need + wide - 1) / wide));
-    const dim3 block(kWave ? 256 : (unsigned)((chunks + 64 * kC - 1) / (64 * kC) * 64));
+    const dim3 block(kLanes ? 256 : (unsigned)((chunks + 64 * kC - 1) / (64 * kC) * 64));
 #define FP4Q_NORM(EDGE)                                                                                           \
     do {                                                                                                          \
         if (a.residual)                                                                                           \
-            hipLaunchKernelGGL((norm_kernel<T, kWave, kC, true, EDGE, kMx>), grid, block, 0, st, a, d, a.gamma, a.beta);  \
+            hipLaunchKernelGGL((norm_kernel<T, kLanes, kC, true, EDGE, kMx>), grid, block, 0, st, a, d, a.gamma, a.beta);  \
         else                                                                                                      \
-            hipLaunchKernelGGL((norm_kernel<T, kWave, kC, false, EDGE, kMx>), grid, block, 0, st, a, d, a.gamma, a.beta); \
+            hipLaunchKernelGGL((norm_kernel<T, kLanes, kC, false, EDGE, kMx>), grid, block, 0, st, a, d, a.gamma, a.beta); \
     } while (0)
     const Edge edge = edge_of(a.cols);  // an operand's is kWhole, and only short rows are tiny
-    if constexpr (kWave && kC == 1 && !kMx) {
+    if constexpr (kLanes == 16 && !kMx) {
         if (edge == kTiny) FP4Q_NORM(kTiny);
     }
     if constexpr (!kMx) {
@@ -320,16 +332,20 @@ void run_norm(const NormArgs &a, const Dropout &d, hipStream_t st)
 template <typename T, bool kMx>
 void pick_norm(const NormArgs &a, const Dropout &d, hipStream_t st)
 {
-    if (a.cols <= 512)
-        run_norm<T, true, 1, kMx>(a, d, st);
+    if (a.cols <= 128)
+        run_norm<T, 16, 1, kMx>(a, d, st);
+    else if (a.cols <= 256)
+        run_norm<T, 32, 1, kMx>(a, d, st);
+    else if (a.cols <= 512)
+        run_norm<T, 64, 1, kMx>(a, d, st);
     else if (a.cols <= 1024)
-        run_norm<T, true, 2, kMx>(a, d, st);
+        run_norm<T, 64, 2, kMx>(a, d, st);
     else if (a.cols <= 4096)
-        run_norm<T, false, 1, kMx>(a, d, st);
+        run_norm<T, 0, 1, kMx>(a, d, st);
     else if (a.cols <= 16384)
-        run_norm<T, false, 2, kMx>(a, d, st);
+        run_norm<T, 0, 2, kMx>(a, d, st);
     else
-        run_norm<T, false, 4, kMx>(a, d, st);
+        run_norm<T, 0, 4, kMx>(a, d, st);
 }
 
 // ------------------------------------------------------------------ gradient
@@ -393,15 +409,16 @@ __device__ __forceinline__ void weight_sums(const NormGradArgs &a, uint32_t bloc
     }
 }
 
-// A workgroup takes a.groups rows at a time, a.waves waves each, and loads
-// the next ones before it works on those it has (kAhead).  Weight sums:
+// A workgroup takes a.groups rows at a time, a.waves waves each (kLanes < 64:
+// one wave takes 64 / kLanes rows), and loads the next ones before it works
+// on those it has (kAhead).  Weight sums:
 // kInRegs and kInLds, each workgroup keeps those of its rows and leaves them
 // in the workspace; kNone, where they are asked for, the workgroups from
 // a.row_blocks on take them from all rows (weight_sums), 64 columns each, and
 // a workgroup ends with its first rows; kWalk has no sums and walks the rows
 // like kInRegs.
 enum Sums { kNone, kWalk, kInRegs, kInLds };
-template <typename T, int kC, bool kAhead, Sums kSums, bool kRes, bool kDx, Edge kEdge>
+template <typename T, int kC, bool kAhead, int kLanes, Sums kSums, bool kRes, bool kDx, Edge kEdge>
 __global__ __launch_bounds__(1024) void norm_grad_kernel(const NormGradArgs a, const Dropout d, float *dgamma,
                                                          float *dbeta)
 {
@@ -418,8 +435,10 @@ __global__ __launch_bounds__(1024) void norm_grad_kernel(const NormGradArgs a, c
     __shared__ __attribute__((aligned(16))) float keep[kSums <= kWalk ? 1 : (kSums == kInLds ? 2 : 1) * kC * 8 * 1024];
     const uint32_t wave = (uint32_t)__builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));  // rows in scalar registers
     const uint32_t lane = threadIdx.x & 63u, cols = (uint32_t)a.cols;
-    const uint32_t g = (uint32_t)__builtin_amdgcn_readfirstlane((int)(wave / a.waves)), first = g * a.waves;
-    const uint32_t tpr = a.waves * 64u, t = threadIdx.x - first * 64u;
+    constexpr bool kShort = kLanes < 64;
+    const auto same_in_wave = [](uint32_t v) { return (uint32_t)__builtin_amdgcn_readfirstlane((int)v); };
+    const uint32_t g = kShort ? threadIdx.x / kLanes : same_in_wave(wave / a.waves), first = g * a.waves;
+    const uint32_t tpr = kShort ? kLanes : a.waves * 64u, t = kShort ? threadIdx.x % kLanes : threadIdx.x - first * 64u;
     const float inv_n = 1.0f / (float)cols;
     // wide rows read the weights again for each row rather than hold them
     constexpr bool kHoldW = kC <= 2;
@@ -454,7 +473,8 @@ __global__ __launch_bounds__(1024) void norm_grad_kernel(const NormGradArgs a, c
     const uint32_t rows = (uint32_t)a.rows;
     const float *means = a.layer ? a.mean : a.rstd;
     const auto fetch = [&](uint32_t base, Row &r) {  // past the end: the last row again
-        const int64_t row = __builtin_amdgcn_readfirstlane((int)min(base + g, rows - 1u));
+        const uint32_t at = min(base + g, rows - 1u);
+        const int64_t row = kShort ? at : same_in_wave(at);
 #pragma unroll
         for (int i = 0; i < kC; ++i) {
             load_chunk<T, kEdge, kStream<T>>(reinterpret_cast<const T *>(a.dy) + row * a.ld_dy, sp[i], cols, r.dy[i]);
@@ -469,11 +489,11 @@ __global__ __launch_bounds__(1024) void norm_grad_kernel(const NormGradArgs a, c
     // rows < 2^31 and three strides (where there is a loop) < 2^16: below 2^32
     const uint32_t stride = a.row_blocks * a.groups, base0 = block * a.groups;
     // whether each lane of the wave has a full chunk of its own in place i
-    const auto whole = [&](int i) { return (i * tpr + (wave - first) * 64u + 64u) * 8u <= cols; };
+    const auto whole = [&](int i) { return (i * tpr + (kShort ? kLanes : (wave - first) * 64u + 64u)) * 8u <= cols; };
     int parity = 0;
     const auto work = [&](uint32_t base, const Row &cur) {
-        const int64_t row = (uint32_t)__builtin_amdgcn_readfirstlane((int)(base + g));
-        // the same on every lane of a wave; waves past the last group (the
+        const int64_t row = kShort ? base + g : same_in_wave(base + g);
+        // the same on every lane of a row; waves past the last group (the
         // workgroups beside this one need 1024 threads) have no row
         const bool live = row < a.rows && g < a.groups;
         Draws x[kC];
@@ -528,9 +548,9 @@ __global__ __launch_bounds__(1024) void norm_grad_kernel(const NormGradArgs a, c
         }
         // both sums with one barrier, lanes 0-15 the one and 16-31 the other;
         // the two parities keep a row's slots apart from the next row's
-        s1 = wave_sum(s1);
-        s2 = wave_sum(s2);
-        if (a.waves > 1) {
+        s1 = lanes_sum<kLanes>(s1);
+        s2 = lanes_sum<kLanes>(s2);
+        if (!kShort && a.waves > 1) {
             if (lane == 0) red[parity][0][wave] = s1, red[parity][1][wave] = s2;
             __syncthreads();
             const uint32_t k = lane & 15u;
@@ -592,10 +612,21 @@ __global__ __launch_bounds__(1024) void norm_grad_kernel(const NormGradArgs a, c
         }
     }
     if constexpr (kSums > kWalk) {  // parts[workgroup][gamma, beta][cols]
+        if constexpr (kShort) {  // the sums of a wave's rows
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+#pragma unroll
+                for (int k = kLanes; k < 64; k *= 2) {
+                    sum_w[0][j] += __shfl_xor(sum_w[0][j], k);
+                    sum_b[0][j] += __shfl_xor(sum_b[0][j], k);
+                }
+            }
+        }
+        const uint32_t folds = kShort ? 16u : a.groups, apart = kShort ? 64u : tpr;
 #pragma unroll
         for (int which = 0; which < 2; ++which) {
             if (which == 1 && !dbeta) break;
-            if (kSums == kInRegs && a.groups > 1) {
+            if (kSums == kInRegs && folds > 1) {
                 __syncthreads();
 #pragma unroll
                 for (int i = 0; i < kC; ++i) {
@@ -605,7 +636,7 @@ __global__ __launch_bounds__(1024) void norm_grad_kernel(const NormGradArgs a, c
                         *kept(0, i, half) = make_float4(v[4 * half], v[4 * half + 1], v[4 * half + 2], v[4 * half + 3]);
                 }
             }
-            if (a.groups > 1) __syncthreads();
+            if (folds > 1) __syncthreads();
             if (g == 0) {  // the first group's threads add the others' sums
                 float *part = a.parts + ((size_t)block * 2 + which) * cols;
 #pragma unroll
@@ -620,8 +651,8 @@ __global__ __launch_bounds__(1024) void norm_grad_kernel(const NormGradArgs a, c
                             const float *r = (which ? sum_b[kRegs > i ? i : 0] : sum_w[kRegs > i ? i : 0]) + 4 * half;
                             m = make_float4(r[0], r[1], r[2], r[3]);
                         }
-                        for (uint32_t k = 1; k < a.groups; ++k) {
-                            const float4 o = kept(kSums == kInLds ? which : 0, i, half)[k * tpr];
+                        for (uint32_t k = 1; k < folds; ++k) {
+                            const float4 o = kept(kSums == kInLds ? which : 0, i, half)[k * apart];
                             m.x += o.x, m.y += o.y, m.z += o.z, m.w += o.w;
                         }
                         v[4 * half] = m.x, v[4 * half + 1] = m.y, v[4 * half + 2] = m.z, v[4 * half + 3] = m.w;
@@ -686,6 +717,7 @@ enum How { kNoSums, kRowsWalked, kInRows, kBeside, kApart };
 struct GradPlan {
     How sums;
     int chunks_per_thread;
+    int lanes;
     uint32_t waves, groups;
     int64_t row_blocks, parts;
 };
@@ -696,7 +728,8 @@ GradPlan grad_plan(int64_t rows, int64_t cols, bool sums)
     // 16 waves fit a workgroup
     g.chunks_per_thread = waves1 > 32 ? 4 : waves1 > 16 ? 2 : 1;
     g.waves = (uint32_t)((waves1 + g.chunks_per_thread - 1) / g.chunks_per_thread);
-    g.groups = 16 / g.waves;
+    g.lanes = lanes_of(cols);
+    g.groups = 16 / g.waves * (64 / g.lanes);
     const int64_t need = (rows + g.groups - 1) / g.groups;
     const bool small = rows * cols <= (3 << 20);
     if (g.chunks_per_thread == 4)
@@ -711,16 +744,17 @@ GradPlan grad_plan(int64_t rows, int64_t cols, bool sums)
     return g;
 }
 
-template <typename T, int kC, Sums kSums>
+template <typename T, int kC, Sums kSums, int kLanes = 64>
 void run_norm_grad(const NormGradArgs &a, const Dropout &d, How how, float *dgamma, float *dbeta, hipStream_t st)
 {
     const unsigned blocks = a.row_blocks + (how == kBeside ? (unsigned)((a.cols + 63) / 64) : 0u);
     const unsigned wide = 1u << 20;  // a launch's threads along x are below 2^32
     const dim3 grid(blocks < wide ? blocks : wide, (blocks + wide - 1) / wide);
-    const dim3 block(how == kBeside ? 1024 : a.waves * a.groups * 64);
+    const dim3 block(how == kBeside ? 1024 : a.waves * a.groups * kLanes);
     const Edge edge = edge_of(a.cols);
 #define FP4Q_NORM_GRAD(RES, DX, EDGE)                                                                          \
-    hipLaunchKernelGGL((norm_grad_kernel<T, kC, kC == 1 || (kC == 2 && (sizeof(T) == 2 || !RES)), kSums, RES, DX, EDGE>), \
+    hipLaunchKernelGGL((norm_grad_kernel<T, kC, kC == 1 || (kC == 2 && (sizeof(T) == 2 || !RES)), kLanes, kSums, RES,  \
+                                         DX, EDGE>),                                                                  \
                        grid, block, 0, st, a, d, dgamma, dbeta)
 #define FP4Q_NORM_GRAD_E(RES, DX)                            \
     do {                                                     \
@@ -728,7 +762,7 @@ void run_norm_grad(const NormGradArgs &a, const Dropout &d, How how, float *dgam
             FP4Q_NORM_GRAD(RES, DX, kWhole);                 \
         else if (edge == kRagged)                            \
             FP4Q_NORM_GRAD(RES, DX, kRagged);                \
-        else if constexpr (kC == 1)                          \
+        else if constexpr (kLanes == 16)                     \
             FP4Q_NORM_GRAD(RES, DX, kTiny);                  \
     } while (0)
     if (a.dres) {
@@ -738,6 +772,20 @@ void run_norm_grad(const NormGradArgs &a, const Dropout &d, How how, float *dgam
     }
 #undef FP4Q_NORM_GRAD_E
 #undef FP4Q_NORM_GRAD
+}
+
+template <typename T, Sums kOne, Sums kTwo>
+void run_norm_grad_n(const NormGradArgs &a, const Dropout &d, const GradPlan &g, How how, float *dgamma, float *dbeta,
+                     hipStream_t st)
+{
+    if (g.chunks_per_thread == 2)
+        run_norm_grad<T, 2, kTwo>(a, d, how, dgamma, dbeta, st);
+    else if (g.lanes == 64)
+        run_norm_grad<T, 1, kOne>(a, d, how, dgamma, dbeta, st);
+    else if (g.lanes == 32)
+        run_norm_grad<T, 1, kOne, 32>(a, d, how, dgamma, dbeta, st);
+    else
+        run_norm_grad<T, 1, kOne, 16>(a, d, how, dgamma, dbeta, st);
 }
 
 template <typename T>
@@ -763,18 +811,14 @@ void pick_norm_grad(const NormGradArgs &a, const Dropout &d, const GradPlan &g, 
         how = kNoSums;
     }
     if (how == kNoSums) dgamma = dbeta = nullptr;  // not the rows' kernel's
-    const bool two = g.chunks_per_thread == 2;
     if (g.chunks_per_thread == 4)
         run_norm_grad<T, 4, kNone>(a, d, how, dgamma, dbeta, st);
     else if (how == kNoSums || how == kBeside)
-        two ? run_norm_grad<T, 2, kNone>(a, d, how, dgamma, dbeta, st)
-            : run_norm_grad<T, 1, kNone>(a, d, how, dgamma, dbeta, st);
+        run_norm_grad_n<T, kNone, kNone>(a, d, g, how, dgamma, dbeta, st);
     else if (how == kRowsWalked)
-        two ? run_norm_grad<T, 2, kWalk>(a, d, how, dgamma, dbeta, st)
-            : run_norm_grad<T, 1, kWalk>(a, d, how, dgamma, dbeta, st);
+        run_norm_grad_n<T, kWalk, kWalk>(a, d, g, how, dgamma, dbeta, st);
     else
-        two ? run_norm_grad<T, 2, kInLds>(a, d, how, dgamma, dbeta, st)
-            : run_norm_grad<T, 1, kInRegs>(a, d, how, dgamma, dbeta, st);
+        run_norm_grad_n<T, kInRegs, kInLds>(a, d, g, how, dgamma, dbeta, st);
 }
 
 }  // namespace

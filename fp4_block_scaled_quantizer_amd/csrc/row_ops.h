@@ -265,6 +265,22 @@ __device__ __forceinline__ float wave_sum(float v)
     return lane_value(v, 63);
 }
 
+// The sum of each group of kLanes neighbouring lanes (16, 32 or 64), on every
+// lane of it: rotations inside a row of 16 and one exchange between two rows.
+template <int kLanes>
+__device__ __forceinline__ float lanes_sum(float v)
+{
+    if (kLanes == 64) return wave_sum(v);
+    v = dpp_add<0x128, 0xF>(v);  // row_ror:8
+    v = dpp_add<0x124, 0xF>(v);  // row_ror:4
+    v = dpp_add<0x122, 0xF>(v);  // row_ror:2
+    v = dpp_add<0x121, 0xF>(v);  // row_ror:1
+    if (kLanes == 32) v += u2f((uint32_t)__builtin_amdgcn_ds_swizzle((int)f2u(v), 0x401F));  // lane ^ 16
+    return v;
+}
+// How many lanes a short row takes (one chunk each); 64 above 256 columns.
+inline int lanes_of(int64_t cols) { return cols <= 128 ? 16 : cols <= 256 ? 32 : 64; }
+
 // Dropout.  Element (r, k) draws 16 bits as stochastic rounding does, from
 // Philox4x32-10 under counter {k / 8, r, stream_id, 1} (the 1 keeps the two
 // uses apart) and is kept iff they are >= drop = rint(p 2^16); kept values

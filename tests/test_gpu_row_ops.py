@@ -44,7 +44,8 @@ def same(a, b, what):
 
 
 SHAPES = [(1, 1), (3, 7), (2, 8), (5, 63), (33, 512), (17, 520), (9, 1000), (6, 1024), (5, 2048), (7, 2056), (4, 4096),
-          (3, 5003), (2, 8192), (3, 8200), (2, 16384), (2, 16392), (2, 32768)]
+          (3, 5003), (2, 8192), (3, 8200), (2, 16384), (2, 16392), (2, 32768),
+          (70, 100), (131, 128), (66, 136), (21, 200), (37, 256), (35, 257)]  # several rows to a wave, and not
 
 
 # ---------------------------------------------------------------- dropout
@@ -160,8 +161,9 @@ def test_norm(rows, cols, dtype, layer):
         assert ph.untouched() and py.untouched()
 
 
-@pytest.mark.parametrize("rows,cols,layout", [(1, 32, 0), (5, 96, 0), (33, 4096, 0), (3, 1056, 0), (1, 128, 1),
-                                              (33, 4096, 1), (31, 2176, 1), (64, 8320, 1), (2, 32768, 1), (40, 640, 1)])
+@pytest.mark.parametrize("rows,cols,layout", [(1, 32, 0), (5, 96, 0), (45, 192, 0), (33, 4096, 0), (3, 1056, 0),
+                                              (1, 128, 1), (70, 128, 1), (300, 256, 1), (33, 4096, 1),
+                                              (31, 2176, 1), (64, 8320, 1), (2, 32768, 1), (40, 640, 1)])
 @pytest.mark.parametrize("want_y", [True, False])
 def test_norm_mx_operand(rows, cols, layout, want_y):
     dev = device()
@@ -223,7 +225,7 @@ def test_norm_in_place():
 
 # ---------------------------------------------------------------- norm's gradient
 
-GRAD_SHAPES = SHAPES + [(700, 129), (5000, 64), (1100, 1032), (600, 2100), (515, 9000)]
+GRAD_SHAPES = SHAPES + [(700, 129), (5000, 64), (40000, 16), (30000, 130), (1100, 1032), (600, 2100), (515, 9000)]
 
 
 @pytest.mark.parametrize("layer", [True, False])
