@@ -441,7 +441,8 @@ def test_swiglu_gradient_against_differences():
 @pytest.mark.parametrize("half", [True, False])
 @pytest.mark.parametrize("n,heads,dim,rot,gap", [(1, 1, 2, 2, 0), (3, 5, 128, 128, 0), (33, 40, 128, 128, 1024), (7, 3, 80, 40, 8),
                                                  (5, 2, 96, 36, 3), (130, 1, 64, 64, 0), (9, 4, 256, 256, 0), (2, 3, 1024, 1024, 0),
-                                                 (4, 2, 1000, 14, 5), (1100, 3, 48, 48, 0)])
+                                                 (4, 2, 1000, 14, 5), (1100, 3, 48, 48, 0), (40000, 1, 64, 64, 0),
+                                                 (6, 5, 100, 50, 0), (700, 3, 104, 100, 0), (6001, 3, 24, 24, 0)])
 def test_rotary(n, heads, dim, rot, gap, half, dtype):
     dev = device()
     announce(f"rotary {dtype} {n}x{heads}x{dim} rot {rot} half {half}")
