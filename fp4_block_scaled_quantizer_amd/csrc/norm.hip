@@ -455,7 +455,8 @@ __global__ __launch_bounds__(1024) void norm_grad_kernel(const NormGradArgs a, c
     };
 #pragma unroll
     for (int i = 0; i < kC; ++i) {
-        sp[i] = span_of<kEdge>(i * tpr + t, cols);
+        // (a wave past the last group: one past the row's end, a load of one line)
+        sp[i] = span_of<kEdge>(kSums == kNone && g >= a.groups ? cols : i * tpr + t, cols);
         if (kSums == kInRegs) {
 #pragma unroll
             for (int j = 0; j < 8; ++j) sum_w[kRegs > i ? i : 0][j] = 0.0f, sum_b[kRegs > i ? i : 0][j] = 0.0f;
@@ -731,13 +732,11 @@ GradPlan grad_plan(int64_t rows, int64_t cols, bool sums)
     g.lanes = lanes_of(cols);
     g.groups = 16 / g.waves * (64 / g.lanes);
     const int64_t need = (rows + g.groups - 1) / g.groups;
-    const bool small = rows * cols <= (3 << 20);
-    if (g.chunks_per_thread == 4)
-        g.sums = sums ? kApart : kNoSums;
-    else if (sums)
-        g.sums = small && rows <= 768 ? kBeside : kInRows;
+    const int64_t few = g.chunks_per_thread > 1 ? 640 : 16 % g.waves == 0 ? 768 : 400;
+    if (sums)
+        g.sums = rows <= few ? kBeside : g.chunks_per_thread == 4 ? kApart : kInRows;
     else
-        g.sums = small ? kNoSums : kRowsWalked;
+        g.sums = g.chunks_per_thread == 4 || rows * cols <= (3 << 20) ? kNoSums : kRowsWalked;
     g.row_blocks = (g.sums == kInRows || g.sums == kRowsWalked) && need > kMaxParts ? kMaxParts : need;
     const int64_t runs = (rows + 127) / 128;
     g.parts = g.sums == kInRows ? g.row_blocks : g.sums == kApart ? (runs < 4 ? runs : 4) : 0;
