@@ -702,18 +702,24 @@ __global__ __launch_bounds__(1024) void norm_grad_weights_kernel(const float *__
     }
 }
 
-// How a call is run.  Weight sums: in the rows' own kernel (kInRows), beside
-// it in workgroups of their own that read the rows again (kBeside: small
-// calls, where a second launch costs more than the reading; a bf16 call
-// beside / in rows: 96 x 1024 4.3 / 7.9 us, 512 x 4096 10.1 / 12.7, 300 x
-// 7000 11.1 / 18.1, but 1000 x 1000 12.9 / 10.6 and 1024 x 4096 17.4 /
-// 15.8), or by a kernel of their own before the rows' (kApart: rows too wide
-// for a workgroup to keep their sums; and in place of kBeside where the rows'
-// results overwrite what it reads).  Without weight sums a workgroup per
-// compute unit walks the rows as for kInRows (kRowsWalked), whose loads then
-// never pause: 8192 x 4096 34.9 us, a workgroup to every two rows 47.5 (2047
-// x 14336 binary32 68 / 75, 65536 x 128 19.4 / 34.5); no difference up to
-// 2^21 elements, where the latter has the shorter code (kNoSums).
+// How a call is run.  Weight sums are made
+//   in the rows' own kernel (kInRows), each workgroup leaving its own;
+//   beside it (kBeside) in workgroups of their own, which read the rows again:
+//     few rows, where the workgroups' sums are as many as the rows and a
+//     second launch costs more than the reading.  The row counts are where
+//     the two meet, bf16 beside / in rows: 96 x 1024 4.3 / 7.9 us, 768 x 4096
+//     13.2 / 13.6, 400 x 5000 11.5 / 12.2, but 512 x 5000 (10 of 16 waves)
+//     14.8 / 12.8, 1000 x 1000 12.9 / 10.6; two chunks a thread 256 x 16384
+//     13.4 / 24.0, 640 x 12000 25.4 / 31.4, 768 x 8192 20.7 / 19.7;
+//   by a kernel of their own before the rows' (kApart): rows too wide for a
+//     workgroup to keep their sums (beside / apart 1024 x 20000 66 / 78, 2048
+//     x 20000 123 / 122, 4096 x 16392 226 / 206), and in place of kBeside
+//     where the rows' results overwrite what it reads.
+// Without them a workgroup per compute unit walks the rows as for kInRows
+// (kRowsWalked), whose loads then never pause: 8192 x 4096 34.9 us, a
+// workgroup to every two rows 47.5 (2047 x 14336 binary32 68 / 75); no
+// difference up to 2^21 elements, where the latter has the shorter code
+// (kNoSums).
 enum How { kNoSums, kRowsWalked, kInRows, kBeside, kApart };
 struct GradPlan {
     How sums;
@@ -732,7 +738,10 @@ GradPlan grad_plan(int64_t rows, int64_t cols, bool sums)
     g.lanes = lanes_of(cols);
     g.groups = 16 / g.waves * (64 / g.lanes);
     const int64_t need = (rows + g.groups - 1) / g.groups;
-    const int64_t few = g.chunks_per_thread > 1 ? 640 : 16 % g.waves == 0 ? 768 : 400;
+    const int64_t few = g.chunks_per_thread == 4   ? 1024
+                        : g.chunks_per_thread == 2 ? 640
+                        : 16 % g.waves == 0        ? 768
+                                                   : 400;
     if (sums)
         g.sums = rows <= few ? kBeside : g.chunks_per_thread == 4 ? kApart : kInRows;
     else

@@ -226,7 +226,7 @@ def test_norm_in_place():
 # ---------------------------------------------------------------- norm's gradient
 
 GRAD_SHAPES = SHAPES + [(700, 129), (5000, 64), (40000, 16), (30000, 130), (1100, 1032), (600, 2100), (515, 9000), (660, 9000),
-                        (641, 16392)]
+                        (641, 16392), (1030, 16392)]
 
 
 @pytest.mark.parametrize("layer", [True, False])
@@ -276,7 +276,7 @@ def test_norm_grad(rows, cols, dtype, layer):
 
 
 @pytest.mark.parametrize("rows,cols", [(50, 5), (300, 1000), (700, 2048), (1500, 1032), (300, 9000), (260, 20000),
-                                       (650, 9000), (650, 20000)])
+                                       (650, 9000), (650, 20000), (1030, 16392)])
 @pytest.mark.parametrize("dtype", [BF, F32])
 def test_norm_grad_in_place_with_weights(rows, cols, dtype):
     """dh or dx in the place of an input that the weight gradients are made
