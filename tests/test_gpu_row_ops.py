@@ -381,7 +381,7 @@ def test_norm_gradient_against_differences(layer):
 # ---------------------------------------------------------------- SwiGLU's gradient
 
 @pytest.mark.parametrize("M,F,pair,pad", [(1, 8, 8, 0), (5, 64, 32, 8), (3, 64, 64, 0), (17, 2080, 32, 16), (2, 14336, 32, 0),
-                                          (9, 4104, 4104, 0)])
+                                          (9, 4104, 4104, 0), (70, 2048, 2048, 8), (300, 72, 8, 0)])
 @pytest.mark.parametrize("want_h", [True, False])
 def test_swiglu_grad(M, F, pair, pad, want_h):
     dev = device()
