@@ -2,8 +2,9 @@
 
 Argument marshalling only: every step of the quantizers, GEMMs and row-wise
 operators runs in the library's HIP kernels.  PyTorch supplies device memory (``data_ptr()``) and the
-stream (``torch.cuda.current_stream()``).  If the library has not been built
-this module raises -- there is no fallback path.
+stream (``torch.cuda.current_stream()``, or the one a call names with
+``stream``, whose memory the outputs made for it then are).  If the library has
+not been built this module raises -- there is no fallback path.
 """
 from __future__ import annotations
 
@@ -145,6 +146,22 @@ def _stream(stream) -> int:
     return s.cuda_stream
 
 
+def _empty(shape, dtype, device, stream, *, returned: bool = True) -> torch.Tensor:
+    """Memory made for a call on `stream` is that stream's: from the caller's
+    current stream it could hold what kernels queued there still use, and be
+    given out there while the call's kernels still write. What the call
+    returns is recorded on the caller's stream too, where it is read next."""
+    if stream is None or torch.device(device).type != "cuda":
+        return torch.empty(shape, dtype=dtype, device=device)
+    if not hasattr(stream, "stream_id"):  # a handle of another library's
+        stream = torch.cuda.ExternalStream(stream.cuda_stream)
+    with torch.cuda.stream(stream):
+        t = torch.empty(shape, dtype=dtype, device=device)
+    if returned:
+        t.record_stream(torch.cuda.current_stream())
+    return t
+
+
 def _input(x: torch.Tensor, cols: Optional[int]):
     if x.dtype != torch.bfloat16 or x.dim() != 2 or x.stride(1) != 1:
         raise ValueError("x must be a 2-D bf16 tensor with unit column stride")
@@ -166,12 +183,12 @@ def mx_output_shapes(R: int, K: int, layout: int):
     return (R, K // 2), (R, K // 32)
 
 
-def _mx_outputs(R, K, layout, codes, scales, device):
+def _mx_outputs(R, K, layout, codes, scales, device, stream):
     cshape, sshape = mx_output_shapes(R, K, layout)
     if codes is None:
-        codes = torch.empty(cshape, dtype=torch.uint8, device=device)
+        codes = _empty(cshape, torch.uint8, device, stream)
     if scales is None:
-        scales = torch.empty(sshape, dtype=torch.uint8, device=device)
+        scales = _empty(sshape, torch.uint8, device, stream)
     return (_check_out(codes, "codes", torch.uint8, cshape, device),
             _check_out(scales, "scales", torch.uint8, sshape, device))
 
@@ -182,7 +199,7 @@ def fp4_quantize_mx(x: torch.Tensor, *, cols: Optional[int] = None, axis: int = 
                     stream=None) -> Tuple[torch.Tensor, torch.Tensor]:
     rows, cols, ld = _input(x, cols)
     R, K = _logical(rows, cols, axis)
-    codes, scales = _mx_outputs(R, K, layout, codes, scales, x.device)
+    codes, scales = _mx_outputs(R, K, layout, codes, scales, x.device, stream)
     _check("fp4_quantize_mx", lib().fp4_quantize_mx(x.data_ptr(), rows, cols, ld, axis, round, seed, stream_id,
                                                     codes.data_ptr(), scales.data_ptr(), layout, _stream(stream)))
     return codes, scales
@@ -197,8 +214,8 @@ def fp4_quantize_mx_dual(x: torch.Tensor, *, round_rows: int = RNE, stream_id_ro
     """x along rows and x^T along columns (optionally Hadamard) from one read
     of x: (codes_rows, scales_rows, codes_cols, scales_cols)."""
     rows, cols, ld = _input(x, None)
-    codes_rows, scales_rows = _mx_outputs(rows, cols, layout, codes_rows, scales_rows, x.device)
-    codes_cols, scales_cols = _mx_outputs(cols, rows, layout, codes_cols, scales_cols, x.device)
+    codes_rows, scales_rows = _mx_outputs(rows, cols, layout, codes_rows, scales_rows, x.device, stream)
+    codes_cols, scales_cols = _mx_outputs(cols, rows, layout, codes_cols, scales_cols, x.device, stream)
     _check("fp4_quantize_mx_dual",
            lib().fp4_quantize_mx_dual(x.data_ptr(), rows, cols, ld, round_rows, stream_id_rows, codes_rows.data_ptr(),
                                       scales_rows.data_ptr(), int(bool(hadamard_cols)), sign_mask & 0xFFFFFFFF,
@@ -213,7 +230,7 @@ def fp4_hadamard32_quantize(x: torch.Tensor, sign_mask: int, *, cols: Optional[i
                             stream=None) -> Tuple[torch.Tensor, torch.Tensor]:
     rows, cols, ld = _input(x, cols)
     R, K = _logical(rows, cols, axis)
-    codes, scales = _mx_outputs(R, K, layout, codes, scales, x.device)
+    codes, scales = _mx_outputs(R, K, layout, codes, scales, x.device, stream)
     _check("fp4_hadamard32_quantize",
            lib().fp4_hadamard32_quantize(x.data_ptr(), rows, cols, ld, axis, sign_mask & 0xFFFFFFFF, round, seed,
                                          stream_id, codes.data_ptr(), scales.data_ptr(), layout, _stream(stream)))
@@ -248,11 +265,11 @@ def fp4_quantize_nv(x: torch.Tensor, domain: int = NV_GLOBAL, *, cols: Optional[
     R, K = _logical(rows, cols, axis)
     cshape, sshape = nv_output_shapes(R, K, layout)
     if codes is None:
-        codes = torch.empty(cshape, dtype=torch.uint8, device=x.device)
+        codes = _empty(cshape, torch.uint8, x.device, stream)
     if scales is None:
-        scales = torch.empty(sshape, dtype=torch.uint8, device=x.device)
+        scales = _empty(sshape, torch.uint8, x.device, stream)
     if tensor_scale is None:
-        tensor_scale = torch.empty(nv_tensor_scale_shape(R, K, domain), dtype=torch.float32, device=x.device)
+        tensor_scale = _empty(nv_tensor_scale_shape(R, K, domain), torch.float32, x.device, stream)
     _check_out(codes, "codes", torch.uint8, cshape, x.device)
     _check_out(scales, "scales", torch.uint8, sshape, x.device)
     _check_out(tensor_scale, "tensor_scale", torch.float32, nv_tensor_scale_shape(R, K, domain), x.device)
@@ -268,7 +285,7 @@ def fp4_quantize_nv(x: torch.Tensor, domain: int = NV_GLOBAL, *, cols: Optional[
         return codes, scales, tensor_scale
     need = fp4q_nv_workspace_bytes(rows, cols, axis, domain)
     if workspace is None and need > 0:
-        workspace = torch.empty((need,), dtype=torch.uint8, device=x.device)
+        workspace = _empty((need,), torch.uint8, x.device, stream, returned=False)
     if workspace is not None and (workspace.device != x.device or not workspace.is_contiguous()):
         raise ValueError("workspace must be a contiguous tensor on x's device")
     wbytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
@@ -296,11 +313,11 @@ def fp4_quantize_nv_noalloc(x: torch.Tensor, domain: int = NV_GLOBAL, *, cols: O
     R, K = _logical(rows, cols, axis)
     cshape, sshape = nv_output_shapes(R, K, layout)
     if codes is None:
-        codes = torch.empty(cshape, dtype=torch.uint8, device=x.device)
+        codes = _empty(cshape, torch.uint8, x.device, stream)
     if scales is None:
-        scales = torch.empty(sshape, dtype=torch.uint8, device=x.device)
+        scales = _empty(sshape, torch.uint8, x.device, stream)
     if tensor_scale is None:
-        tensor_scale = torch.empty(nv_tensor_scale_shape(R, K, domain), dtype=torch.float32, device=x.device)
+        tensor_scale = _empty(nv_tensor_scale_shape(R, K, domain), torch.float32, x.device, stream)
     _check_out(codes, "codes", torch.uint8, cshape, x.device)
     _check_out(scales, "scales", torch.uint8, sshape, x.device)
     _check_out(tensor_scale, "tensor_scale", torch.float32, nv_tensor_scale_shape(R, K, domain), x.device)
@@ -311,9 +328,9 @@ def fp4_quantize_nv_noalloc(x: torch.Tensor, domain: int = NV_GLOBAL, *, cols: O
     return codes, scales, tensor_scale
 
 
-def _gemm_out(M: int, N: int, out_dtype, device, c: Optional[torch.Tensor]):
+def _gemm_out(M: int, N: int, out_dtype, device, c: Optional[torch.Tensor], stream):
     if c is None:
-        c = torch.empty((M, N), dtype=out_dtype, device=device)
+        c = _empty((M, N), out_dtype, device, stream)
     if c.dtype not in (torch.float32, torch.bfloat16) or c.dim() != 2 or c.stride(1) != 1:
         raise ValueError("c must be a 2-D fp32 or bf16 tensor with unit column stride")
     if tuple(c.shape) != (M, N) or c.device != torch.device(device):
@@ -336,7 +353,7 @@ def fp4_gemm_mx(a_codes: torch.Tensor, a_scales: torch.Tensor, b_codes: torch.Te
     K = a_codes.shape[1] * 2
     if b_codes.shape[1] * 2 != K:
         raise ValueError("A and B must have the same K")
-    c, ctype, ldc = _gemm_out(M, N, out_dtype, a_codes.device, c)
+    c, ctype, ldc = _gemm_out(M, N, out_dtype, a_codes.device, c, stream)
     if c_amax is not None:
         _check("fp4_gemm_mx_amax",
                lib().fp4_gemm_mx_amax(a_codes.data_ptr(), a_scales.data_ptr(), b_codes.data_ptr(), b_scales.data_ptr(),
@@ -360,7 +377,7 @@ def fp4_gemm_mx_quant(a_codes: torch.Tensor, a_scales: torch.Tensor, b_codes: to
     K = a_codes.shape[1] * 2
     if b_codes.shape[1] * 2 != K:
         raise ValueError("A and B must have the same K")
-    codes, scales = _mx_outputs(M, N, c_layout, codes, scales, a_codes.device)
+    codes, scales = _mx_outputs(M, N, c_layout, codes, scales, a_codes.device, stream)
     _check("fp4_gemm_mx_quant",
            lib().fp4_gemm_mx_quant(a_codes.data_ptr(), a_scales.data_ptr(), b_codes.data_ptr(), b_scales.data_ptr(),
                                    M, N, K, float(alpha), layout, codes.data_ptr(), scales.data_ptr(), c_layout,
@@ -381,7 +398,7 @@ def fp4_gemm_mx_swiglu_quant(a_codes: torch.Tensor, a_scales: torch.Tensor, b_co
     K = a_codes.shape[1] * 2
     if b_codes.shape[1] * 2 != K:
         raise ValueError("A and B must have the same K")
-    codes, scales = _mx_outputs(M, N // 2, h_layout, codes, scales, a_codes.device)
+    codes, scales = _mx_outputs(M, N // 2, h_layout, codes, scales, a_codes.device, stream)
     _check("fp4_gemm_mx_swiglu_quant",
            lib().fp4_gemm_mx_swiglu_quant(a_codes.data_ptr(), a_scales.data_ptr(), b_codes.data_ptr(),
                                           b_scales.data_ptr(), M, N, K, float(alpha), layout, codes.data_ptr(),
@@ -397,7 +414,7 @@ def fp4_swiglu_bf16(c: torch.Tensor, f: int, *, pair: int = 32, h: Optional[torc
         raise ValueError("c must be a 2-D bf16 tensor with contiguous rows")
     M = c.shape[0]
     if h is None:
-        h = torch.empty((M, f), dtype=torch.bfloat16, device=c.device)
+        h = _empty((M, f), torch.bfloat16, c.device, stream)
     if (h.dtype != torch.bfloat16 or h.dim() != 2 or h.stride(1) != 1 or tuple(h.shape) != (M, f)
             or h.device != c.device or (M > 1 and h.stride(0) < f)):
         raise ValueError(f"h must be a [{M} x {f}] bf16 tensor on {c.device} with unit column stride")
@@ -430,7 +447,7 @@ def fp4_gemm_nv(a_codes: torch.Tensor, a_scales: torch.Tensor, a_tensor_scale: t
     K = a_codes.shape[1] * 2
     if b_codes.shape[1] * 2 != K:
         raise ValueError("A and B must have the same K")
-    c, ctype, ldc = _gemm_out(M, N, out_dtype, a_codes.device, c)
+    c, ctype, ldc = _gemm_out(M, N, out_dtype, a_codes.device, c, stream)
     if c_amax is not None:
         _check("fp4_gemm_nv_amax",
                lib().fp4_gemm_nv_amax(a_codes.data_ptr(), a_scales.data_ptr(), a_tensor_scale.data_ptr(),
@@ -469,7 +486,7 @@ def _rows():
         at = [ctypes.cast(getattr(L, f), ctypes.c_void_p).value for f in
               ("fp4_dropout", "fp4_norm", "fp4q_norm_grad_workspace_bytes", "fp4_norm_grad", "fp4_swiglu_grad_bf16",
                "fp4_rotary")]
-        calls.bind(*at, Fp4qError, torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream)
+        calls.bind(*at, Fp4qError, torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream, torch.cuda.ExternalStream)
         _row_calls, _row_lib = calls, L
     return _row_calls
 
@@ -504,7 +521,7 @@ def fp4_norm(x: torch.Tensor, gamma: Optional[torch.Tensor] = None, beta: Option
     takes; `mx` for the MXFP4 operand of a bf16 y in `layout` (with want_y
     False, instead of y). h and y may each be x or residual."""
     if mx or codes is not None or scales is not None:
-        codes, scales = _mx_outputs(x.shape[0], x.shape[1], layout, codes, scales, x.device)
+        codes, scales = _mx_outputs(x.shape[0], x.shape[1], layout, codes, scales, x.device, stream)
     y, h, mean, rstd = _rows().norm(x, gamma, beta, kind, eps, residual, p, seed, stream_id, save, want_y, layout, y, h,
                                     mean, rstd, codes, scales, stream)
     return _new(Norm, (y, h, mean, rstd, codes, scales))

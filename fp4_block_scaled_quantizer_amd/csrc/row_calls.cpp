@@ -10,10 +10,12 @@
 
 #include <ATen/core/Tensor.h>
 #include <ATen/ops/empty.h>
+#include <c10/core/StreamGuard.h>
 #include <torch/csrc/autograd/python_variable.h>
 
 #include <stdexcept>
 #include <string>
+#include <vector>
 
 #include "../../include/fp4q.h"
 
@@ -27,7 +29,7 @@ struct Library {
     decltype(&::fp4_swiglu_grad_bf16) swiglu_grad;
     decltype(&::fp4_rotary) rotary;
     PyObject *error;          // Fp4qError
-    PyObject *current, *raw;  // torch's current device and its current stream
+    PyObject *current, *raw, *external;  // torch's current device, its current stream, a stream of a handle
 } lib{};
 
 struct Refused : std::runtime_error {
@@ -98,6 +100,56 @@ Matrix rows_of(const at::Tensor &t, const char *name)
     return Matrix{t.data_ptr(), ld};
 }
 
+// While a call runs, the `stream` it names is torch's current one. What the
+// call makes is then that stream's memory, which is given out again in the
+// order of its work; from the caller's stream it could hold what kernels
+// queued there still use, and be given out there while this call's kernels
+// still write. Outputs are recorded on the caller's stream as well, where they
+// are read next: they may be let go of there without more ado.
+class OnStream {
+public:
+    OnStream(PyObject *stream, const at::Tensor &t)
+    {
+        if (stream == Py_None || !t.is_cuda()) return;
+        PyObject *own = nullptr;
+        if (!PyObject_HasAttrString(stream, "stream_id")) {  // a handle of another library's
+            PyObject *h = PyObject_GetAttrString(stream, "cuda_stream");
+            own = h ? PyObject_CallOneArg(lib.external, h) : nullptr;
+            Py_XDECREF(h);
+            if (!own) throw PythonError();
+            stream = own;
+        }
+        const int64_t id = member(stream, "stream_id"), index = member(stream, "device_index"),
+                      type = member(stream, "device_type");
+        Py_XDECREF(own);
+        if (PyErr_Occurred()) throw PythonError();
+        if (type != (int64_t)at::kCUDA) throw Refused("stream must be a GPU stream");
+        guard_.reset_stream(c10::Stream::unpack3(id, (c10::DeviceIndex)index, at::kCUDA));
+    }
+    at::Tensor empty(at::IntArrayRef sizes, const at::TensorOptions &o)
+    {
+        at::Tensor t = at::empty(sizes, o);
+        if (guard_.original_stream()) made_.push_back(t);
+        return t;
+    }
+    void done() const
+    {
+        if (const auto caller = guard_.original_stream())
+            for (const at::Tensor &t : made_) t.record_stream(*caller);
+    }
+
+private:
+    static int64_t member(PyObject *o, const char *name)
+    {
+        PyObject *v = PyErr_Occurred() ? nullptr : PyObject_GetAttrString(o, name);
+        const int64_t k = v ? PyLong_AsLongLong(v) : -1;
+        Py_XDECREF(v);
+        return k;
+    }
+    c10::OptionalStreamGuard guard_;
+    std::vector<at::Tensor> made_;
+};
+
 // A call's first matrix, and others of its shape, type and device.
 struct Like {
     const at::Tensor &t;
@@ -117,7 +169,7 @@ struct Like {
         return rows_of(o, name);
     }
     // given, made here, or (neither wanted nor given) none; `keep` holds it
-    Matrix output(PyObject *o, const char *name, bool wanted, at::Tensor &keep) const
+    Matrix output(OnStream &on, PyObject *o, const char *name, bool wanted, at::Tensor &keep) const
     {
         const at::Tensor *g = tensor_or_null(o, name);
         if (g) {
@@ -125,7 +177,7 @@ struct Like {
             return matrix(*g, name);
         }
         if (!wanted) return Matrix{};
-        keep = at::empty({rows, cols}, t.options());
+        keep = on.empty({rows, cols}, t.options());
         return Matrix{keep.data_ptr(), cols};
     }
     Matrix input(PyObject *o, const char *name) const
@@ -140,13 +192,13 @@ struct Like {
                           " elements on the same device");
         return o.data_ptr();
     }
-    float *floats(PyObject *o, const char *name, int64_t n, bool wanted, at::Tensor &keep) const
+    float *floats(OnStream &on, PyObject *o, const char *name, int64_t n, bool wanted, at::Tensor &keep) const
     {
         const at::Tensor *g = tensor_or_null(o, name);
         if (g)
             keep = *g;
         else if (wanted)
-            keep = at::empty({n}, t.options().dtype(at::kFloat));
+            keep = on.empty({n}, t.options().dtype(at::kFloat));
         else
             return nullptr;
         return static_cast<float *>(vector(keep, name, n, at::kFloat));
@@ -163,9 +215,9 @@ struct Like {
     }
 };
 
-// The handle of `stream`, or of the current one.  The library launches on
-// the current GPU, which the tensors have to be on.
-void *stream_of(PyObject *stream, const at::Tensor &t)
+// The handle of the current stream.  The library launches on the current GPU,
+// which the tensors have to be on.
+void *stream_of(const at::Tensor &t)
 {
     PyObject *dev = t.is_cuda() ? PyObject_CallNoArgs(lib.current) : nullptr;
     if (t.is_cuda() && !dev) throw PythonError();
@@ -174,25 +226,13 @@ void *stream_of(PyObject *stream, const at::Tensor &t)
         Py_XDECREF(dev);
         throw Refused("the tensors must be on the current GPU");
     }
-    PyObject *h = stream == Py_None ? PyObject_CallOneArg(lib.raw, dev) : PyObject_GetAttrString(stream, "cuda_stream");
+    PyObject *h = PyObject_CallOneArg(lib.raw, dev);
     Py_DECREF(dev);
     if (!h) throw PythonError();
     void *s = PyLong_AsVoidPtr(h);
     Py_DECREF(h);
     if (!s && PyErr_Occurred()) throw PythonError();
     return s;
-}
-
-// Memory made here for a call on a `stream` of the user's, and let go of when
-// the call returns: not given out again before that stream is through with it.
-void used_on(PyObject *stream, const at::Tensor &t)
-{
-    if (stream == Py_None || !t.defined()) return;
-    PyObject *o = THPVariable_Wrap(t);
-    PyObject *r = o ? PyObject_CallMethod(o, "record_stream", "O", stream) : nullptr;
-    Py_XDECREF(o);
-    if (!r) throw PythonError();
-    Py_DECREF(r);
 }
 
 void done(const char *fn, fp4q_status status)
@@ -233,13 +273,15 @@ PyObject *dropout(PyObject *const *a)
 {
     enum { X, P, SEED, STREAM_ID, RES, Y, STREAM };
     const Like x(a[X], "x");
+    OnStream on(a[STREAM], x.t);
     const Matrix mx = x.matrix(x.t, "x"), mr = x.input(a[RES], "residual");
     at::Tensor y;
-    const Matrix my = x.output(a[Y], "y", true, y);
+    const Matrix my = x.output(on, a[Y], "y", true, y);
     const double p = real(a[P]);
-    void *st = stream_of(a[STREAM], x.t);
+    void *st = stream_of(x.t);
     done("fp4_dropout", lib.dropout(mx.p, x.rows, x.cols, mx.ld, x.type, mr.p, mr.ld, (float)p, bits64(a[SEED]),
                                     (uint32_t)bits64(a[STREAM_ID]), my.p, my.ld, st));
+    on.done();
     return result(y);
 }
 
@@ -247,22 +289,24 @@ PyObject *norm(PyObject *const *a)
 {
     enum { X, GAMMA, BETA, KIND, EPS, RES, P, SEED, STREAM_ID, SAVE, WANT_Y, LAYOUT, Y, H, MEAN, RSTD, CODES, SCALES, STREAM };
     const Like x(a[X], "x");
+    OnStream on(a[STREAM], x.t);
     const Matrix mx = x.matrix(x.t, "x"), mr = x.input(a[RES], "residual");
     const double p = real(a[P]);
     const int kind = (int)integer(a[KIND]);
     const bool save = truth(a[SAVE]);
     at::Tensor y, h, mean, rstd;
-    const Matrix mh = x.output(a[H], "h", mr.p || p > 0, h), my = x.output(a[Y], "y", truth(a[WANT_Y]), y);
-    float *pm = x.floats(a[MEAN], "mean", x.rows, save && kind == FP4Q_NORM_LAYER, mean);
-    float *ps = x.floats(a[RSTD], "rstd", x.rows, save, rstd);
+    const Matrix mh = x.output(on, a[H], "h", mr.p || p > 0, h), my = x.output(on, a[Y], "y", truth(a[WANT_Y]), y);
+    float *pm = x.floats(on, a[MEAN], "mean", x.rows, save && kind == FP4Q_NORM_LAYER, mean);
+    float *ps = x.floats(on, a[RSTD], "rstd", x.rows, save, rstd);
     int wt = -1;
     const void *pg = x.weight(a[GAMMA], "gamma", wt), *pb = x.weight(a[BETA], "beta", wt);
     const at::Tensor *codes = tensor_or_null(a[CODES], "codes"), *scales = tensor_or_null(a[SCALES], "scales");
-    void *st = stream_of(a[STREAM], x.t);
+    void *st = stream_of(x.t);
     done("fp4_norm", lib.norm(mx.p, x.rows, x.cols, mx.ld, x.type, mr.p, mr.ld, (float)p, bits64(a[SEED]),
                               (uint32_t)bits64(a[STREAM_ID]), mh.p, mh.ld, kind, pg, pb, wt < 0 ? FP4Q_OUT_F32 : wt,
                               (float)real(a[EPS]), my.p, my.ld, pm, ps, codes ? codes->data_ptr() : nullptr,
                               scales ? scales->data_ptr() : nullptr, (int)integer(a[LAYOUT]), st));
+    on.done();
     return results({&y, &h, &mean, &rstd});
 }
 
@@ -270,19 +314,20 @@ PyObject *norm_grad(PyObject *const *a)
 {
     enum { DY, H, GAMMA, KIND, MEAN, RSTD, DRES, P, SEED, STREAM_ID, WEIGHTS, DH, DX, DGAMMA, DBETA, WORKSPACE, STREAM };
     const Like x(a[DY], "dy");
+    OnStream on(a[STREAM], x.t);
     const Matrix my = x.matrix(x.t, "dy"), mh = x.matrix(tensor(a[H], "h"), "h"), mr = x.input(a[DRES], "dres");
     const double p = real(a[P]);
     const int kind = (int)integer(a[KIND]);
     const bool weights = truth(a[WEIGHTS]);
     at::Tensor dh, dx, dgamma, dbeta, mean, rstd, ws;
-    const Matrix md = x.output(a[DH], "dh", true, dh), mx = x.output(a[DX], "dx", p > 0, dx);
-    float *pg = x.floats(a[DGAMMA], "dgamma", x.cols, weights, dgamma);
-    float *pb = x.floats(a[DBETA], "dbeta", x.cols, weights && kind == FP4Q_NORM_LAYER, dbeta);
+    const Matrix md = x.output(on, a[DH], "dh", true, dh), mx = x.output(on, a[DX], "dx", p > 0, dx);
+    float *pg = x.floats(on, a[DGAMMA], "dgamma", x.cols, weights, dgamma);
+    float *pb = x.floats(on, a[DBETA], "dbeta", x.cols, weights && kind == FP4Q_NORM_LAYER, dbeta);
     int wt = -1;
     const void *gamma = x.weight(a[GAMMA], "gamma", wt);
-    const float *pm = x.floats(a[MEAN], "mean", x.rows, false, mean);
+    const float *pm = x.floats(on, a[MEAN], "mean", x.rows, false, mean);
     const float *ps = static_cast<float *>(x.vector(tensor(a[RSTD], "rstd"), "rstd", x.rows, at::kFloat));
-    void *st = stream_of(a[STREAM], x.t);
+    void *st = stream_of(x.t);
     size_t bytes = 0;
     if (const at::Tensor *w = tensor_or_null(a[WORKSPACE], "workspace")) {
         if (w->device() != x.t.device() || !w->is_contiguous())
@@ -292,12 +337,12 @@ PyObject *norm_grad(PyObject *const *a)
     } else if (pg || pb) {
         bytes = lib.norm_grad_workspace(x.rows, x.cols);
         if (bytes) ws = at::empty({(int64_t)bytes}, x.t.options().dtype(at::kByte));
-        used_on(a[STREAM], ws);
     }
     done("fp4_norm_grad",
          lib.norm_grad(my.p, x.rows, x.cols, my.ld, x.type, mh.p, mh.ld, mr.p, mr.ld, kind, gamma,
                        wt < 0 ? FP4Q_OUT_F32 : wt, pm, ps, (float)p, bits64(a[SEED]), (uint32_t)bits64(a[STREAM_ID]),
                        md.p, md.ld, mx.p, mx.ld, pg, pb, bytes ? ws.data_ptr() : nullptr, bytes, st));
+    on.done();
     return results({&dh, &dx, &dgamma, &dbeta});
 }
 
@@ -305,6 +350,7 @@ PyObject *swiglu_grad(PyObject *const *a)
 {
     enum { DH, C, PAIR, WANT_H, DC, H, STREAM };
     const Like x(a[DH], "dh");
+    OnStream on(a[STREAM], x.t);
     const Matrix mi = x.matrix(x.t, "dh");
     const int64_t M = x.rows, F = x.cols;
     const auto wide = [&](const at::Tensor &t, const char *name) {
@@ -319,11 +365,12 @@ PyObject *swiglu_grad(PyObject *const *a)
     if (const at::Tensor *g = tensor_or_null(a[DC], "dc"))
         dc = *g;
     else
-        dc = at::empty({M, 2 * F}, x.t.options());
-    const Matrix mo = wide(dc, "dc"), mh = x.output(a[H], "h", truth(a[WANT_H]), h);
-    void *st = stream_of(a[STREAM], x.t);
+        dc = on.empty({M, 2 * F}, x.t.options());
+    const Matrix mo = wide(dc, "dc"), mh = x.output(on, a[H], "h", truth(a[WANT_H]), h);
+    void *st = stream_of(x.t);
     done("fp4_swiglu_grad_bf16", lib.swiglu_grad(mi.p, mi.ld, mc.p, M, F, mc.ld, integer(a[PAIR]), mo.p, mo.ld, mh.p,
                                                  mh.ld, st));
+    on.done();
     return results({&dc, &h});
 }
 
@@ -333,6 +380,7 @@ PyObject *rotary(PyObject *const *a)
     const at::Tensor &x = tensor(a[X], "x");
     const int type = type_of(x);
     if (type < 0 || x.dim() != 3) throw Refused("x must be a [tokens, heads, dim] fp32 or bf16 tensor");
+    OnStream on(a[STREAM], x);
     const int64_t n = x.size(0), heads = x.size(1), dim = x.size(2);
     struct Strides {
         int64_t token, head;
@@ -349,7 +397,7 @@ PyObject *rotary(PyObject *const *a)
             throw Refused("y must be a tensor of x's shape, type and device");
         y = *g;
     } else {
-        y = at::empty(x.sizes(), x.options());
+        y = on.empty(x.sizes(), x.options());
     }
     const Strides sy = strides(y, "y");
     const at::Tensor &pos = tensor(a[POSITIONS], "positions"), &freq = tensor(a[FREQ], "inv_freq");
@@ -358,11 +406,12 @@ PyObject *rotary(PyObject *const *a)
         throw Refused("positions must be one contiguous int32 or int64 per token on the same device");
     if (freq.scalar_type() != at::kFloat || freq.device() != x.device() || !freq.is_contiguous())
         throw Refused("inv_freq must be contiguous fp32 on the same device");
-    void *st = stream_of(a[STREAM], x);
+    void *st = stream_of(x);
     done("fp4_rotary",
          lib.rotary(x.data_ptr(), n, heads, dim, sx.token, sx.head, type, pos.data_ptr(), wide ? 64 : 32,
                     static_cast<const float *>(freq.data_ptr()), 2 * freq.numel(), (int)integer(a[STYLE]),
                     truth(a[INVERSE]) ? 1 : 0, (float)real(a[SCALE]), y.data_ptr(), sy.token, sy.head, st));
+    on.done();
     return result(y);
 }
 
@@ -389,12 +438,13 @@ PyObject *entry(PyObject *, PyObject *const *args, Py_ssize_t n)
 PyObject *bind(PyObject *, PyObject *args)
 {
     unsigned long long f[6];
-    PyObject *error, *current, *raw;
-    if (!PyArg_ParseTuple(args, "KKKKKKOOO", &f[0], &f[1], &f[2], &f[3], &f[4], &f[5], &error, &current, &raw))
+    PyObject *error, *current, *raw, *external;
+    if (!PyArg_ParseTuple(args, "KKKKKKOOOO", &f[0], &f[1], &f[2], &f[3], &f[4], &f[5], &error, &current, &raw, &external))
         return nullptr;
     Py_INCREF(error);
     Py_INCREF(current);
     Py_INCREF(raw);
+    Py_INCREF(external);
     lib.dropout = reinterpret_cast<decltype(lib.dropout)>(f[0]);
     lib.norm = reinterpret_cast<decltype(lib.norm)>(f[1]);
     lib.norm_grad_workspace = reinterpret_cast<decltype(lib.norm_grad_workspace)>(f[2]);
@@ -404,12 +454,13 @@ PyObject *bind(PyObject *, PyObject *args)
     lib.error = error;
     lib.current = current;
     lib.raw = raw;
+    lib.external = external;
     Py_RETURN_NONE;
 }
 
 template <typename F> PyCFunction method(F *f) { return reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(f)); }
 
-PyMethodDef methods[] = {{"bind", bind, METH_VARARGS, "the library's entry points, Fp4qError, torch's current device and stream"},
+PyMethodDef methods[] = {{"bind", bind, METH_VARARGS, "the library's entry points, Fp4qError, torch's current device and stream, ExternalStream"},
                          {"dropout", method(entry<dropout, 7>), METH_FASTCALL, nullptr},
                          {"norm", method(entry<norm, 19>), METH_FASTCALL, nullptr},
                          {"norm_grad", method(entry<norm_grad, 17>), METH_FASTCALL, nullptr},
