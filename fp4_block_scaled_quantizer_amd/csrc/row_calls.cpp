@@ -295,7 +295,7 @@ PyObject *norm(PyObject *const *a)
     const int kind = (int)integer(a[KIND]);
     const bool save = truth(a[SAVE]);
     at::Tensor y, h, mean, rstd;
-    const Matrix mh = x.output(on, a[H], "h", mr.p || p > 0, h), my = x.output(on, a[Y], "y", truth(a[WANT_Y]), y);
+    const Matrix mh = x.output(on, a[H], "h", a[RES] != Py_None || p > 0, h), my = x.output(on, a[Y], "y", truth(a[WANT_Y]), y);
     float *pm = x.floats(on, a[MEAN], "mean", x.rows, save && kind == FP4Q_NORM_LAYER, mean);
     float *ps = x.floats(on, a[RSTD], "rstd", x.rows, save, rstd);
     int wt = -1;
