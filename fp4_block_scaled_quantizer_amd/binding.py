@@ -561,8 +561,9 @@ def fp4_swiglu_grad_bf16(dh: torch.Tensor, c: torch.Tensor, *, pair: int = 32, w
 def fp4_rotary(x: torch.Tensor, positions: torch.Tensor, inv_freq: torch.Tensor, *, style: int = ROTARY_HALF,
                scale: float = 1.0, inverse: bool = False, y: Optional[torch.Tensor] = None,
                stream=None) -> torch.Tensor:
-    """Rotary positions of x [tokens, heads, dim] (any token and head
-    strides, so a slice of a fused QKV output serves): pair i of each head
+    """Rotary positions of x [tokens, heads, dim] (tokens of whole heads, so a
+    slice of a fused QKV output serves, or heads of whole tokens, such as
+    `t.transpose(0, 1)` of an attention's [heads, tokens, dim]): pair i of each head
     turns by positions[t] * inv_freq[i], the first 2 len(inv_freq) elements
     of the head taking part. `inverse` turns back: the gradient. y may be x."""
     return _rows().rotary(x, positions, inv_freq, style, scale, inverse, y, stream)

@@ -784,9 +784,13 @@ fp4q_status fp4_rotary(const void *x, int64_t tokens, int64_t heads, int64_t dim
     if (tokens < 0 || heads < 0 || dim < 0 || tokens > kMaxDim || heads > 65536 || dim > 1024 || rot < 2 ||
         rot % 2 != 0 || rot > dim)
         return FP4Q_ESHAPE;
-    // the heads of a token lie side by side or apart, and so do the tokens
-    if (x_head < dim || y_head < dim || x_head > kMaxDim || y_head > kMaxDim || x_token > kMaxDim || y_token > kMaxDim ||
-        (heads > 0 && (x_token < (heads - 1) * x_head + dim || y_token < (heads - 1) * y_head + dim)))
+    // tokens of whole heads or heads of whole tokens, side by side or apart
+    const auto nested = [dim](int64_t n, int64_t inner, int64_t outer) {
+        return inner >= dim && (n == 0 || outer >= (n - 1) * inner + dim);
+    };
+    if (x_head > kMaxDim || y_head > kMaxDim || x_token > kMaxDim || y_token > kMaxDim ||
+        !(nested(heads, x_head, x_token) || nested(tokens, x_token, x_head)) ||
+        !(nested(heads, y_head, y_token) || nested(tokens, y_token, y_head)))
         return FP4Q_ESHAPE;
     if (tokens == 0 || heads == 0) return FP4Q_OK;
     if (!x || !y || !positions || !inv_freq) return FP4Q_EINVAL;

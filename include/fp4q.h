@@ -430,7 +430,8 @@ FP4Q_API fp4q_status fp4_swiglu_grad_bf16(const void *dh, int64_t ld_dh, const v
 
 /* Rotary positions.  Element (t, head, d) of x lies at t * x_token + head *
  * x_head + d, so the query and key heads can be rotated where a fused QKV
- * GEMM left them.  Pair i of a head (elements i and i + rot/2 in the half
+ * GEMM left them, or moved into (or out of) an attention's [heads, tokens,
+ * dim] on the way; x and y need not agree in order.  Pair i of a head (elements i and i + rot/2 in the half
  * style, 2i and 2i + 1 interleaved) turns by positions[t] * inv_freq[i]:
  *   (a, b) -> scale * (a cos - b sin, b cos + a sin),
  * by the opposite angle with inverse = 1 (the gradient: scale * R^T); the
@@ -439,7 +440,8 @@ FP4Q_API fp4q_status fp4_swiglu_grad_bf16(const void *dh, int64_t ld_dh, const v
  * inv_freq: rot/2 binary32, scaled for a long context as its user wants.  The
  * angle's whole turns are removed in binary64.  FP4Q_ESHAPE unless 2 <= rot
  * <= dim <= 1024, rot even, heads <= 65536, heads and tokens not overlapping
- * (x_head >= dim, x_token >= the span of a token's heads).  y may be x. */
+ * (x_head >= dim and x_token >= the span of a token's heads, or x_token >= dim
+ * and x_head >= the span of a head's tokens; y alike).  y may be x. */
 FP4Q_API fp4q_status fp4_rotary(const void *x, int64_t tokens, int64_t heads, int64_t dim, int64_t x_token,
                                 int64_t x_head, int type, const void *positions, int position_bits,
                                 const float *inv_freq, int64_t rot, int style, int inverse, float scale, void *y,

@@ -44,3 +44,33 @@ def test_empty_matrices(rows, cols, dtype):
         x = torch.empty((n, heads, 32), dtype=dtype, device=dev)
         assert B.fp4_rotary(x, torch.zeros((n,), dtype=torch.int64, device=dev), freq).shape == (n, heads, 32)
     torch.cuda.synchronize()
+
+
+# ---------------------------------------------------------------- heads of whole tokens
+
+@pytest.mark.parametrize("half", [True, False])
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("n,heads,dim,rot", [(1, 3, 64, 64), (7, 1, 64, 32), (33, 5, 128, 128), (1030, 2, 100, 50), (9, 4, 48, 14)])
+def test_rotary_of_heads_of_whole_tokens(n, heads, dim, rot, dtype, half):
+    """[heads, tokens, dim] storage on either side and in place, at a pitch."""
+    dev = device()
+    announce(f"rotary of heads of whole tokens {dtype} {n}x{heads}x{dim} rot {rot} half {half}")
+    style = B.ROTARY_HALF if half else B.ROTARY_INTERLEAVED
+    x = draw((heads, n, dim), n + dim, dtype)
+    pos = torch.randint(0, 1 << 18, (n,), generator=torch.Generator().manual_seed(n))
+    freq, _ = B.rotary_frequencies(rot, 500000.0)
+    args = dict(style=style, scale=1.25)
+    want, e = R.rotary(x.transpose(0, 1).contiguous(), pos, freq, half, False, 1.25)
+    px = Padded(heads, n * dim, dtype, dev, 24, 0, x.reshape(heads, -1))
+    xv = px.view.unflatten(1, (n, dim)).transpose(0, 1)
+    y = B.fp4_rotary(xv, pos.to(dev), freq.to(dev), **args)
+    assert y.shape == (n, heads, dim) and y.is_contiguous()
+    R.check(y, want, e, "y")
+    py = Padded(heads, n * dim, dtype, dev, 5, 1)
+    yv = py.view.unflatten(1, (n, dim)).transpose(0, 1)
+    B.fp4_rotary(xv, pos.to(dev), freq.to(dev), y=yv, **args)
+    same(yv, y, "into heads of whole tokens")
+    assert py.untouched()
+    B.fp4_rotary(xv, pos.to(dev), freq.to(dev), y=xv, **args)
+    same(xv, y, "in place")
+    assert px.untouched()
