@@ -366,21 +366,35 @@ fp4q_status run_quantize_nv(const void *x, int64_t rows, int64_t cols, int64_t l
 
 // ---- the row-wise operators between the GEMMs
 
-// A row-major [rows x cols] argument: its leading dimension and byte range.
+// A row-major [rows x cols] argument: its leading dimension and byte range,
+// and in bytes its pitch and the width of its rows.
 struct Matrix {
     const void *p;
     int64_t ld;
     Range r;
+    uint64_t pitch, width;
 };
 Matrix matrix(const void *p, int64_t rows, int64_t cols, int64_t ld, uint64_t esize)
 {
-    return Matrix{p, ld, bytes(p, p ? ((uint64_t)(rows - 1) * (uint64_t)ld + (uint64_t)cols) * esize : 0)};
+    return Matrix{p, ld, bytes(p, p ? ((uint64_t)(rows - 1) * (uint64_t)ld + (uint64_t)cols) * esize : 0),
+                  (uint64_t)ld * esize, (uint64_t)cols * esize};
 }
 bool meet(Range a, Range b) { return a.lo != a.hi && b.lo != b.hi && overlap(a, b); }
+// Matrices whose ranges meet share no byte if they have the same pitch and
+// their columns, which start `d` apart in it, do not meet: column blocks of
+// one buffer.
+bool apart(const Matrix &a, const Matrix &b)
+{
+    if (!meet(a.r, b.r)) return true;
+    if (a.pitch != b.pitch) return false;
+    const uint64_t d = b.r.lo >= a.r.lo ? (b.r.lo - a.r.lo) % a.pitch
+                                        : (a.pitch - (a.r.lo - b.r.lo) % a.pitch) % a.pitch;
+    return d >= a.width && d + b.width <= a.pitch;
+}
 // An output and an input that share memory must be the same matrix.
 bool same_or_apart(const Matrix &out, const Matrix &in)
 {
-    return !meet(out.r, in.r) || (out.p == in.p && out.ld == in.ld);
+    return apart(out, in) || (out.p == in.p && out.ld == in.ld);
 }
 
 bool type_ok(int type) { return type == FP4Q_OUT_F32 || type == FP4Q_OUT_BF16; }
@@ -630,7 +644,7 @@ fp4q_status fp4_norm(const void *x, int64_t rows, int64_t cols, int64_t ld_x, in
                            bytes(scales, scales ? (uint64_t)rows_out * cols / 32 : 0)};
     for (int i = 0; i < 6; ++i) {
         for (int j = i + 1; j < 6; ++j)
-            if (meet(outs[i], outs[j])) return FP4Q_EINVAL;
+            if (i == 0 && j == 1 ? !apart(mh, my) : meet(outs[i], outs[j])) return FP4Q_EINVAL;
         for (const Range &w : weights)
             if (meet(outs[i], w)) return FP4Q_EINVAL;
         for (const Matrix &m : in) {
@@ -708,7 +722,7 @@ fp4q_status fp4_norm_grad(const void *dy, int64_t rows, int64_t cols, int64_t ld
                                bytes(dbeta, dbeta ? cols * 4 : 0), bytes(workspace, need)};
         for (int i = 0; i < 5; ++i) {
             for (int j = i + 1; j < 5; ++j)
-                if (meet(outs[i], outs[j])) return FP4Q_EINVAL;
+                if (i == 0 && j == 1 ? !apart(mo[0], mo[1]) : meet(outs[i], outs[j])) return FP4Q_EINVAL;
             for (const Range &r : small)
                 if (meet(outs[i], r)) return FP4Q_EINVAL;
             for (const Matrix &m : in) {
@@ -756,7 +770,7 @@ fp4q_status fp4_swiglu_grad_bf16(const void *dh, int64_t ld_dh, const void *c, i
     if (!aligned(dh, 16) || !aligned(c, 16) || !aligned(dc, 16) || !aligned(h, 16)) return FP4Q_EALIGN;
     const Matrix mi = matrix(dh, M, F, ld_dh, 2), mc = matrix(c, M, 2 * F, ldc, 2);
     const Matrix mo = matrix(dc, M, 2 * F, ld_dc, 2), mh = matrix(h, M, F, ldh, 2);
-    if (meet(mo.r, mi.r) || !same_or_apart(mo, mc) || meet(mh.r, mc.r) || meet(mh.r, mo.r) || !same_or_apart(mh, mi))
+    if (!apart(mo, mi) || !same_or_apart(mo, mc) || !apart(mh, mc) || !apart(mh, mo) || !same_or_apart(mh, mi))
         return FP4Q_EINVAL;
     fp4q::SwigluGradArgs a{};
     a.dh = dh;
@@ -797,11 +811,14 @@ fp4q_status fp4_rotary(const void *x, int64_t tokens, int64_t heads, int64_t dim
     const uint64_t es = type_size(type);
     if (!aligned(x, es) || !aligned(y, es) || !aligned(positions, position_bits / 8) || !aligned(inv_freq, 4))
         return FP4Q_EALIGN;
-    const Range rx = bytes(x, ((uint64_t)(tokens - 1) * x_token + (uint64_t)(heads - 1) * x_head + dim) * es);
-    const Range ry = bytes(y, ((uint64_t)(tokens - 1) * y_token + (uint64_t)(heads - 1) * y_head + dim) * es);
+    const auto heads_of = [&](const void *p, int64_t token, int64_t head) {
+        return nested(heads, head, token) ? matrix(p, tokens, (heads - 1) * head + dim, token, es)
+                                          : matrix(p, heads, (tokens - 1) * token + dim, head, es);
+    };
+    const Matrix mx = heads_of(x, x_token, x_head), my = heads_of(y, y_token, y_head);
     const bool in_place = x == y && x_token == y_token && x_head == y_head;
-    if ((meet(rx, ry) && !in_place) || meet(ry, bytes(positions, (uint64_t)tokens * position_bits / 8)) ||
-        meet(ry, bytes(inv_freq, (uint64_t)rot / 2 * 4)))
+    if ((!apart(my, mx) && !in_place) || meet(my.r, bytes(positions, (uint64_t)tokens * position_bits / 8)) ||
+        meet(my.r, bytes(inv_freq, (uint64_t)rot / 2 * 4)))
         return FP4Q_EINVAL;
     fp4q::RotaryArgs a{};
     a.x = x;

@@ -358,7 +358,9 @@ FP4Q_API fp4q_status fp4_quantize_nv_amax(const void *x, int64_t rows, int64_t c
  * element's alignment (rows whose width, pitch and start are multiples of
  * eight elements are the fast ones).  An output may be one of the inputs
  * named at the call, with the same leading dimension, or must not overlap
- * any.  NaN and Inf follow the formulas; they stay within their row, and
+ * any (FP4Q_EINVAL): its memory from the first element to the last must not
+ * meet another argument's, unless both are matrices of the same leading
+ * dimension in different columns, blocks of one buffer.  NaN and Inf follow the formulas; they stay within their row, and
  * within their column of the weight gradients.  Errors as above, plus
  * FP4Q_ESHAPE where rows * ceil(cols / 8) reaches 2^32.
  * ------------------------------------------------------------------------ */

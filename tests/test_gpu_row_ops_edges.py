@@ -74,3 +74,75 @@ def test_rotary_of_heads_of_whole_tokens(n, heads, dim, rot, dtype, half):
     B.fp4_rotary(xv, pos.to(dev), freq.to(dev), y=xv, **args)
     same(xv, y, "in place")
     assert px.untouched()
+
+
+# ---------------------------------------------------------------- column blocks of one buffer
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("rows,cols,gap", [(40, 64, 0), (37, 100, 3), (300, 1001, 0), (1100, 1032, 8), (20, 9000, 1)])
+def test_outputs_in_other_columns_of_the_inputs_buffer(rows, cols, gap, dtype):
+    dev = device()
+    announce(f"column blocks of one buffer {rows}x{cols} gap {gap} {dtype}")
+    n, step = 7, cols + gap
+    buf = torch.full((rows, n * step), 777.0, dtype=dtype, device=dev)
+    block = [buf[:, i * step:i * step + cols] for i in range(n)]
+    ins = [draw((rows, cols), i, dtype).to(dev) for i in range(3)]
+    g = (1 + draw((cols,), 4, F32, 0.2)).to(dev)
+
+    def fill():
+        buf.fill_(777.0)
+        for b, v in zip(block, ins):
+            b.copy_(v)
+
+    def kept(written):
+        m = torch.ones_like(buf, dtype=torch.bool)
+        for i in (0, 1, 2, *written):
+            m[:, i * step:i * step + cols] = False
+        assert bool((buf[m] == 777.0).all())
+        for b, v in zip(block, ins):
+            same(b, v, "an input")
+
+    want = B.fp4_dropout(ins[0], 0.1, seed=SEED, residual=ins[1])
+    fill()
+    B.fp4_dropout(block[0], 0.1, seed=SEED, residual=block[1], y=block[3])
+    same(block[3], want, "dropout")
+    kept((3,))
+    want = B.fp4_norm(ins[0], g, residual=ins[1], p=0.1, seed=SEED, save=True)
+    fill()
+    B.fp4_norm(block[0], g, residual=block[1], p=0.1, seed=SEED, h=block[3], y=block[5])
+    same(block[3], want.h, "h")
+    same(block[5], want.y, "y")
+    kept((3, 5))
+    args = dict(mean=want.mean, rstd=want.rstd, p=0.1, seed=SEED)
+    want = B.fp4_norm_grad(ins[0], ins[1], g, dres=ins[2], **args)
+    fill()
+    got = B.fp4_norm_grad(block[0], block[1], g, dres=block[2], dh=block[4], dx=block[6], **args)
+    for a, b, what in zip(got, want, ("dh", "dx", "dgamma", "dbeta")):
+        same(a, b, what)
+    kept((4, 6))
+    x = ins[0][:, :cols // 32 * 32].contiguous().unflatten(1, (-1, 32))
+    freq, pos = B.rotary_frequencies(32, device=dev)[0], torch.arange(rows, device=dev)
+    want = B.fp4_rotary(x, pos, freq)
+    fill()
+    v = [block[i][:, :cols // 32 * 32].unflatten(1, (-1, 32)) for i in (0, 3)]
+    B.fp4_rotary(v[0], pos, freq, y=v[1])
+    same(v[1], want, "rotary")
+    kept((3,))
+
+
+def test_swiglu_grad_in_other_columns_of_the_inputs_buffer():
+    dev = device()
+    announce("SwiGLU's gradient in column blocks of one buffer")
+    for rows, f in ((33, 64), (300, 2048)):
+        c, dh = draw((rows, 2 * f), 1, BF, 3.0).to(dev), draw((rows, f), 2, BF).to(dev)
+        want = B.fp4_swiglu_grad_bf16(dh, c, want_h=True)
+        buf = torch.full((rows, 7 * f), 777.0, dtype=BF, device=dev)
+        vc, vd, vo, vh = buf[:, :2 * f], buf[:, 2 * f:3 * f], buf[:, 3 * f:5 * f], buf[:, 6 * f:]
+        vc.copy_(c)
+        vd.copy_(dh)
+        B.fp4_swiglu_grad_bf16(vd, vc, dc=vo, h=vh)
+        same(vo, want[0], "dc")
+        same(vh, want[1], "h")
+        same(vc, c, "c")
+        same(vd, dh, "dh")
+        assert bool((buf[:, 5 * f:6 * f] == 777.0).all())

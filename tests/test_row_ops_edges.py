@@ -21,3 +21,65 @@ def test_rotary_takes_heads_of_whole_tokens():
     assert f(xh=6399) == B.ESHAPE and f(yt=64, yh=6399) == B.ESHAPE  # a head's last token meets the next head
     assert f(xt=63, xh=6400) == B.ESHAPE and f(xt=0) == B.ESHAPE and f(xh=-6400) == B.ESHAPE
     assert f(n=0, xt=0) in (B.OK, B.ESHAPE) and f(heads=1, xt=64, xh=64) in RAN
+
+
+def test_outputs_in_other_columns_of_an_inputs_buffer():
+    """Matrices of one pitch whose columns do not meet do not overlap; with
+    another pitch, or a column in common, they may."""
+    L = B.lib()
+    X, far = A[0], A[1]
+
+    def dropout(y, x=X, rows=4, cols=100, ld=256, ldy=256, t=1, res=None):
+        return L.fp4_dropout(x, rows, cols, ld, t, res, ld, 0.1, 1, 0, y, ldy, None)
+
+    assert dropout(X + 200) in RAN and dropout(X + 312) in RAN       # columns 100 and 156 on, of 256
+    assert dropout(X + 198) == B.EINVAL and dropout(X + 314) == B.EINVAL  # a column in common, on the right and (of the next row) the left
+    assert dropout(X - 200) in RAN and dropout(X - 198) == B.EINVAL and dropout(X - 312) in RAN and dropout(X - 314) == B.EINVAL
+    assert dropout(X + 200 + 512) in RAN                              # beside, and a row further on
+    assert dropout(X + 200, ldy=255) == B.EINVAL                      # another pitch
+    assert dropout(X + 400, t=0) in RAN and dropout(X + 396, t=0) == B.EINVAL
+    assert dropout(X, res=X + 200) in RAN and dropout(X + 200, res=X + 200) in RAN and dropout(X + 200, res=X + 202) == B.EINVAL
+
+    def norm(h, y, mean=None):
+        return L.fp4_norm(X, 4, 100, 512, 1, far, 100, 0.1, 1, 0, h, 512, 0, None, None, 0, 1e-5, y, 512, mean, None, None,
+                          None, 0, None)
+
+    assert norm(X + 200, X + 400) in RAN and norm(X, X + 400) in RAN
+    assert norm(X + 200, X + 398) == B.EINVAL and norm(X + 198, X + 400) == B.EINVAL and norm(X + 200, X + 200) == B.EINVAL
+    assert norm(X + 200, X + 400, mean=X + 800) == B.EINVAL           # not a matrix of that pitch
+
+    def grad(dh, dx, dy=X, h=X + 200):
+        return L.fp4_norm_grad(dy, 4, 100, 512, 1, h, 512, None, 0, 1, None, 0, None, far, 0.1, 1, 0, dh, 512, dx, 512, None,
+                               None, None, 0, None)
+
+    assert grad(X + 400, X + 600) in RAN and grad(X, X + 200) in RAN and grad(X + 200, X + 400) in RAN
+    assert grad(X + 400, X + 598) == B.EINVAL and grad(X + 398, X + 600) == B.EINVAL and grad(X + 400, X + 400) == B.EINVAL
+
+    def swiglu(dc, h, c=X, dh=X + 256, ld=512):
+        return L.fp4_swiglu_grad_bf16(dh, 512, c, 16, 64, 512, 32, dc, ld, h, 512, None)
+
+    assert swiglu(X + 384, X + 640) in RAN and swiglu(X, X + 256) in RAN and swiglu(X + 384, None) in RAN
+    assert swiglu(X + 240, None) == B.EINVAL and swiglu(X + 384, X + 624) == B.EINVAL and swiglu(X + 384, X + 112) == B.EINVAL
+    assert swiglu(X + 384, None, ld=520) == B.EINVAL
+
+    def rotary(y, xt=512, xh=64, yt=512, yh=64, n=50):
+        return L.fp4_rotary(X, n, 3, 64, xt, xh, 1, far, 64, A[2], 64, 0, 0, 1.0, y, yt, yh, None)
+
+    assert rotary(X + 384) in RAN and rotary(X + 640) in RAN and rotary(X + 382) == B.EINVAL and rotary(X + 642) == B.EINVAL
+    assert rotary(X + 384, yt=520) == B.EINVAL
+    apart = dict(xt=64, xh=8000, yt=64, yh=8000)                      # heads of 50 tokens at a pitch of 125
+    assert rotary(X + 6400, **apart) in RAN and rotary(X + 6398, **apart) == B.EINVAL and rotary(X + 9600, **apart) in RAN
+    assert rotary(X + 9602, **apart) == B.EINVAL
+
+
+def test_refused_overlaps_are_those_that_share_bytes():
+    """Every start of y around x, against the bytes themselves."""
+    L = B.lib()
+    x = A[0]
+    for rows, cols, ld in ((1, 5, 9), (3, 4, 9), (4, 7, 7), (2, 3, 16)):
+        own = {x + 2 * (r * ld + c) for r in range(rows) for c in range(cols)}
+        for at in range(-2 * rows * ld, 2 * rows * ld + 1):
+            y = x + 2 * at
+            meets = any(y + 2 * (r * ld + c) in own for r in range(rows) for c in range(cols))
+            got = L.fp4_dropout(x, rows, cols, ld, 1, None, 0, 0.1, 1, 0, y, ld, None)
+            assert got in (RAN if not meets or at == 0 else (B.EINVAL,)), (rows, cols, ld, at)
