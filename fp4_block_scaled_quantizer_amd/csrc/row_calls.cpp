@@ -11,8 +11,10 @@
 #include <ATen/core/Tensor.h>
 #include <ATen/ops/empty.h>
 #include <c10/core/StreamGuard.h>
+#include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
 
+#include <exception>
 #include <stdexcept>
 #include <string>
 #include <vector>
@@ -429,8 +431,8 @@ PyObject *entry(PyObject *, PyObject *const *args, Py_ssize_t n)
     } catch (const PythonError &) {
     } catch (const Refused &e) {
         PyErr_SetString(PyExc_ValueError, e.what());
-    } catch (const std::exception &e) {
-        PyErr_SetString(PyExc_RuntimeError, e.what());
+    } catch (...) {  // torch's own, such as memory that its allocator refuses, as torch raises them
+        torch::translate_exception_to_python(std::current_exception());
     }
     return nullptr;
 }

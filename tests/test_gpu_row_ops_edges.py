@@ -146,3 +146,30 @@ def test_swiglu_grad_in_other_columns_of_the_inputs_buffer():
         same(vc, c, "c")
         same(vd, dh, "dh")
         assert bool((buf[:, 5 * f:6 * f] == 777.0).all())
+
+
+# ---------------------------------------------------------------- errors
+
+def test_out_of_memory_is_torchs_own_error():
+    """The allocator refuses the output (its limit is lowered, the GPU has
+    room): the caller gets torch's OutOfMemoryError, and goes on after it."""
+    dev = device()
+    announce("outputs that the allocator refuses")
+    x = torch.zeros((4096, 8192), dtype=BF, device=dev)
+    torch.cuda.synchronize()
+    torch.cuda.empty_cache()
+    one, freq = torch.ones(4096, device=dev), B.rotary_frequencies(64, device=dev)[0]
+    total = torch.cuda.get_device_properties(0).total_memory
+    torch.cuda.set_per_process_memory_fraction((torch.cuda.memory_reserved() + (8 << 20)) / total)
+    try:
+        for call in (lambda: B.fp4_dropout(x, 0.1, seed=1), lambda: B.fp4_norm(x),
+                     lambda: B.fp4_norm_grad(x, x, rstd=one, mean=one),
+                     lambda: B.fp4_swiglu_grad_bf16(x[:, :4096], x),
+                     lambda: B.fp4_rotary(x.view(4096, 128, 64), torch.zeros(4096, dtype=torch.int32, device=dev), freq),
+                     lambda: B.fp4_dropout(x, 0.1, seed=1, stream=torch.cuda.Stream())):
+            with pytest.raises(torch.OutOfMemoryError, match="allocate"):
+                call()
+    finally:
+        torch.cuda.set_per_process_memory_fraction(1.0)
+    assert torch.cuda.current_stream() == torch.cuda.default_stream()
+    assert bool((B.fp4_dropout(x, 0.1, seed=1) == 0).all())
