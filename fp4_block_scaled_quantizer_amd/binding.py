@@ -521,6 +521,10 @@ def fp4_norm(x: torch.Tensor, gamma: Optional[torch.Tensor] = None, beta: Option
     takes; `mx` for the MXFP4 operand of a bf16 y in `layout` (with want_y
     False, instead of y). h and y may each be x or residual."""
     if mx or codes is not None or scales is not None:
+        if not isinstance(x, torch.Tensor):
+            raise ValueError("x must be a tensor")
+        if x.dim() != 2:
+            raise ValueError("x must be a 2-D fp32 or bf16 tensor")
         codes, scales = _mx_outputs(x.shape[0], x.shape[1], layout, codes, scales, x.device, stream)
     y, h, mean, rstd = _rows().norm(x, gamma, beta, kind, eps, residual, p, seed, stream_id, save, want_y, layout, y, h,
                                     mean, rstd, codes, scales, stream)

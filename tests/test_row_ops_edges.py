@@ -83,3 +83,16 @@ def test_refused_overlaps_are_those_that_share_bytes():
             meets = any(y + 2 * (r * ld + c) in own for r in range(rows) for c in range(cols))
             got = L.fp4_dropout(x, rows, cols, ld, 1, None, 0, 0.1, 1, 0, y, ld, None)
             assert got in (RAN if not meets or at == 0 else (B.EINVAL,)), (rows, cols, ld, at)
+
+
+@pytest.mark.parametrize("given", [{}, dict(mx=True), dict(mx=True, layout=B.LAYOUT_TILED),
+                                   dict(codes=torch.zeros(4, dtype=torch.uint8))])
+def test_norm_of_what_is_no_matrix(given):
+    """The same refusal with the operand and without."""
+    x = torch.zeros((4, 128), dtype=torch.bfloat16)
+    for bad in (x[0], x[None], x.half()):
+        with pytest.raises(ValueError):
+            B.fp4_norm(bad, **given)
+    for bad in (None, 3, x.numpy):
+        with pytest.raises(ValueError, match="x must be a tensor"):
+            B.fp4_norm(bad, **given)
