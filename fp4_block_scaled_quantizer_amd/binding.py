@@ -600,4 +600,4 @@ def rotary_frequencies(rot: int, base: float = 10000.0, *, factor: float = 1.0, 
         keep = ((turns - slow_turns) / (fast_turns - slow_turns)).clamp(0, 1)
         freq = freq * (keep + (1 - keep) / factor)
         scale = 1 + 0.1 * math.log(factor)
-    return freq.to(torch.float32).to(device or "cpu"), scale
+    return freq.to(torch.float32).to("cpu" if device is None else device), scale

@@ -96,3 +96,20 @@ def test_norm_of_what_is_no_matrix(given):
     for bad in (None, 3, x.numpy):
         with pytest.raises(ValueError, match="x must be a tensor"):
             B.fp4_norm(bad, **given)
+
+
+@pytest.mark.parametrize("device", [None, 0, 1, "cpu", "cuda:0"])
+def test_rotary_frequencies_go_to_the_device_asked_for(device, monkeypatch):
+    """Index 0 is a device; only None is none."""
+    asked = []
+    to = torch.Tensor.to
+
+    def record(self, *args, **kwargs):
+        if args and args[0] is torch.float32:
+            return to(self, *args, **kwargs)
+        asked.append(args[0])
+        return self
+
+    monkeypatch.setattr(torch.Tensor, "to", record)
+    B.rotary_frequencies(64, device=device)
+    assert asked == ["cpu" if device is None else device]
