@@ -1,6 +1,10 @@
 """Build ``libfp4q.so`` (hand-written HIP for gfx950) in-tree with hipcc, and
 ``_row_calls.so``, the binding's compiled argument marshalling (host C++).
 
+The library needs hipcc alone (``build_library``, or ``--library`` on the
+command line); the marshalling also torch, a host compiler and Python's
+headers, as the binding that it belongs to.
+
 Every source is compiled for gfx950 only, with FMA contraction off (the
 quantizers' binary32 steps must round exactly as written), packed-fp32
 instructions disabled, and HIP's default correctly rounded fp32 division.
@@ -8,6 +12,7 @@ instructions disabled, and HIP's default correctly rounded fp32 division.
 from __future__ import annotations
 
 import concurrent.futures as cf
+import importlib.util
 import os
 import shutil
 import subprocess
@@ -64,23 +69,28 @@ def _row_calls(verbose: bool) -> None:
     libs = os.path.join(os.path.dirname(torch.__file__), "lib")
     includes = [sysconfig.get_paths()["include"], *cpp_extension.include_paths()]
     tmp = ROW_CALLS_OUT + ".tmp"
-    cmd = [shutil.which("g++") or "g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden", "-Wall",
+    cmd = [_host_compiler(), "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden", "-Wall",
            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", *(f"-I{i}" for i in includes),
            os.path.join(CSRC, "row_calls.cpp"), "-o", tmp, f"-L{libs}", "-ltorch_python", "-ltorch_cpu", "-lc10"]
     if verbose:
         print(" ".join(cmd), flush=True)
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
-        raise RuntimeError(f"g++ failed on row_calls.cpp:\n{r.stderr}")
+        raise RuntimeError(f"{cmd[0]} failed on row_calls.cpp:\n{r.stderr}")
     os.replace(tmp, ROW_CALLS_OUT)
 
 
-def build(verbose: bool = False) -> str:
+def _host_compiler() -> str:
+    for cand in ("g++", "c++", "clang++", "/opt/rocm/bin/amdclang++"):
+        if shutil.which(cand):
+            return shutil.which(cand)
+    raise RuntimeError("no host C++ compiler found for row_calls.cpp")
+
+
+def build_library(verbose: bool = False) -> str:
     os.makedirs(BUILD_DIR, exist_ok=True)
-    with cf.ThreadPoolExecutor(max_workers=min(4, len(SOURCES) + 1)) as ex:
-        rows = ex.submit(_row_calls, verbose)
+    with cf.ThreadPoolExecutor(max_workers=min(4, len(SOURCES))) as ex:
         objs = list(ex.map(lambda s: _compile(s, verbose), SOURCES))
-        rows.result()
     tmp = OUT + ".tmp"
     cmd = [hipcc(), "--offload-arch=gfx950", "-shared", "-fPIC", *objs, "-o", tmp]
     if verbose:
@@ -90,5 +100,18 @@ def build(verbose: bool = False) -> str:
     return OUT
 
 
+def build(verbose: bool = False) -> str:
+    """Both. The library is there whatever becomes of the marshalling, which
+    is left out where there is no torch, and so no binding, to use it."""
+    with cf.ThreadPoolExecutor(max_workers=1) as ex:
+        rows = ex.submit(_row_calls, verbose) if importlib.util.find_spec("torch") else None
+        out = build_library(verbose)
+        if rows is not None:
+            rows.result()
+        else:
+            print(f"torch is not installed: {ROW_CALLS_OUT} is not built", flush=True)
+    return out
+
+
 if __name__ == "__main__":
-    print(build(verbose="-v" in sys.argv))
+    print((build_library if "--library" in sys.argv else build)(verbose="-v" in sys.argv))
