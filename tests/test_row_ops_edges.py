@@ -113,3 +113,29 @@ def test_rotary_frequencies_go_to_the_device_asked_for(device, monkeypatch):
     monkeypatch.setattr(torch.Tensor, "to", record)
     B.rotary_frequencies(64, device=device)
     assert asked == ["cpu" if device is None else device]
+
+
+def test_the_workspace_is_that_of_the_shape():
+    """A larger matrix may need less, as the header says; a call takes what
+    the query gave for its own shape, or more, and refuses less."""
+    L = B.lib()
+    need = L.fp4q_norm_grad_workspace_bytes
+    assert need(500, 4096) == 0 and need(500, 3000) == 6_000_000
+    assert need(2000, 32768) < need(2000, 16384)
+
+    def f(rows, cols, given):
+        return L.fp4_norm_grad(A[0], rows, cols, cols, 1, A[1], cols, None, 0, 0, None, 0, A[2], A[3], 0.0, 1, 0, A[4], cols,
+                               None, 0, A[5], A[6], A[7] if given else None, given, None)
+
+    for rows, cols in ((500, 4096), (500, 3000), (2000, 16384), (2000, 32768), (1, 1), (10 ** 5, 64), (800, 9000)):
+        n = need(rows, cols)
+        assert f(rows, cols, n) in RAN and f(rows, cols, n + 1000) in RAN
+        assert n == 0 or f(rows, cols, n - 1) == B.EINVAL
+    assert f(500, 3000, need(500, 4096)) == B.EINVAL
+
+
+def test_the_header_says_that_the_workspace_is_that_of_the_shape():
+    with open(B.HEADER) as f:
+        text = " ".join(f.read().replace("*", " ").split())
+    at = text.index("size_t fp4q_norm_grad_workspace_bytes")
+    assert "a larger matrix may need less (500 x 4096: none, 500 x 3000: 6 MB)" in text[at - 400:at]
