@@ -4,7 +4,9 @@ Argument marshalling only: every step of the quantizers, GEMMs and row-wise
 operators runs in the library's HIP kernels.  PyTorch supplies device memory (``data_ptr()``) and the
 stream (``torch.cuda.current_stream()``, or the one a call names with
 ``stream``, whose memory the outputs made for it then are).  If the library has
-not been built this module raises -- there is no fallback path.
+not been built this module raises -- there is no fallback path.  No call
+records itself for autograd: an input may require grad, the outputs never do,
+and the gradients are calls of their own.
 """
 from __future__ import annotations
 
@@ -495,7 +497,9 @@ def fp4_dropout(x: torch.Tensor, p: float, *, seed: int, stream_id: int = 0, res
                 y: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
     """[residual +] dropout(x): each element is kept with probability 1 - p
     (from 16 random bits of (seed, stream_id, row, column)) and scaled. The
-    gradient is the same call on the gradient. y may be x or residual."""
+    gradient is the same call on the gradient. seed is a number of the host's:
+    a captured graph draws the same mask at every replay. y may be x or
+    residual."""
     return _rows().dropout(x, p, seed, stream_id, residual, y, stream)
 
 

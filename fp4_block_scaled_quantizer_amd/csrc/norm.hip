@@ -262,15 +262,14 @@ __global__ __launch_bounds__(kLanes ? 256 : 1024) void norm_kernel(const NormArg
     for (int i = 0; i < kC; ++i) {
         float v[8], e = 0.0f;
         q[i].get(v);
-        if (kEdge != kWhole && !whole(i)) {
 #pragma unroll
-            for (int j = 0; j < 8; ++j) v[j] = sp[i].own(j) ? v[j] : mean;
+        for (int j = 0; j < 8; ++j) v[j] -= mean;
+        if (kEdge != kWhole && !whole(i)) {  // after the mean is taken off: it may be infinite
+#pragma unroll
+            for (int j = 0; j < 8; ++j) v[j] = sp[i].own(j) ? v[j] : 0.0f;
         }
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            const float c = v[j] - mean;
-            e = __builtin_fmaf(c, c, e);
-        }
+        for (int j = 0; j < 8; ++j) e = __builtin_fmaf(v[j], v[j], e);
         sq += kEdge != kWhole || sp[i].any() ? e : 0.0f;
     }
     const float rstd = 1.0f / __builtin_sqrtf(sum_of(sq, red[1]) * inv_n + a.eps);

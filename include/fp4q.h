@@ -360,9 +360,13 @@ FP4Q_API fp4q_status fp4_quantize_nv_amax(const void *x, int64_t rows, int64_t c
  * named at the call, with the same leading dimension, or must not overlap
  * any (FP4Q_EINVAL): its memory from the first element to the last must not
  * meet another argument's, unless both are matrices of the same leading
- * dimension in different columns, blocks of one buffer.  NaN and Inf follow the formulas; they stay within their row, and
- * within their column of the weight gradients.  Errors as above, plus
- * FP4Q_ESHAPE where rows * ceil(cols / 8) reaches 2^32.
+ * dimension in different columns, blocks of one buffer.  NaN and
+ * Inf follow the formulas; they stay within their row, and within their column
+ * of the weight gradients.  Errors as above, plus FP4Q_ESHAPE where rows *
+ * ceil(cols / 8) reaches 2^32.
+ *
+ * seed and stream_id are the call's, read when it is made: a captured graph
+ * draws the same mask at every replay.
  * ------------------------------------------------------------------------ */
 
 /* Dropout with a mask that is never stored, and an optional residual add:
@@ -382,6 +386,9 @@ FP4Q_API fp4q_status fp4_dropout(const void *x, int64_t rows, int64_t cols, int6
  *   h    = [residual +] dropout(x, p, seed, stream_id), rounded to `type`;
  *   mean = sum h / cols (RMS: 0),  rstd = 1 / sqrt(sum (h - mean)^2 / cols + eps);
  *   y    = (h - mean) * rstd * gamma + beta.
+ * The sums are binary32: a row whose squares sum to 2^128 (one element 1.8e19
+ * from the mean is enough) has rstd 0, and y = beta; a layer norm's row whose
+ * elements sum to it has an infinite mean, and NaN where h is finite.
  * Optional (null): residual, gamma (1), beta (0), and of the outputs h, mean
  * (must be null for RMS), rstd, and y if codes are asked for.  With codes and
  * scales (bf16 only: FP4Q_EUNSUPPORTED for binary32) the MXFP4 operand of y

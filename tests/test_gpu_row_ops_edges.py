@@ -173,3 +173,51 @@ def test_out_of_memory_is_torchs_own_error():
         torch.cuda.set_per_process_memory_fraction(1.0)
     assert torch.cuda.current_stream() == torch.cuda.default_stream()
     assert bool((B.fp4_dropout(x, 0.1, seed=1) == 0).all())
+
+
+# ---------------------------------------------------------------- what overflows
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("cols", [64, 1000, 4096, 6003])
+def test_rows_whose_sums_overflow(cols, dtype):
+    """As the header says: squares that sum to 2^128 give rstd 0 and y = beta,
+    elements that do an infinite mean; other rows are left alone, and the
+    gradient of such rows is 0 or NaN within them."""
+    dev = device()
+    announce(f"rows whose sums overflow, {cols} {dtype}")
+    x = draw((5, cols), 1, dtype)
+    x[1, cols // 2] = 1e30
+    x[2] = 3e38
+    x[3, 0], x[3, 1] = 1e19, -1e19  # squares 2e38: below 2^128
+    b = draw((cols,), 2, dtype)
+    for layer in (True, False):
+        kind = B.NORM_LAYER if layer else B.NORM_RMS
+        bd = b.to(dev)
+        o = B.fp4_norm(x.to(dev), None, bd, kind=kind, save=True)
+        assert o.rstd[1:3].tolist() == [0.0, 0.0]
+        same(o.y[1], b, "y = beta")
+        if layer:
+            assert o.mean[2] == float("inf") and bool(torch.isnan(o.y[2]).all())
+        else:
+            same(o.y[2], b, "y = beta")
+        y, _, rstd, ey, _, er = R.norm(x[[0, 3, 4]], None, b, layer, 1e-5)
+        R.check(o.y[[0, 3, 4]], y, ey, "the other rows")
+        R.check(o.rstd[[0, 3, 4]], rstd[:, 0], er[:, 0], "their rstd")
+        dy = draw((5, cols), 3, dtype).to(dev)
+        g = B.fp4_norm_grad(dy, x.to(dev), kind=kind, mean=o.mean, rstd=o.rstd, weights=False)
+        alone = B.fp4_norm_grad(dy[[0, 3, 4]], x[[0, 3, 4]].to(dev), kind=kind, rstd=o.rstd[[0, 3, 4]],
+                                mean=o.mean[[0, 3, 4]] if layer else None, weights=False)
+        assert bool((g.dh[1] == 0).all())
+        same(g.dh[[0, 3, 4]], alone.dh, "dh of the other rows")
+
+
+def test_no_autograd():
+    """An input may require grad; the outputs do not."""
+    dev = device()
+    announce("inputs that require grad")
+    x = torch.randn((4, 64), device=dev).to(BF).requires_grad_()
+    w = torch.ones(64, device=dev, requires_grad=True)
+    for out in (B.fp4_dropout(x, 0.1, seed=1), B.fp4_norm(x, w).y,
+                B.fp4_norm_grad(x, x, w, rstd=w[:4].detach(), mean=w[:4].detach()).dgamma,
+                B.fp4_rotary(x[:, None], torch.arange(4, device=dev), w.detach()[:32])):
+        assert not out.requires_grad and out.grad_fn is None
