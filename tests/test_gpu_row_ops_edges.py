@@ -221,3 +221,242 @@ def test_no_autograd():
                 B.fp4_norm_grad(x, x, w, rstd=w[:4].detach(), mean=w[:4].detach()).dgamma,
                 B.fp4_rotary(x[:, None], torch.arange(4, device=dev), w.detach()[:32])):
         assert not out.requires_grad and out.grad_fn is None
+
+
+# ---------------------------------------------------------------- NaN and Inf in the fused operand
+
+@pytest.mark.parametrize("cols,layout", [(64, 0), (96, 0), (512, 0), (8192, 0), (128, 1), (256, 1), (1024, 1), (4096, 1),
+                                         (20480, 1)])
+def test_operand_of_nan_and_inf_rows(cols, layout):
+    """Byte for byte what the producer makes of y, NaN and Inf among it."""
+    dev = device()
+    announce(f"operand of NaN and Inf rows, {cols} layout {layout}")
+    x = draw((37, cols), 1, BF)
+    x[1, 3], x[2, cols - 1], x[3, 40], x[6, 5] = float("nan"), float("inf"), -float("inf"), 1e30
+    x[4], x[5], x[7] = float("nan"), float("inf"), 3e38
+    g = torch.ones(cols)
+    g[7], g[9], g[33] = float("nan"), float("inf"), -float("inf")
+    for kind in (B.NORM_LAYER, B.NORM_RMS):
+        for w in (None, g.to(dev)):
+            for res in (None, x.to(dev)):
+                o = B.fp4_norm(x.to(dev), w, kind=kind, residual=res, mx=True, layout=layout)
+                codes, scales = B.fp4_quantize_mx(o.y, layout=layout)
+                assert torch.equal(o.codes, codes) and torch.equal(o.scales, scales)
+                same(o.y, B.fp4_norm(x.to(dev), w, kind=kind, residual=res).y, "y")
+
+
+# ---------------------------------------------------------------- in place at a pitch
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("rows,cols,pad,lead", [(70, 100, 3, 1), (40, 1000, 24, 0), (33, 4096, 8, 0), (9, 5003, 5, 3),
+                                                (700, 2056, 1, 1), (300, 9000, 3, 0), (20, 16392, 7, 1)])
+def test_norm_and_gradient_in_place_at_a_pitch(rows, cols, pad, lead, dtype):
+    """Results in the place of inputs whose rows lie apart; what lies between
+    the rows is not touched."""
+    dev = device()
+    announce(f"norm and gradient in place {rows}x{cols} pad {pad} lead {lead} {dtype}")
+    ins = [draw((rows, cols), i, dtype) for i in range(3)]
+    g = (1 + draw((cols,), 4, F32, 0.2)).to(dev)
+
+    def fresh():
+        return [Padded(rows, cols, dtype, dev, pad, lead, v) for v in ins]
+
+    d = [v.to(dev) for v in ins]
+    want = B.fp4_dropout(d[0], 0.1, seed=SEED, residual=d[1])
+    for i in (0, 1):
+        t = fresh()
+        B.fp4_dropout(t[0].view, 0.1, seed=SEED, residual=t[1].view, y=t[i].view)
+        same(t[i].view, want, f"dropout in place {i}")
+        assert all(v.untouched() for v in t)
+    f = B.fp4_norm(d[0], g, residual=d[1], p=0.1, seed=SEED, save=True)
+    for i, j in ((0, 1), (1, 0)):
+        t = fresh()
+        B.fp4_norm(t[0].view, g, residual=t[1].view, p=0.1, seed=SEED, h=t[i].view, y=t[j].view)
+        same(t[i].view, f.h, f"h in place {i}")
+        same(t[j].view, f.y, f"y in place {j}")
+        assert all(v.untouched() for v in t)
+    args = dict(mean=f.mean, rstd=f.rstd, p=0.1, seed=SEED)
+    want = B.fp4_norm_grad(d[0], d[1], g, dres=d[2], **args)
+    for weights in (True, False):
+        for i, j in ((0, 1), (1, 2), (2, 0)):
+            t = fresh()
+            o = B.fp4_norm_grad(t[0].view, t[1].view, g, dres=t[2].view, dh=t[i].view, dx=t[j].view, weights=weights, **args)
+            same(t[i].view, want.dh, f"dh in place {i}")
+            same(t[j].view, want.dx, f"dx in place {j}")
+            if weights:
+                same(o.dgamma, want.dgamma, "dgamma")
+                same(o.dbeta, want.dbeta, "dbeta")
+            assert all(v.untouched() for v in t)
+
+
+@pytest.mark.parametrize("M,F,pair,pad", [(33, 64, 32, 8), (70, 2048, 2048, 24), (300, 72, 8, 16), (9, 4104, 4104, 8)])
+def test_swiglu_grad_in_place_at_a_pitch(M, F, pair, pad):
+    dev = device()
+    announce(f"SwiGLU's gradient in place {M}x{F} pair {pair} pad {pad}")
+    c, dh = draw((M, 2 * F), 1, BF, 3.0), draw((M, F), 2, BF)
+    want = B.fp4_swiglu_grad_bf16(dh.to(dev), c.to(dev), pair=pair, want_h=True)
+    pc, pd = Padded(M, 2 * F, BF, dev, pad, 0, c), Padded(M, F, BF, dev, pad, 0, dh)
+    B.fp4_swiglu_grad_bf16(pd.view, pc.view, pair=pair, dc=pc.view, h=pd.view)
+    same(pc.view, want[0], "dc in place of c")
+    same(pd.view, want[1], "h in place of dh")
+    assert pc.untouched() and pd.untouched()
+
+
+@pytest.mark.parametrize("half", [True, False])
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("n,heads,dim,rot,gap", [(33, 40, 128, 128, 1024), (7, 3, 80, 40, 8), (5, 2, 96, 36, 3),
+                                                 (6, 5, 100, 50, 28), (1100, 3, 48, 48, 16), (9, 4, 24, 14, 1)])
+def test_rotary_in_place_at_a_pitch(n, heads, dim, rot, gap, half, dtype):
+    """As inside a fused QKV output: the elements from rot on, and what lies
+    behind the heads, stay as they are."""
+    dev = device()
+    announce(f"rotary in place {dtype} {n}x{heads}x{dim} rot {rot} gap {gap} half {half}")
+    x = draw((n, heads, dim), n + dim, dtype)
+    pos = torch.randint(0, 1 << 18, (n,), generator=torch.Generator().manual_seed(n)).to(dev)
+    args = dict(style=B.ROTARY_HALF if half else B.ROTARY_INTERLEAVED, scale=1.25)
+    freq = B.rotary_frequencies(rot, 500000.0, device=dev)[0]
+    want = B.fp4_rotary(x.to(dev), pos, freq, **args)
+    p = Padded(n, heads * dim, dtype, dev, gap, 0, x.reshape(n, -1))
+    v = p.view.unflatten(1, (heads, dim))
+    assert not v.is_contiguous()
+    B.fp4_rotary(v, pos, freq, y=v, **args)
+    same(v, want, "in place")
+    same(v[..., rot:], x[..., rot:], "elements from rot on")
+    assert p.untouched()
+
+
+# ---------------------------------------------------------------- far positions
+
+@pytest.mark.parametrize("half", [True, False])
+def test_rotary_positions_up_to_2_31(half):
+    """Against sine and cosine of the angle's fraction of a turn, from integers:
+    a frequency is f = m 2^-s exactly, and the position's product with it and
+    the turns of 2 pi are taken at 200 bits. The kernel's own turns are off by
+    2^-53 of themselves twice (the frequency over 2 pi, and its product with
+    the position): at 2^31 positions and frequency 1, 2^31 / 2 pi 2^-52 turns,
+    2^-21 radians."""
+    from fractions import Fraction
+
+    dev = device()
+    announce(f"rotary at positions up to 2^31, half {half}")
+    pos = [2 ** 29 - 3, 2 ** 30 + 1, 2 ** 31 - 1, -(2 ** 31), 2 ** 31 + 5]
+    freq, _ = B.rotary_frequencies(64, 10000.0)
+    # 2 pi to 200 bits, by Machin's formula
+    one = 1 << 260
+
+    def arctan_inverse(q):
+        total, term, k = 0, one // q, 0
+        while term:
+            total += (-1) ** k * (term // (2 * k + 1))
+            term //= q * q
+            k += 1
+        return total
+
+    two_pi = Fraction(2 * 4 * (4 * arctan_inverse(5) - arctan_inverse(239)), one)
+    angle = np.empty((len(pos), 32))
+    for i, p in enumerate(pos):
+        for j, f in enumerate(freq.double().tolist()):
+            turns = Fraction(p) * Fraction(f) / two_pi
+            angle[i, j] = float((turns - round(turns)) * two_pi)
+    x = draw((len(pos), 2, 64), 1, F32)
+    v = x.double().numpy()
+    ia = np.arange(32) if half else 2 * np.arange(32)
+    ib = ia + 32 if half else ia + 1
+    c, s = np.cos(angle)[:, None], np.sin(angle)[:, None]
+    a, b = v[..., ia], v[..., ib]
+    want, e = np.empty_like(v), np.empty_like(v)
+    want[..., ia], want[..., ib] = a * c - b * s, b * c + a * s
+    # row_ref.rotary's bound, and the turns
+    e[..., ia] = e[..., ib] = (np.abs(a) + np.abs(b)) * (10 * R.U + 2.0 ** -20)
+    style = B.ROTARY_HALF if half else B.ROTARY_INTERLEAVED
+    R.check(B.fp4_rotary(x.to(dev), torch.tensor(pos, device=dev), freq.to(dev), style=style), want, e, "y")
+    few = torch.tensor(pos[:4], dtype=torch.int32, device=dev)
+    R.check(B.fp4_rotary(x[:4].to(dev), few, freq.to(dev), style=style), want[:4], e[:4], "y, 32-bit positions")
+
+
+# ---------------------------------------------------------------- launches with a second grid dimension
+
+def free_gib(dev):
+    torch.cuda.synchronize()
+    torch.cuda.empty_cache()
+    return torch.cuda.mem_get_info(dev)[0] / 2 ** 30
+
+
+def test_norm_past_2_20_workgroups():
+    """2^24 + 77 rows of eight, sixteen to a workgroup, and 2^20 + 9 rows of a
+    workgroup each: as the same rows in smaller calls, whose launches have one
+    dimension."""
+    dev = device()
+    announce("norm past 2^20 workgroups")
+    if free_gib(dev) < 24:
+        pytest.skip("needs 24 GiB")
+    for rows, cols in ((2 ** 24 + 77, 8), (2 ** 20 + 9, 1032)):
+        g = torch.Generator(device=dev).manual_seed(1)
+        x = torch.randn((rows, cols), generator=g, device=dev).to(BF)
+        w = (1 + torch.randn((cols,), generator=g, device=dev) / 8).to(BF)
+        whole = B.fp4_norm(x, w, save=True)
+        grad = B.fp4_norm_grad(whole.y, x, w, mean=whole.mean, rstd=whole.rstd, weights=False).dh
+        for lo in range(0, rows, rows // 5 + 1):
+            part = slice(lo, min(rows, lo + rows // 5 + 1))
+            o = B.fp4_norm(x[part], w, save=True)
+            for a, b in ((whole.y[part], o.y), (whole.mean[part], o.mean), (whole.rstd[part], o.rstd)):
+                assert torch.equal(a, b), (rows, cols, lo)
+            d = B.fp4_norm_grad(o.y, x[part], w, mean=o.mean, rstd=o.rstd, weights=False).dh
+            assert torch.equal(grad[part], d), (rows, cols, lo)
+
+
+def test_norm_operand_past_2_20_workgroups():
+    """The tiled operand, whose workgroups are permuted in runs of 256 rows."""
+    dev = device()
+    announce("norm's tiled operand past 2^20 workgroups")
+    if free_gib(dev) < 24:
+        pytest.skip("needs 24 GiB")
+    rows, cols = 2 ** 20 + 300, 1152
+    x = torch.randn((rows, cols), generator=torch.Generator(device=dev).manual_seed(2), device=dev).to(BF)
+    o = B.fp4_norm(x, mx=True, layout=B.LAYOUT_TILED)
+    codes, scales = B.fp4_quantize_mx(o.y, layout=B.LAYOUT_TILED)
+    assert torch.equal(o.codes, codes) and torch.equal(o.scales, scales)
+
+
+def test_rotary_past_2_20_workgroups():
+    dev = device()
+    announce("rotary past 2^20 workgroups")
+    if free_gib(dev) < 24:
+        pytest.skip("needs 24 GiB")
+    n = 2 ** 27 + 1000  # one pair each, 128 to a workgroup
+    x = torch.randn((n, 1, 2), generator=torch.Generator(device=dev).manual_seed(3), device=dev).to(BF)
+    pos = torch.arange(n, dtype=torch.int32, device=dev)
+    freq = torch.ones(1, device=dev)
+    y = B.fp4_rotary(x, pos, freq)
+    for lo in range(0, n, n // 5 + 1):
+        part = slice(lo, min(n, lo + n // 5 + 1))
+        assert torch.equal(y[part], B.fp4_rotary(x[part], pos[part], freq)), lo
+
+
+def test_swiglu_grad_past_2_31_chunks():
+    """2^28 + 40 rows of 64: rows at the start, around the second dimension's
+    first and at the end, against calls on those rows alone. dc takes c's place
+    (the rest of the memory holds whatever it holds)."""
+    dev = device()
+    announce("SwiGLU's gradient past 2^31 chunks")
+    if free_gib(dev) < 160:
+        pytest.skip("needs 160 GiB")
+    rows, f = 2 ** 28 + 40, 64
+    c = torch.empty((rows, 2 * f), dtype=BF, device=dev)
+    dh = torch.empty((rows, f), dtype=BF, device=dev)
+    for want_h in (False, True):
+        want = []
+        parts = [slice(0, 100), slice(2 ** 28 - 50, 2 ** 28 + 20), slice(rows - 10, rows)]
+        for i, part in enumerate(parts):
+            n = part.stop - part.start
+            ci, di = draw((n, 2 * f), 2 * i, BF, 2.0).to(dev), draw((n, f), 2 * i + 1, BF).to(dev)
+            c[part], dh[part] = ci, di
+            want.append((ci, di))
+        want = [B.fp4_swiglu_grad_bf16(di, ci, want_h=True) for ci, di in want]
+        B.fp4_swiglu_grad_bf16(dh, c, dc=c, h=dh if want_h else None)
+        for part, (dc, h) in zip(parts, want):
+            assert torch.equal(c[part], dc)
+            if want_h:
+                assert torch.equal(dh[part], h)
+    del c, dh
+    torch.cuda.empty_cache()
