@@ -165,9 +165,13 @@ int launch_rotary(RotaryArgs a, hipStream_t st)
     const uint32_t turned = a.interleaved ? (a.rot + 7) / 8 : angles / 8;
     const uint32_t per_head = turned + (a.copy ? (a.dim - a.rot + 7) / 8 : 0), per_token = per_head * a.heads;
     // four tokens to a workgroup, or as many as give its threads an item each
-    // (one head of 64, 16384 tokens: 4.4 us, four tokens at once 6.2), but at
-    // least about four workgroups to a compute unit
-    const int64_t cap = (kThreads + per_token - 1) / per_token;
+    // (one head of 64, 65536 tokens: 8.7 us, four tokens at once 18.9), but at
+    // least about four workgroups to a compute unit. Binary32 items of the half
+    // style, 64 bytes in and out, go to half the threads (16384 tokens of two
+    // heads of 128: 9.8 us, to all 11.0, four tokens 10.2; of three 14.6, 16.0,
+    // 13.2; interleaved, 32 bytes, to all 10.4, to half 10.9)
+    const int64_t items = a.bf16 || a.interleaved ? kThreads : kThreads / 2;
+    const int64_t cap = (items + per_token - 1) / per_token;
     int64_t at_once = kAngles / angles;
     if (at_once > (cap > 4 ? cap : 4)) at_once = cap > 4 ? cap : 4;
     while (at_once > 1 && (a.tokens + at_once - 1) / at_once < 1024) at_once >>= 1;

@@ -460,3 +460,21 @@ def test_swiglu_grad_past_2_31_chunks():
                 assert torch.equal(dh[part], h)
     del c, dh
     torch.cuda.empty_cache()
+
+
+# ---------------------------------------------------------------- sizes on either side of a rule
+
+@pytest.mark.parametrize("half", [True, False])
+@pytest.mark.parametrize("n,heads,dim", [(8192, 2, 64), (4100, 3, 64), (2050, 2, 128), (20000, 1, 64), (1030, 6, 128), (5000, 4, 32)])
+def test_rotary_few_heads(n, heads, dim, half):
+    """Few heads, where a workgroup's tokens go by type and style: bf16 and
+    binary32, against the binary64 form."""
+    dev = device()
+    announce(f"rotary of few heads {n}x{heads}x{dim} half {half}")
+    pos = torch.randint(0, 1 << 18, (n,), generator=torch.Generator().manual_seed(n))
+    freq, _ = B.rotary_frequencies(dim, 500000.0)
+    for dtype in (BF, F32):
+        x = draw((n, heads, dim), n + dim, dtype)
+        want, e = R.rotary(x, pos, freq, half, False, 1.0)
+        style = B.ROTARY_HALF if half else B.ROTARY_INTERLEAVED
+        R.check(B.fp4_rotary(x.to(dev), pos.to(dev), freq.to(dev), style=style), want, e, "y")
