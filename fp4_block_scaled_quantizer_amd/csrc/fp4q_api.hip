@@ -685,7 +685,10 @@ fp4q_status fp4_norm(const void *x, int64_t rows, int64_t cols, int64_t ld_x, in
 
 size_t fp4q_norm_grad_workspace_bytes(int64_t rows, int64_t cols)
 {
-    return rows_cols_ok(rows, cols) && cols <= kMaxNormCols ? fp4q::norm_grad_workspace_bytes(rows, cols) : 0;
+    if (!rows_cols_ok(rows, cols) || cols > kMaxNormCols) return 0;
+    // enough for either type
+    const size_t f = fp4q::norm_grad_workspace_bytes(rows, cols, false), b = fp4q::norm_grad_workspace_bytes(rows, cols, true);
+    return f > b ? f : b;
 }
 
 fp4q_status fp4_norm_grad(const void *dy, int64_t rows, int64_t cols, int64_t ld_dy, int type, const void *h,
@@ -708,7 +711,7 @@ fp4q_status fp4_norm_grad(const void *dy, int64_t rows, int64_t cols, int64_t ld
     const uint64_t es = type_size(type), ws = type_size(w_type);
     if (rows > 0) {
         if (!dy || !h || !rstd || (kind == FP4Q_NORM_LAYER && !mean) || (!dh && !dx && !sums)) return FP4Q_EINVAL;
-        const size_t need = sums ? fp4q::norm_grad_workspace_bytes(rows, cols) : 0;
+        const size_t need = sums ? fp4q::norm_grad_workspace_bytes(rows, cols, type == FP4Q_OUT_BF16) : 0;
         if (need > 0 && (!workspace || workspace_bytes < need)) return FP4Q_EINVAL;
         if (!aligned(dy, es) || !aligned(h, es) || !aligned(dres, es) || !aligned(dh, es) || !aligned(dx, es) ||
             !aligned(gamma, ws) || !aligned(mean, 4) || !aligned(rstd, 4) || (need > 0 && !aligned(workspace, 16)))

@@ -127,7 +127,7 @@ int launch_swiglu(const void *c, int64_t M, int64_t F, int64_t ldc, int64_t pair
                   hipStream_t st);
 int launch_dropout(const DropoutArgs &a, hipStream_t st);
 int launch_norm(const NormArgs &a, hipStream_t st);
-size_t norm_grad_workspace_bytes(int64_t rows, int64_t cols);
+size_t norm_grad_workspace_bytes(int64_t rows, int64_t cols, bool bf16);
 int launch_norm_grad(NormGradArgs a, float *dgamma, float *dbeta, hipStream_t st);
 int launch_swiglu_grad(const SwigluGradArgs &a, hipStream_t st);
 int launch_rotary(RotaryArgs a, hipStream_t st);

@@ -705,11 +705,12 @@ __global__ __launch_bounds__(1024) void norm_grad_weights_kernel(const float *__
 //   in the rows' own kernel (kInRows), each workgroup leaving its own;
 //   beside it (kBeside) in workgroups of their own, which read the rows again:
 //     few rows, where the workgroups' sums are as many as the rows and a
-//     second launch costs more than the reading.  The row counts are where
-//     the two meet, bf16 beside / in rows: 96 x 1024 4.3 / 7.9 us, 768 x 4096
-//     13.2 / 13.6, 400 x 5000 11.5 / 12.2, but 512 x 5000 (10 of 16 waves)
-//     14.8 / 12.8, 1000 x 1000 12.9 / 10.6; two chunks a thread 256 x 16384
-//     13.4 / 24.0, 640 x 12000 25.4 / 31.4, 768 x 8192 20.7 / 19.7;
+//     second launch costs more than the reading.  The row counts are about
+//     where the two meet, beside / in rows: bf16 96 x 1024 4.8 / 8.2 us, 768 x
+//     4096 12.7 / 13.5, 768 x 8192 19.0 / 20.3, 400 x 5000 (10 of 16 waves)
+//     11.0 / 14.2, 512 x 5000 14.0 / 15.0, but 1000 x 1000 13.2 / 11.0; two
+//     chunks a thread 256 x 16384 12.0 / 25.0, 640 x 12000 22.5 / 25.6;
+//     binary32 in 16 waves 640 x 8192 22.8 / 22.6, 768 x 8192 27.3 / 23.9;
 //   by a kernel of their own before the rows' (kApart): rows too wide for a
 //     workgroup to keep their sums (beside / apart 1024 x 20000 66 / 78, 2048
 //     x 20000 123 / 122, 4096 x 16392 226 / 206), and in place of kBeside
@@ -727,7 +728,7 @@ struct GradPlan {
     uint32_t waves, groups;
     int64_t row_blocks, parts;
 };
-GradPlan grad_plan(int64_t rows, int64_t cols, bool sums)
+GradPlan grad_plan(int64_t rows, int64_t cols, bool bf16, bool sums)
 {
     const int64_t waves1 = (cols + 511) / 512;  // waves of a row at one chunk per thread
     GradPlan g{};
@@ -737,10 +738,10 @@ GradPlan grad_plan(int64_t rows, int64_t cols, bool sums)
     g.lanes = lanes_of(cols);
     g.groups = 16 / g.waves * (64 / g.lanes);
     const int64_t need = (rows + g.groups - 1) / g.groups;
-    const int64_t few = g.chunks_per_thread == 4   ? 1024
-                        : g.chunks_per_thread == 2 ? 640
-                        : 16 % g.waves == 0        ? 768
-                                                   : 400;
+    const int64_t few = g.chunks_per_thread == 4                                ? 1024
+                        : g.chunks_per_thread == 2 || (g.waves == 16 && !bf16) ? 640
+                        : 16 % g.waves == 0                                     ? 768
+                                                                                : 400;
     if (sums)
         g.sums = rows <= few ? kBeside : g.chunks_per_thread == 4 ? kApart : kInRows;
     else
@@ -842,16 +843,16 @@ int launch_norm(const NormArgs &a, hipStream_t st)
     return hipGetLastError() == hipSuccess ? 0 : 1;
 }
 
-size_t norm_grad_workspace_bytes(int64_t rows, int64_t cols)
+size_t norm_grad_workspace_bytes(int64_t rows, int64_t cols, bool bf16)
 {
-    return rows <= 0 || cols <= 0 ? 0 : (size_t)grad_plan(rows, cols, true).parts * 2u * (size_t)cols * sizeof(float);
+    return rows <= 0 || cols <= 0 ? 0 : (size_t)grad_plan(rows, cols, bf16, true).parts * 2u * (size_t)cols * sizeof(float);
 }
 
 int launch_norm_grad(NormGradArgs a, float *dgamma, float *dbeta, hipStream_t st)
 {
     const Dropout d = dropout_of(a.p, a.seed, a.stream_id);
     const bool sums = dgamma || dbeta;
-    const GradPlan g = grad_plan(a.rows, a.cols, sums);
+    const GradPlan g = grad_plan(a.rows, a.cols, a.bf16, sums);
     a.waves = g.waves;
     a.groups = g.groups;
     a.row_blocks = (uint32_t)g.row_blocks;

@@ -405,7 +405,8 @@ FP4Q_API fp4q_status fp4_norm(const void *x, int64_t rows, int64_t cols, int64_t
 /* Bytes of device workspace fp4_norm_grad needs for its weight gradients, for
  * these rows and columns: a larger matrix may need less (500 x 4096: none, 500
  * x 3000: 6 MB), so ask for each shape, or take the largest answer of all that
- * a buffer is to serve. */
+ * a buffer is to serve.  Enough for either type; a call refuses only what is
+ * too little for its own. */
 FP4Q_API size_t fp4q_norm_grad_workspace_bytes(int64_t rows, int64_t cols);
 
 /* The gradient of fp4_norm.  With xh = (h - mean) * rstd and g = dy * gamma:

@@ -478,3 +478,25 @@ def test_rotary_few_heads(n, heads, dim, half):
         want, e = R.rotary(x, pos, freq, half, False, 1.0)
         style = B.ROTARY_HALF if half else B.ROTARY_INTERLEAVED
         R.check(B.fp4_rotary(x.to(dev), pos.to(dev), freq.to(dev), style=style), want, e, "y")
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("rows,cols", [(640, 8192), (641, 8192), (768, 7700), (769, 8192)])
+def test_norm_grad_on_either_side_of_the_row_counts(rows, cols, dtype):
+    """Weight sums beside the rows and in them, by type, in place too."""
+    dev = device()
+    announce(f"norm gradient {rows}x{cols} {dtype}")
+    h, dy, dres = (draw((rows, cols), i, dtype, 2.0) for i in range(3))
+    g = 1 + draw((cols,), 4, F32, 0.2)
+    _, mean, rstd, _, _, _ = R.norm(h, g, None, True, 1e-5)
+    mean, rstd = (torch.from_numpy(v[:, 0]).float() for v in (mean, rstd))
+    dh, dg, db, edh, edg, edb = R.norm_grad(dy, h, g, mean, rstd, True, dres)
+    args = dict(mean=mean.to(dev), rstd=rstd.to(dev))
+    o = B.fp4_norm_grad(dy.to(dev), h.to(dev), g.to(dev), dres=dres.to(dev), **args)
+    R.check(o.dh, dh, edh, "dh")
+    R.check(o.dgamma, dg, edg, "dgamma")
+    R.check(o.dbeta, db, edb, "dbeta")
+    u = dy.to(dev)
+    q = B.fp4_norm_grad(u, h.to(dev), g.to(dev), dres=dres.to(dev), dh=u, **args)
+    for a, b in zip((u, q.dgamma, q.dbeta), (o.dh, o.dgamma, o.dbeta)):
+        same(a, b, "in place")

@@ -139,3 +139,21 @@ def test_the_header_says_that_the_workspace_is_that_of_the_shape():
         text = " ".join(f.read().replace("*", " ").split())
     at = text.index("size_t fp4q_norm_grad_workspace_bytes")
     assert "a larger matrix may need less (500 x 4096: none, 500 x 3000: 6 MB)" in text[at - 400:at]
+
+
+def test_the_workspace_serves_either_type():
+    """Binary32 rows of 16 waves keep weight sums in the workspace from 641
+    rows on, bf16 from 769 on; the query does not know the type."""
+    L = B.lib()
+    need = L.fp4q_norm_grad_workspace_bytes
+
+    def f(rows, cols, t, given):
+        return L.fp4_norm_grad(A[0], rows, cols, cols, t, A[1], cols, None, 0, 0, None, 0, A[2], A[3], 0.0, 1, 0, A[4], cols,
+                               None, 0, A[5], A[6], A[7] if given else None, given, None)
+
+    for rows, cols in ((641, 8192), (768, 8192), (700, 7700)):
+        assert need(rows, cols) == 256 * 2 * cols * 4
+        assert f(rows, cols, B.OUT_F32, need(rows, cols)) in RAN and f(rows, cols, B.OUT_BF16, need(rows, cols)) in RAN
+        assert f(rows, cols, B.OUT_F32, 0) == B.EINVAL and f(rows, cols, B.OUT_BF16, 0) in RAN
+    assert need(640, 8192) == 0 and need(768, 4096) == 0 and need(768, 7680) == 256 * 2 * 7680 * 4
+    assert f(769, 8192, B.OUT_BF16, 0) == B.EINVAL
