@@ -5,8 +5,8 @@
 // HBM-bound: each input read and the output written once.  A thread takes
 // kPerThread chunks of eight elements, kThreads apart, and makes their random
 // words (one Philox call of ten rounds per chunk, about half the time that
-// the memory takes) while the loads are under way.  8192 x 14336 bf16: 75.8
-// us, 6.2 TB/s, as without dropout (p = 0: 75 us); 64 x 4096: 4.2 us a call,
+// the memory takes) while the loads are under way.  8192 x 14336 bf16: 75.4
+// us, 6.2 TB/s, as without dropout (p = 0: 75.2); 64 x 4096: 4.0 us a call,
 // launch and latency.
 #include <hip/hip_runtime.h>
 #include <stdint.h>

@@ -14,13 +14,16 @@
 // 16384; at 1024 and below a wave per row, at 256 half a wave and at 128, the
 // norms of single heads, a quarter), many workgroups to a compute unit, so
 // that one row's loads run under another's sums and stores.
-// Measured on rows that do not fit the caches, of a copy's 6.3 TB/s:
-//   8192 x 4096 bf16, layer norm, dropout, residual: 44.5 us, 6.0 TB/s;
-//   327680 x 128 bf16, layer norm: 30.0 us, 5.6 TB/s (a wave per row 80; 32768
-//   x 256: half a wave 9.1, a wave 12.6);
-//   1537 x 5003 binary32, layer norm: 13.4 us, 4.6 TB/s (all rows resident
-//   at once: the loads of all, then the stores of all);
-//   1 x 4096 bf16: 4.5 us a call, launch and latency.
+// Measured a call, matrices from memory, where a copy reaches 6.3 TB/s:
+//   8192 x 4096 bf16, layer norm, dropout, residual: 44.7 us, 6.0 TB/s;
+//   327680 x 128 bf16, layer norm: 32.9 us, 5.2 TB/s (a wave per row 80; 32768
+//   x 256 9.4, a wave per row 12.6);
+//   1537 x 5003 binary32, layer norm: 18.6 us, 3.3 TB/s, or 13.4 where three
+//   such in turn fit the last-level cache (1536 rows at once, six workgroups
+//   to a compute unit: the loads of all, the stores of all, and one row more);
+//   4097 x 4099 bf16: 23.9 us, 2.8 TB/s (rows share cache lines, and two chunks
+//   a thread leave a fifth of the places empty);
+//   1 x 4096 bf16: 4.8 us a call, launch and latency.
 //
 // Gradient, with xh = (h - mean) rstd and g = dy gamma:
 //   dh = [dres +] rstd (g - sum g / n - xh sum(g xh) / n) (RMS: no second
@@ -30,11 +33,16 @@
 // workspace and a second kernel adds them in a fixed order (no atomics: two
 // runs give the same bits).  More workgroups would hide more latency but
 // leave more sums to write and read: 512 took 69 us where 256 take 63.
-//   8192 x 4096 bf16, layer norm, dropout, dres: 63.9 us, 5.3 TB/s (59 us
-//   the rows, 5 the second kernel); 2047 x 14336 binary32: 77.9 us, 4.5 TB/s
+//   8192 x 4096 bf16, layer norm, dropout, dres: 64.6 us, 5.2 TB/s (62.6 the
+//   rows' kernel, 4.9 the second); 2047 x 14336 binary32: 77.2 us, 4.6 TB/s
 //   (eight rows to a compute unit, of which the first one's loads and the
-//   sums' 59 MB are not hidden); 327680 x 128 bf16, dres: 64.0 us, 5.3 TB/s (a
-//   wave per row 94); 96 x 1024: 4.6 us a call.
+//   sums' 59 MB are not hidden); 327680 x 128 bf16, dres: 63.7 us, 5.3 TB/s (a
+//   wave per row 94); 96 x 1024: 4.8 us a call.
+// Above 8192 columns some kernels do not fit a workgroup's 128 registers and
+// spill: two chunks a thread up to 46 (16384 columns bf16 with dres and dropout
+// 19: 4096 rows 145 us, 4.6 TB/s), four chunks up to 16 for bf16 and 63 for
+// binary32, ragged 131 (4096 x 24000 bf16 199 us, 4096 x 24001 508: there the
+// rows' kernel moves more than three times its rows' bytes).
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 

@@ -13,9 +13,10 @@
 // A workgroup evaluates them once per token, into LDS, for all its heads,
 // while its first elements are on their way.
 // HBM-bound: each element read and written once.  8192 tokens x 40 heads x
-// 128 bf16 out of QKV rows: 28.6 us, 5.9 TB/s (interleaved 29.2; angles
-// before loads and plain loads 37); 32 tokens: 3.9 us a call, launch and
-// latency.
+// 128 bf16 out of QKV rows, from memory: 32.8 us, 5.1 TB/s; on three sets in
+// turn, which the last-level cache holds in part, 28.6 (angles before loads and
+// plain loads 37).  Interleaved 35.6, heads of whole tokens 35.0, both from
+// memory.  32 tokens: 4.2 us a call, launch and latency.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -33,9 +34,10 @@ constexpr int kAngles = 1024;  // angles of a workgroup: tokens * pairs, pairs r
 // made: kAgain, as the part's last eight elements, some of them a second
 // time; kOwn, in place, the same but stored without those, which their
 // chunk may have turned already; kShort, parts below eight, element by
-// element.  kOwn against element by element for all rests in place: 8192 x 32
-// heads, 24 of 96 turned, half style 19.0 / 29.3 us; 50 of 100, interleaved
-// 32.6 / 30.1.
+// element.  kOwn against element by
+// element for all rests in place, 8192 x 32 heads bf16: half style, 24 of 96
+// turned 19.1 / 29.1 us; interleaved, 100 of 100 24.7 / 35.4, 50 of 100 30.8 /
+// 30.5, 250 of 256 72.1 / 67.8.
 enum Rest { kAgain, kOwn, kShort };
 template <typename T, Rest kRest, bool kNt>
 __device__ __forceinline__ void load8(const T *p, uint32_t n, Chunk<T> &q)

@@ -8,7 +8,7 @@
 // thread takes eight hidden columns of one row: three 16-byte loads and two
 // or three stores, whose pieces of 64 bytes (pair = 32) the caches join, so
 // nothing is streamed past them (non-temporal loads: 250 us instead of 237).
-// 8192 x 14336 with h: 237 us, 5.9 TB/s; without h 195 us, 6.0 TB/s; 64 x
+// 8192 x 14336 with h: 238 us, 5.9 TB/s; without h 196 us, 6.0 TB/s; 64 x
 // 14336: 4.2 us a call, launch and latency.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
