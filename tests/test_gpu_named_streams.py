@@ -173,3 +173,42 @@ def test_streams_of_a_handle_and_of_nothing():
             B.fp4_quantize_mx(x, stream=bad)
     assert torch.equal(B.fp4_dropout(x, 0.2, seed=3), want[0])
     torch.cuda.synchronize()
+
+
+def test_named_streams_in_a_captured_graph():
+    """Calls on a stream forked off the captured one: every replay as the eager
+    calls on its inputs."""
+    dev = device()
+    announce("named streams in a captured graph")
+    rows, cols = 1200, 1024  # the gradient needs a workspace
+    g = torch.Generator().manual_seed(1)
+    x, r = (torch.randn((rows, cols), generator=g).to(BF).to(dev) for _ in range(2))
+    w = (1 + torch.randn((cols,), generator=g) / 8).to(dev)
+    side = torch.cuda.Stream()
+
+    def step(**s):
+        f = B.fp4_norm(x, w, residual=r, p=0.1, seed=1, save=True, mx=True, layout=T, **s)
+        d = B.fp4_norm_grad(f.y, f.h, w, mean=f.mean, rstd=f.rstd, p=0.1, seed=1, **s)
+        c, e = B.fp4_quantize_mx(d.dx, layout=T, **s)
+        return [f.y, f.codes, f.scales, d.dh, d.dgamma, d.dbeta, B.fp4_dropout(d.dh, 0.2, seed=2, **s), c, e]
+
+    def forked():
+        side.wait_stream(torch.cuda.current_stream())
+        out = step(stream=side)
+        torch.cuda.current_stream().wait_stream(side)
+        return out
+
+    forked()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = forked()
+    for k in range(3):
+        x.copy_(torch.randn((rows, cols), generator=g).to(BF))
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        got = [t.clone() for t in out]
+        want = step()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got, want)), k
