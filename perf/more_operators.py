@@ -1,0 +1,489 @@
+"""Measured cases of the operators on 8-bit block-scaled rows and of the
+products of few rows with 4-bit weights: activations packed to 8 bits and back,
+a norm that leaves its result packed, the gradients that read packed
+activations, and matrix-vector products with MXFP4 and NVFP4 weights.
+
+`run` computes an operator in its plain form (elementary torch operations in
+binary32) or, with `own` set, by the library's calls; `exact` is the same
+operator from its definition in binary64.
+"""
+import math
+
+import torch
+
+own = False
+
+EPS = 1e-5
+TYPES = {"bf16": torch.bfloat16, "f32": torch.float32}
+
+# A micro-batch is 8192 tokens; model width 4096, fused QKV width 6144, MLP
+# width 14336 (gate and up together 28672).
+MAX_ROW_WORK = 8192 * 4096
+MAX_MLP_WORK = 8192 * 28672
+MAX_WEIGHTS = 28672 * 4096
+
+
+def listed():
+    return [
+        # training: the gate/up GEMM's output of a micro-batch, kept in 8 bits for the backward pass
+        dict(name="pack, micro-batch", op="pack", rows=8192, cols=28672, type="bf16", pad=0),
+        # backward: a short sequence's layer input brought back for the weight gradient's producer
+        dict(name="unpack, short", op="unpack", rows=1537, cols=4096, type="bf16"),
+        # serving: residual add and norm of the one token being decoded, its result in 8 bits for the linear layer
+        dict(name="packing norm, one token", op="norm", rows=1, cols=4096, type="bf16", kind="rms", residual=True, pad=0),
+        # training: the same over a micro-batch, the result kept for the backward pass
+        dict(name="packing norm, micro-batch", op="norm", rows=8192, cols=4096, type="bf16", kind="rms", residual=True,
+             pad=0),
+        # a short sequence's gradient in a narrow model
+        dict(name="norm gradient, few rows", op="norm_grad", rows=96, cols=1024, type="bf16", kind="rms", dres=False),
+        # training: the norm's gradient over a micro-batch whose normed rows were kept in 8 bits
+        dict(name="norm gradient, micro-batch", op="norm_grad", rows=8192, cols=4096, type="bf16", kind="layer",
+             dres=True),
+        # the MLP's gradient for a short sequence
+        dict(name="swiglu gradient, short", op="swiglu_grad", rows=64, f=14336, pair=32, want_h=False),
+        # the MLP's gradient for a micro-batch, the hidden activations recomputed for the weight's gradient
+        dict(name="swiglu gradient, micro-batch", op="swiglu_grad", rows=8192, f=14336, pair=32, want_h=True),
+        # decoding: the attention's output projection of one token
+        dict(name="matvec, one token", op="matvec", m=1, n=4096, k=4096, weights="mx", layout="tiled", x="bf16",
+             out="bf16"),
+        # decoding: the gate/up projection of one token
+        dict(name="matvec, MLP", op="matvec", m=1, n=28672, k=4096, weights="mx", layout="tiled", x="bf16", out="bf16"),
+        # verifying a few drafted tokens: the down projection with NVFP4 weights as a checkpoint holds them
+        dict(name="matvec, NVFP4", op="matvec", m=5, n=4096, k=14336, weights="nv", layout="linear", x="bf16",
+             out="bf16"),
+        # serving a batch: the gate/up projection of 32 sequences' tokens that the norm left in 8 bits
+        dict(name="matvec, 8-bit rows", op="matvec", m=32, n=28672, k=4096, weights="mx", layout="tiled", x="pack8",
+             out="bf16"),
+    ]
+
+
+def _log(rng, lo, hi):
+    return max(lo, min(hi, int(round(math.exp(rng.uniform(math.log(lo), math.log(hi)))))))
+
+
+def draw(rng):
+    op = rng.choice(["pack", "unpack", "norm", "norm", "norm_grad", "norm_grad", "swiglu_grad", "matvec", "matvec",
+                     "matvec", "matvec"])
+    if op in ("pack", "unpack"):
+        cols = 32 * _log(rng, 1, 896)
+        case = dict(op=op, rows=_log(rng, 1, min(32768, MAX_MLP_WORK // (2 * cols))), cols=cols,
+                    type=rng.choice(["bf16", "bf16", "f32"]))
+        return dict(case, pad=rng.choice([0, 0, 8, 24])) if op == "pack" else case
+    if op in ("norm", "norm_grad"):
+        cols = 32 * _log(rng, 2, 512)
+        case = dict(op=op, rows=_log(rng, 1, min(8192, MAX_ROW_WORK // (2 * cols))), cols=cols,
+                    type=rng.choice(["bf16", "bf16", "f32"]), kind=rng.choice(["layer", "rms", "rms"]))
+        case["residual" if op == "norm" else "dres"] = rng.random() < 0.5
+        return dict(case, pad=rng.choice([0, 0, 8, 24])) if op == "norm" else case
+    if op == "swiglu_grad":
+        f = 32 * _log(rng, 2, 448)
+        return dict(op=op, rows=_log(rng, 1, min(8192, MAX_MLP_WORK // (2 * f))), f=f, pair=rng.choice([32, f]),
+                    want_h=rng.random() < 0.5)
+    k = 128 * _log(rng, 2, 112)
+    weights = rng.choice(["mx", "mx", "nv", "nv tile"])
+    return dict(op=op, m=rng.choice([1, 1, 2, 3, 4, 8, 13, 16, 24, 32]), n=_log(rng, 64, min(28672, MAX_WEIGHTS // k)),
+                k=k, weights=weights, layout=rng.choice(["tiled", "tiled", "linear"]),
+                x=rng.choice(["bf16", "pack8"]) if weights == "mx" else "bf16", out=rng.choice(["bf16", "bf16", "f32"]))
+
+
+# ---------------------------------------------------------------- inputs
+
+def _rows(g, rows, cols, pad, dtype, scale=1.0, outliers=False):
+    """A [rows x cols] view with `pad` unused elements after each row: N(0, scale^2), with outliers one in a thousand
+    entries fifty times as large, as activations have them."""
+    x = torch.randn((rows, cols + pad), generator=g, device="cuda").mul_(scale)
+    if outliers:
+        x = torch.where(torch.rand((rows, cols + pad), generator=g, device="cuda") < 1e-3, 50.0 * x, x)
+    return x.to(dtype)[:, :cols]
+
+
+def _weights(g, s):
+    """FP4 weights of N(0, 1 / k) in the format and layout asked for."""
+    n, k, nv = s["n"], s["k"], s["weights"] != "mx"
+    stored = (n + 31) // 32 * 32 if s["layout"] == "tiled" else n
+    block = 16 if nv else 32
+    w = torch.randn((n, k // block, block), generator=g, device="cuda").div_(math.sqrt(k))
+    amax = w.abs().amax(2)
+    if nv:  # the tensor scale puts the largest block scale on E4M3's largest value
+        if s["weights"] == "nv":
+            ts = (amax.max() / 2688).reshape(1)
+            wide = ts.expand(n, k // 128)
+        else:
+            pad = torch.nn.functional.pad(amax, (0, 0, 0, -n % 128))
+            ts = pad.view(-1, 128, k // 128, 8).amax((1, 3)) / 2688
+            wide = ts.repeat_interleave(128, 0)[:n]
+        s["tensor_scale"] = ts
+        wide = wide.repeat_interleave(8, 1)
+        e4m3 = (amax / 6 / wide).clamp(2.0 ** -9, 448).to(torch.float8_e4m3fn)
+        scale, bits = e4m3.float() * wide, e4m3.view(torch.uint8)
+    else:
+        e = (torch.frexp(amax)[1] - 3).clamp(-127, 127)
+        scale, bits = torch.ldexp(torch.ones_like(amax), e), (e + 127).to(torch.uint8)
+    w = w.div_(scale[..., None])
+    code = torch.bucketize(w.abs(), torch.tensor([0.25, 0.75, 1.25, 1.75, 2.5, 3.5, 5.0], device="cuda"),
+                           out_int32=True).to(torch.uint8)
+    code = torch.where(w < 0, code + 8, code).view(n, k)
+    codes = torch.zeros((stored, k // 2), dtype=torch.uint8, device="cuda")
+    codes[:n] = code[:, 0::2] | code[:, 1::2] << 4
+    scales = torch.zeros((stored, k // block), dtype=torch.uint8, device="cuda")
+    scales[:n] = bits
+    if s["layout"] == "tiled":
+        if nv:
+            codes = codes.view(-1, 32, k // 128, 64).transpose(1, 2)
+            scales = scales.view(-1, 32, k // 128, 8).transpose(1, 2)
+        else:
+            codes = codes.view(-1, 32, k // 64, 2, 16).permute(0, 2, 3, 1, 4)
+            scales = scales.view(stored, k // 128, 4).transpose(0, 1)
+    # the shapes that the library's producers give
+    tiled_mx = s["layout"] == "tiled" and not nv
+    s["codes"] = codes.reshape(stored, k // 2)
+    s["scales"] = scales.reshape((k // 128, stored, 4) if tiled_mx else (stored, k // block))
+
+
+def prepare(case, seed):
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    op, s = case["op"], dict(case)
+    if op == "matvec":
+        _weights(g, s)
+        x = _rows(g, s["m"], s["k"], 0, torch.bfloat16, outliers=True)
+        if s["x"] == "pack8":
+            s["x_codes"], s["x_scales"] = _packed(x)
+        else:
+            s["x"] = x
+        s["y"] = torch.empty((s["m"], s["n"]), dtype=TYPES[s["out"]], device="cuda")
+        return s
+    if op == "swiglu_grad":
+        m, f = s["rows"], s["f"]
+        s["codes"], s["scales"] = _packed(_rows(g, m, 2 * f, 0, torch.bfloat16, scale=1.5))
+        s["dh"] = _rows(g, m, f, 0, torch.bfloat16, scale=1e-3)
+        s["dc"] = torch.empty((m, 2 * f), dtype=torch.bfloat16, device="cuda")
+        s["h"] = torch.empty((m, f), dtype=torch.bfloat16, device="cuda") if s["want_h"] else None
+        return s
+    rows, cols, dt = s["rows"], s["cols"], TYPES[s["type"]]
+    room = lambda t=dt, w=cols: torch.empty((rows, w), dtype=t, device="cuda")  # noqa: E731
+    if op in ("norm", "norm_grad"):
+        layer = s["kind"] == "layer"
+        s["gamma"] = (1 + 0.1 * torch.randn(cols, generator=g, device="cuda")).to(dt)
+        s["beta"] = (0.1 * torch.randn(cols, generator=g, device="cuda")).to(dt) if layer else None
+    if op in ("pack", "norm"):
+        s["x"] = _rows(g, rows, cols, s["pad"], dt, outliers=True)
+        s["codes"], s["scales"] = room(torch.uint8), room(torch.uint8, cols // 32)
+    if op == "norm":
+        s["res"] = _rows(g, rows, cols, s["pad"], dt, scale=2.0) if s["residual"] else None
+        s["sum"] = room() if s["residual"] else None
+        s["mean"] = room(torch.float32, 1)[:, 0] if layer else None
+        s["rstd"] = room(torch.float32, 1)[:, 0]
+    elif op == "unpack":
+        s["codes"], s["scales"] = _packed(_rows(g, rows, cols, 0, torch.bfloat16, outliers=True))
+        s["y"] = room()
+    elif op == "norm_grad":
+        h = _rows(g, rows, cols, 0, dt, scale=2.0, outliers=True)
+        s["codes"], s["scales"] = _packed(h)
+        v = h.double()  # the statistics that the forward pass kept are those of the rows themselves
+        mean = v.mean(1, keepdim=True) if layer else torch.zeros_like(v[:, :1])
+        s["mean"] = mean[:, 0].float() if layer else None
+        s["rstd"] = ((v - mean).square().mean(1) + EPS).rsqrt().float()
+        s["dy"] = _rows(g, rows, cols, 0, dt, scale=1e-3)
+        s["res"] = _rows(g, rows, cols, 0, dt, scale=1e-3) if s["dres"] else None
+        s["dh"] = room()
+        s["dgamma"] = torch.empty(cols, dtype=torch.float32, device="cuda")
+        s["dbeta"] = torch.empty(cols, dtype=torch.float32, device="cuda") if layer else None
+    return s
+
+
+# ---------------------------------------------------------------- plain forms
+
+def _packed(x):
+    """(E4M3 codes [rows, cols], E8M0 scale bytes [rows, cols / 32]): the scale is the smallest power of two that
+    brings the block's largest finite magnitude to 448 or below."""
+    v = x.float().unflatten(1, (-1, 32))
+    finite = v.isfinite()
+    amax = torch.where(finite, v.abs(), 0.0).amax(2)
+    m, e = torch.frexp(amax)
+    e = torch.where(amax > 0, (e - 9 + (m > 0.875)).clamp(-127, 119), -127)
+    y = torch.ldexp(v, -e[..., None]).clamp(-448, 448)
+    codes = torch.where(finite, y, math.nan).to(torch.float8_e4m3fn).flatten(1)
+    return codes.view(torch.uint8), (e + 127).to(torch.uint8)
+
+
+def _values(codes, scales):
+    """What packed rows stand for, in binary32."""
+    v = codes.view(torch.float8_e4m3fn).float().unflatten(1, (-1, 32))
+    return torch.ldexp(v, scales[..., None].to(torch.int32) - 127).flatten(1)
+
+
+def _packed_out(codes, scales):
+    return {"codes": codes.view(torch.float8_e4m3fn), "scales": scales.view(torch.float8_e8m0fnu)}
+
+
+def _plain_pack(s):
+    return _packed_out(*_packed(s["x"]))
+
+
+def _plain_unpack(s):
+    return {"y": _values(s["codes"], s["scales"]).to(TYPES[s["type"]])}
+
+
+def _plain_norm(s):
+    dt = s["x"].dtype
+    h = s["x"] if s["res"] is None else (s["x"].float() + s["res"].float()).to(dt)
+    v = h.float()
+    mean = v.mean(1, keepdim=True) if s["kind"] == "layer" else torch.zeros_like(v[:, :1])
+    d = v - mean
+    rstd = (d.square().mean(1, keepdim=True) + EPS).rsqrt()
+    y = d * rstd * s["gamma"].float()
+    if s["beta"] is not None:
+        y = y + s["beta"].float()
+    out = dict(_packed_out(*_packed(y.to(dt))), rstd=rstd[:, 0])
+    if s["res"] is not None:
+        out["h"] = h
+    if s["kind"] == "layer":
+        out["mean"] = mean[:, 0]
+    return out
+
+
+def _plain_norm_grad(s):
+    dy, h, rstd = s["dy"].float(), _values(s["codes"], s["scales"]), s["rstd"][:, None]
+    layer = s["kind"] == "layer"
+    xhat = (h - s["mean"][:, None] if layer else h) * rstd
+    g = dy * s["gamma"].float()
+    d = g - xhat * (g * xhat).mean(1, keepdim=True)
+    if layer:
+        d = d - g.mean(1, keepdim=True)
+    dh = d * rstd
+    if s["res"] is not None:
+        dh = dh + s["res"].float()
+    out = {"dh": dh.to(s["dy"].dtype), "dgamma": (dy * xhat).sum(0)}
+    if layer:
+        out["dbeta"] = dy.sum(0)
+    return out
+
+
+def _plain_swiglu_grad(s):
+    m, f, pair = s["rows"], s["f"], s["pair"]
+    c = _values(s["codes"], s["scales"]).reshape(m, f // pair, 2, pair)
+    g, u, dh = c[:, :, 0], c[:, :, 1], s["dh"].float().reshape(m, f // pair, pair)
+    sig = 1 / (1 + torch.exp(-g))
+    dc = torch.stack((dh * u * (sig * (1 + g * (1 - sig))), dh * (g * sig)), 2)
+    out = {"dc": dc.to(torch.bfloat16).reshape(m, 2 * f)}
+    if s["want_h"]:
+        out["h"] = (g * sig * u).to(torch.bfloat16).reshape(m, f)
+    return out
+
+
+def _linear(s):
+    """The weights' codes [n, k / 2] and scales [n, k / block] in row order."""
+    n, k, codes, scales = s["n"], s["k"], s["codes"], s["scales"]
+    if s["layout"] == "tiled":
+        if s["weights"] == "mx":
+            codes = codes.view(-1, k // 64, 2, 32, 16).permute(0, 3, 1, 2, 4).reshape(-1, k // 2)
+            scales = scales.view(k // 128, -1, 4).transpose(0, 1).reshape(-1, k // 32)
+        else:
+            codes = codes.view(-1, k // 128, 32, 64).transpose(1, 2).reshape(-1, k // 2)
+            scales = scales.view(-1, k // 128, 32, 8).transpose(1, 2).reshape(-1, k // 16)
+    return codes[:n], scales[:n]
+
+
+def _plain_matvec(s):
+    n, k = s["n"], s["k"]
+    codes, scales = _linear(s)
+    grid = torch.tensor([0, 0.5, 1, 1.5, 2, 3, 4, 6, -0.0, -0.5, -1, -1.5, -2, -3, -4, -6], device="cuda")
+    w = grid[torch.stack((codes & 15, codes >> 4), -1).view(n, k).to(torch.int32)]
+    if s["weights"] == "mx":
+        scale = torch.ldexp(torch.ones((), device="cuda"), scales.to(torch.int32) - 127)
+    else:
+        scale = scales.view(torch.float8_e4m3fn).float()
+        ts = s["tensor_scale"]
+        scale = scale * (ts if s["weights"] == "nv" else ts.repeat_interleave(128, 0)[:n].repeat_interleave(8, 1))
+    w = (w.view(n, scale.shape[1], -1) * scale[..., None]).view(n, k)
+    x = _values(s["x_codes"], s["x_scales"]) if s["x"] == "pack8" else s["x"].float()
+    return {"y": (x @ w.t()).to(TYPES[s["out"]])}
+
+
+# ---------------------------------------------------------------- the library's calls
+
+def _own_pack(s):
+    from fp4_block_scaled_quantizer_amd import binding as B
+    return _packed_out(*B.fp4_pack8(s["x"], codes=s["codes"], scales=s["scales"]))
+
+
+def _own_unpack(s):
+    from fp4_block_scaled_quantizer_amd import binding as B
+    return {"y": B.fp4_unpack8(s["codes"], s["scales"], y=s["y"])}
+
+
+def _own_norm(s):
+    from fp4_block_scaled_quantizer_amd import binding as B
+    o = B.fp4_norm_pack8(s["x"], s["gamma"], s["beta"], kind=B.NORM_LAYER if s["kind"] == "layer" else B.NORM_RMS,
+                         eps=EPS, residual=s["res"], h=s["sum"], mean=s["mean"], rstd=s["rstd"], codes8=s["codes"],
+                         scales8=s["scales"])
+    out = dict(_packed_out(o.codes8, o.scales8), rstd=o.rstd)
+    if s["res"] is not None:
+        out["h"] = o.h
+    if s["kind"] == "layer":
+        out["mean"] = o.mean
+    return out
+
+
+def _own_norm_grad(s):
+    from fp4_block_scaled_quantizer_amd import binding as B
+    o = B.fp4_norm_grad_pack8(s["dy"], s["codes"], s["scales"], s["gamma"],
+                              kind=B.NORM_LAYER if s["kind"] == "layer" else B.NORM_RMS, mean=s["mean"], rstd=s["rstd"],
+                              dres=s["res"], dh=s["dh"], dgamma=s["dgamma"], dbeta=s["dbeta"])
+    out = {"dh": o.dh, "dgamma": o.dgamma}
+    if s["kind"] == "layer":
+        out["dbeta"] = o.dbeta
+    return out
+
+
+def _own_swiglu_grad(s):
+    from fp4_block_scaled_quantizer_amd import binding as B
+    dc, h = B.fp4_swiglu_grad_pack8(s["dh"], s["codes"], s["scales"], pair=s["pair"], dc=s["dc"], h=s["h"])
+    return {"dc": dc, "h": h} if s["want_h"] else {"dc": dc}
+
+
+def _own_matvec(s):
+    from fp4_block_scaled_quantizer_amd import binding as B
+    layout = B.LAYOUT_TILED if s["layout"] == "tiled" else B.LAYOUT_LINEAR
+    if s["weights"] != "mx":
+        return {"y": B.fp4_matvec_nv(s["x"], s["codes"], s["scales"], s["tensor_scale"],
+                                     B.NV_GLOBAL if s["weights"] == "nv" else B.NV_TILE128, layout=layout, y=s["y"])}
+    if s["x"] == "pack8":
+        return {"y": B.fp4_matvec_mx_pack8(s["x_codes"], s["x_scales"], s["codes"], s["scales"], layout=layout,
+                                           y=s["y"])}
+    return {"y": B.fp4_matvec_mx(s["x"], s["codes"], s["scales"], layout=layout, y=s["y"])}
+
+
+PLAIN = dict(pack=_plain_pack, unpack=_plain_unpack, norm=_plain_norm, norm_grad=_plain_norm_grad,
+             swiglu_grad=_plain_swiglu_grad, matvec=_plain_matvec)
+OWN = dict(pack=_own_pack, unpack=_own_unpack, norm=_own_norm, norm_grad=_own_norm_grad, swiglu_grad=_own_swiglu_grad,
+           matvec=_own_matvec)
+
+
+def run(state):
+    return (OWN if own else PLAIN)[state["op"]](state)
+
+
+def work(case):
+    op = case["op"]
+    if op == "matvec":  # codes, scales, [tensor scales]; x, y
+        m, n, k = case["m"], case["n"], case["k"]
+        moved = n * k // 2 + n * k // (32 if case["weights"] == "mx" else 16)
+        if case["weights"] != "mx":
+            moved += 4 * ((n + 127) // 128 * (k // 128) if case["weights"] == "nv tile" else 1)
+        moved += m * k * 33 // 32 if case["x"] == "pack8" else 2 * m * k
+        return dict(bytes=moved + m * n * (2 if case["out"] == "bf16" else 4), flops=2 * m * n * k)
+    if op == "swiglu_grad":  # dh, packed c; dc, [h]
+        n = case["rows"] * case["f"]
+        return dict(bytes=n * (2 + 2 + 4 + 2 * case["want_h"]) + n // 16, flops=14 * n)
+    n, e = case["rows"] * case["cols"], 2 if case["type"] == "bf16" else 4
+    packed = n + n // 32
+    layer = case.get("kind") == "layer"
+    if op in ("pack", "unpack"):
+        return dict(bytes=n * e + packed, flops=3 * n)
+    if op == "norm":  # x, [residual, h], packed y; gamma, [beta]; rstd, [mean]
+        moved = n * e * (1 + 2 * case["residual"]) + packed
+        return dict(bytes=moved + (1 + layer) * (case["cols"] * e + case["rows"] * 4), flops=13 * n)
+    # dy, packed h, [dres], dh; gamma, dgamma, [dbeta]; rstd, [mean]
+    moved = n * e * (2 + case["dres"]) + packed
+    return dict(bytes=moved + case["cols"] * (e + 4 + 4 * layer) + case["rows"] * 4 * (1 + layer), flops=16 * n)
+
+
+# ---------------------------------------------------------------- the definitions in 64 bits
+
+def _f64(t):
+    return t.to(torch.float64)
+
+
+def _e4m3(bits):
+    """E4M3 from its fields: (-1)^s 2^(e - 7) (1 + m / 8), or 2^-6 m / 8 where e is 0."""
+    b = bits.to(torch.int16)
+    e, m = b >> 3 & 15, _f64(b & 7) / 8
+    v = torch.where(e == 0, m * 2.0 ** -6, (1 + m) * torch.exp2(_f64(e) - 7))
+    return torch.where(b >= 128, -v, v)
+
+
+def _unpacked(codes, scales):
+    return _e4m3(codes) * torch.exp2(_f64(scales) - 127).repeat_interleave(32, 1)
+
+
+def _block_unit(y):
+    """2^E of each element's block: E the least integer with amax <= 448 * 2^E, from the definition."""
+    amax = y.abs().unflatten(1, (-1, 32)).amax(2)
+    e = torch.ceil(torch.log2(amax / 448))
+    e = torch.where(torch.exp2(e) * 448 < amax, e + 1, torch.where(torch.exp2(e - 1) * 448 >= amax, e - 1, e))
+    return torch.exp2(e.clamp(-127, 119)).repeat_interleave(32, 1)
+
+
+def exact(case, seed):
+    s = prepare(case, seed)
+    op = case["op"]
+    if op == "pack":  # a scale is a step of the largest value: it has no value of more bits
+        x = _f64(s["x"])
+        return {"codes": x.div_(_block_unit(x)), "scales": None}
+    if op == "unpack":
+        return {"y": _unpacked(s["codes"], s["scales"])}
+    if op == "norm":
+        h = _f64(s["x"]) if s["res"] is None else _f64(s["x"]) + _f64(s["res"])
+        v = _f64(h.to(s["x"].dtype))  # the statistics are those of h as it is kept
+        n = case["cols"]
+        mu = v.sum(1) / n if case["kind"] == "layer" else torch.zeros(case["rows"], dtype=torch.float64, device="cuda")
+        inv = 1 / torch.sqrt(((v - mu[:, None]) ** 2).sum(1) / n + EPS)
+        y = (v - mu[:, None]) * (inv[:, None] * _f64(s["gamma"])[None])
+        if s["beta"] is not None:
+            y = y + _f64(s["beta"])
+        # the scales are those of y in its type
+        out = {"codes": y / _block_unit(_f64(y.to(s["x"].dtype))), "scales": None, "rstd": inv}
+        if s["res"] is not None:
+            out["h"] = h
+        if case["kind"] == "layer":
+            out["mean"] = mu
+        return out
+    if op == "norm_grad":
+        # with xhat and g = dy gamma the row's Jacobian is rstd (I - 1 1^T / n - xhat xhat^T / n)
+        n, inv = case["cols"], _f64(s["rstd"])
+        xhat = _unpacked(s["codes"], s["scales"])
+        if case["kind"] == "layer":
+            xhat = xhat - _f64(s["mean"])[:, None]
+        xhat = xhat * inv[:, None]
+        dy = _f64(s["dy"])
+        g = dy * _f64(s["gamma"])
+        along = (g * xhat).sum(1) / n
+        level = g.sum(1) / n if case["kind"] == "layer" else torch.zeros_like(along)
+        dh = inv[:, None] * (g - level[:, None] - xhat * along[:, None])
+        if s["res"] is not None:
+            dh = dh + _f64(s["res"])
+        out = {"dh": dh, "dgamma": (dy * xhat).sum(0)}
+        if case["kind"] == "layer":
+            out["dbeta"] = dy.sum(0)
+        return out
+    if op == "swiglu_grad":  # h = u g sigma(g), d(g sigma)/dg = sigma + g sigma (1 - sigma)
+        f, pair = case["f"], case["pair"]
+        cols = torch.arange(f, device="cuda")
+        at = cols // pair * 2 * pair + cols % pair
+        c = _unpacked(s["codes"], s["scales"])
+        g, u, dh = c[:, at], c[:, at + pair], _f64(s["dh"])
+        sig = torch.sigmoid(g)
+        c[:, at + pair] = dh * g * sig
+        c[:, at] = dh * u * (sig + g * sig * (1 - sig))
+        return {"dc": c, "h": u * g * sig} if case["want_h"] else {"dc": c}
+    # y = x w^T, 2048 rows of w at a time
+    x = _unpacked(s["x_codes"], s["x_scales"]) if case["x"] == "pack8" else _f64(s["x"])
+    codes, scales = _linear(s)
+    n, k, y = case["n"], case["k"], []
+    for at in range(0, n, 2048):
+        c = codes[at:at + 2048].to(torch.int16)
+        c = torch.stack((c % 16, c // 16), 2).reshape(len(c), k)
+        mag = c % 8
+        # E2M1: 2^(e - 1) (1 + m / 2), or m / 2 where e is 0
+        v = torch.where(mag < 2, _f64(mag) / 2, torch.exp2(_f64(mag // 2) - 1) * (1 + _f64(mag % 2) / 2))
+        v = torch.where(c >= 8, -v, v)
+        part = scales[at:at + 2048]
+        unit = torch.exp2(_f64(part) - 127) if case["weights"] == "mx" else _e4m3(part)
+        if case["weights"] == "nv":
+            unit = unit * _f64(s["tensor_scale"])
+        elif case["weights"] == "nv tile":
+            tile = torch.arange(at, at + len(c), device="cuda") // 128
+            unit = unit * _f64(s["tensor_scale"])[tile].repeat_interleave(8, 1)
+        y.append(x @ (v * unit.repeat_interleave(k // unit.shape[1], 1)).t())
+    return {"y": torch.cat(y, 1)}
