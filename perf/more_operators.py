@@ -137,7 +137,7 @@ def _weights(g, s):
     # the shapes that the library's producers give
     tiled_mx = s["layout"] == "tiled" and not nv
     s["codes"] = codes.reshape(stored, k // 2)
-    s["scales"] = scales.reshape((k // 128, stored, 4) if tiled_mx else (stored, k // block))
+    s["scales"] = scales.reshape((k // 128, stored, 4) if tiled_mx else (stored, k // block)).contiguous()
 
 
 def prepare(case, seed):
@@ -347,11 +347,11 @@ def _own_matvec(s):
     layout = B.LAYOUT_TILED if s["layout"] == "tiled" else B.LAYOUT_LINEAR
     if s["weights"] != "mx":
         return {"y": B.fp4_matvec_nv(s["x"], s["codes"], s["scales"], s["tensor_scale"],
-                                     B.NV_GLOBAL if s["weights"] == "nv" else B.NV_TILE128, layout=layout, y=s["y"])}
+                                     B.NV_GLOBAL if s["weights"] == "nv" else B.NV_TILE128, layout=layout, n=s["n"], y=s["y"])}
     if s["x"] == "pack8":
         return {"y": B.fp4_matvec_mx_pack8(s["x_codes"], s["x_scales"], s["codes"], s["scales"], layout=layout,
-                                           y=s["y"])}
-    return {"y": B.fp4_matvec_mx(s["x"], s["codes"], s["scales"], layout=layout, y=s["y"])}
+                                           n=s["n"], y=s["y"])}
+    return {"y": B.fp4_matvec_mx(s["x"], s["codes"], s["scales"], layout=layout, n=s["n"], y=s["y"])}
 
 
 PLAIN = dict(pack=_plain_pack, unpack=_plain_unpack, norm=_plain_norm, norm_grad=_plain_norm_grad,
