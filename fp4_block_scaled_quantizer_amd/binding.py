@@ -88,6 +88,17 @@ def lib() -> ctypes.CDLL:
                                 vp, i64, vp, vp, vp, ctypes.c_size_t, vp]
     L.fp4_swiglu_grad_bf16.argtypes = [vp, i64, vp, i64, i64, i64, i64, vp, i64, vp, i64, vp]
     L.fp4_rotary.argtypes = [vp, i64, i64, i64, i64, i64, i32, vp, i32, vp, i64, i32, i32, f32, vp, i64, i64, vp]
+    L.fp4_pack8.argtypes = [vp, i64, i64, i64, i32, vp, vp, vp]
+    L.fp4_unpack8.argtypes = [vp, vp, i64, i64, vp, i64, i32, vp]
+    L.fp4_norm_pack8.argtypes = [*L.fp4_norm.argtypes[:-1], vp, vp, vp]
+    L.fp4_norm_grad_pack8.argtypes = [vp, i64, i64, i64, i32, vp, vp, *L.fp4_norm_grad.argtypes[7:]]
+    L.fp4_swiglu_grad_pack8.argtypes = [vp, i64, vp, vp, i64, i64, i64, vp, i64, vp, i64, vp]
+    L.fp4_matvec_mx.argtypes = [vp, i64, i64, i64, vp, vp, i64, f32, i32, vp, i32, i64, vp]
+    L.fp4_matvec_mx_pack8.argtypes = [vp, vp, i64, i64, vp, vp, i64, f32, i32, vp, i32, i64, vp]
+    L.fp4_matvec_nv.argtypes = [vp, i64, i64, i64, vp, vp, vp, i32, i64, f32, i32, vp, i32, i64, vp]
+    for fn in ("fp4_pack8", "fp4_unpack8", "fp4_norm_pack8", "fp4_norm_grad_pack8", "fp4_swiglu_grad_pack8",
+               "fp4_matvec_mx", "fp4_matvec_mx_pack8", "fp4_matvec_nv"):
+        getattr(L, fn).restype = i32
     for fn in ("fp4_dropout", "fp4_norm", "fp4_norm_grad", "fp4_swiglu_grad_bf16", "fp4_rotary"):
         getattr(L, fn).restype = i32
     for fn in ("fp4_quantize_mx", "fp4_hadamard32_quantize", "fp4_quantize_mx_dual", "fp4_quantize_nv",
@@ -487,8 +498,9 @@ def _rows():
                 "`python -c 'import __graft_entry__ as g; g.build()'`") from e
         at = [ctypes.cast(getattr(L, f), ctypes.c_void_p).value for f in
               ("fp4_dropout", "fp4_norm", "fp4q_norm_grad_workspace_bytes", "fp4_norm_grad", "fp4_swiglu_grad_bf16",
-               "fp4_rotary")]
-        calls.bind(*at, Fp4qError, torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream, torch.cuda.ExternalStream)
+               "fp4_rotary", "fp4_pack8", "fp4_unpack8", "fp4_norm_pack8", "fp4_norm_grad_pack8",
+               "fp4_swiglu_grad_pack8", "fp4_matvec_mx", "fp4_matvec_mx_pack8", "fp4_matvec_nv")]
+        calls.bind(tuple(at), Fp4qError, torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream, torch.cuda.ExternalStream)
         _row_calls, _row_lib = calls, L
     return _row_calls
 
@@ -605,3 +617,112 @@ def rotary_frequencies(rot: int, base: float = 10000.0, *, factor: float = 1.0, 
         freq = freq * (keep + (1 - keep) / factor)
         scale = 1 + 0.1 * math.log(factor)
     return freq.to(torch.float32).to("cpu" if device is None else device), scale
+
+
+# ---- 8-bit block-scaled rows, and products of few rows with FP4 weights
+
+def fp4_pack8(x: torch.Tensor, *, codes: Optional[torch.Tensor] = None, scales: Optional[torch.Tensor] = None,
+              stream=None) -> Tuple[torch.Tensor, torch.Tensor]:
+    """x (fp32 or bf16 rows, a multiple of 32 wide) in 8 bits: E4M3 codes
+    [rows, cols] and E8M0 scales [rows, cols / 32], both uint8 (views as
+    torch.float8_e4m3fn and torch.float8_e8m0fnu have the values). No finite
+    element saturates; NaN and infinities become NaN."""
+    return _rows().pack8(x, codes, scales, stream)
+
+
+def fp4_unpack8(codes: torch.Tensor, scales: torch.Tensor, *, out_dtype=torch.bfloat16,
+                y: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """The values of packed rows, in y's type or out_dtype (fp32 or bf16)."""
+    return _rows().unpack8(codes, scales, _out_type(out_dtype), y, stream)
+
+
+def _out_type(dtype) -> int:
+    if dtype not in (torch.float32, torch.bfloat16):
+        raise ValueError("out_dtype must be torch.float32 or torch.bfloat16")
+    return OUT_F32 if dtype == torch.float32 else OUT_BF16
+
+
+class NormPack8(NamedTuple):
+    """fp4_norm_pack8's outputs; those not asked for are None."""
+    y: Optional[torch.Tensor]
+    h: Optional[torch.Tensor]
+    mean: Optional[torch.Tensor]
+    rstd: Optional[torch.Tensor]
+    codes: Optional[torch.Tensor]
+    scales: Optional[torch.Tensor]
+    codes8: torch.Tensor
+    scales8: torch.Tensor
+
+
+def fp4_norm_pack8(x: torch.Tensor, gamma: Optional[torch.Tensor] = None, beta: Optional[torch.Tensor] = None, *,
+                   kind: int = NORM_LAYER, eps: float = 1e-5, residual: Optional[torch.Tensor] = None, p: float = 0.0,
+                   seed: int = 0, stream_id: int = 0, save: bool = False, want_y: bool = False, mx: bool = False,
+                   layout: int = LAYOUT_LINEAR, y: Optional[torch.Tensor] = None, h: Optional[torch.Tensor] = None,
+                   mean: Optional[torch.Tensor] = None, rstd: Optional[torch.Tensor] = None,
+                   codes: Optional[torch.Tensor] = None, scales: Optional[torch.Tensor] = None,
+                   codes8: Optional[torch.Tensor] = None, scales8: Optional[torch.Tensor] = None,
+                   stream=None) -> NormPack8:
+    """fp4_norm that leaves y as 8-bit rows (codes8, scales8: what fp4_pack8
+    makes of y): for fp4_matvec_mx_pack8, or kept for the backward pass. y
+    itself comes out with want_y, the MXFP4 operand with mx."""
+    if mx or codes is not None or scales is not None:
+        if not isinstance(x, torch.Tensor) or x.dim() != 2:
+            raise ValueError("x must be a 2-D fp32 or bf16 tensor")
+        codes, scales = _mx_outputs(x.shape[0], x.shape[1], layout, codes, scales, x.device, stream)
+    y, h, mean, rstd, codes8, scales8 = _rows().norm_pack8(x, gamma, beta, kind, eps, residual, p, seed, stream_id, save,
+                                                           want_y, layout, y, h, mean, rstd, codes, scales, stream,
+                                                           codes8, scales8)
+    return _new(NormPack8, (y, h, mean, rstd, codes, scales, codes8, scales8))
+
+
+def fp4_norm_grad_pack8(dy: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor,
+                        gamma: Optional[torch.Tensor] = None, *, rstd: torch.Tensor,
+                        mean: Optional[torch.Tensor] = None, kind: int = NORM_LAYER,
+                        dres: Optional[torch.Tensor] = None, p: float = 0.0, seed: int = 0, stream_id: int = 0,
+                        weights: bool = True, dh: Optional[torch.Tensor] = None, dx: Optional[torch.Tensor] = None,
+                        dgamma: Optional[torch.Tensor] = None, dbeta: Optional[torch.Tensor] = None,
+                        workspace: Optional[torch.Tensor] = None, stream=None) -> NormGrad:
+    """fp4_norm_grad with the normed rows h kept by fp4_pack8 (codes, scales);
+    rstd and mean are the forward's. dh and dx may each be dy or dres."""
+    return _new(NormGrad, _rows().norm_grad_pack8(dy, codes, gamma, kind, mean, rstd, dres, p, seed, stream_id, weights,
+                                                  dh, dx, dgamma, dbeta, workspace, stream, scales))
+
+
+def fp4_swiglu_grad_pack8(dh: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor, *, pair: int = 32,
+                          want_h: bool = False, dc: Optional[torch.Tensor] = None, h: Optional[torch.Tensor] = None,
+                          stream=None) -> Tuple[torch.Tensor, Optional[torch.Tensor]]:
+    """fp4_swiglu_grad_bf16 with the gate/up output C [M x 2F] kept by
+    fp4_pack8 (codes, scales): (dc, h), h being SwiGLU of the packed C. h may
+    be dh."""
+    return _rows().swiglu_grad_pack8(dh, codes, pair, want_h, dc, h, stream, scales)
+
+
+def fp4_matvec_mx(x: torch.Tensor, w_codes: torch.Tensor, w_scales: torch.Tensor, *, alpha: float = 1.0,
+                  out_dtype=torch.float32, y: Optional[torch.Tensor] = None, layout: int = LAYOUT_LINEAR,
+                  n: Optional[int] = None, stream=None) -> torch.Tensor:
+    """Y = alpha * x W^T for at most 64 rows of bf16 x [M x K] and an MXFP4
+    operand W [N x K], in y's type or out_dtype. In the tiled layout the code
+    tensor carries rows padded to a multiple of 32, so pass the logical n."""
+    return _rows().matvec(x, None, w_codes, w_scales, None, 0, alpha, _out_type(out_dtype), layout, -1 if n is None else n,
+                          y, stream)
+
+
+def fp4_matvec_mx_pack8(x_codes: torch.Tensor, x_scales: torch.Tensor, w_codes: torch.Tensor, w_scales: torch.Tensor, *,
+                        alpha: float = 1.0, out_dtype=torch.float32, y: Optional[torch.Tensor] = None,
+                        layout: int = LAYOUT_LINEAR, n: Optional[int] = None, stream=None) -> torch.Tensor:
+    """fp4_matvec_mx of 8-bit rows x, as fp4_norm_pack8 or fp4_pack8 left them."""
+    if x_scales is None:
+        raise ValueError("x_scales must be a tensor")
+    return _rows().matvec(x_codes, x_scales, w_codes, w_scales, None, 0, alpha, _out_type(out_dtype), layout,
+                          -1 if n is None else n, y, stream)
+
+
+def fp4_matvec_nv(x: torch.Tensor, w_codes: torch.Tensor, w_scales: torch.Tensor, w_tensor_scale: torch.Tensor,
+                  domain: int = NV_GLOBAL, *, alpha: float = 1.0, out_dtype=torch.float32,
+                  y: Optional[torch.Tensor] = None, layout: int = LAYOUT_LINEAR, n: Optional[int] = None,
+                  stream=None) -> torch.Tensor:
+    """fp4_matvec_mx with an NVFP4 operand W of either domain."""
+    if w_tensor_scale is None:
+        raise ValueError("w_tensor_scale must be a tensor")
+    return _rows().matvec(x, None, w_codes, w_scales, w_tensor_scale, domain, alpha, _out_type(out_dtype), layout,
+                          -1 if n is None else n, y, stream)

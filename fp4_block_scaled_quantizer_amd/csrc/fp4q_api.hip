@@ -411,6 +411,274 @@ bool rows_cols_ok(int64_t rows, int64_t cols)
            (uint64_t)rows * (uint64_t)((cols + 7) / 8) < (1ull << 32);
 }
 
+constexpr int64_t kMaxMatvecRows = 64;
+
+// fp4_norm, or with `packs` fp4_norm_pack8.
+fp4q_status run_norm(const void *x, int64_t rows, int64_t cols, int64_t ld_x, int type, const void *residual,
+                     int64_t ld_r, float p, uint64_t seed, uint32_t stream_id, void *h, int64_t ld_h, int kind,
+                     const void *gamma, const void *beta, int w_type, float eps, void *y, int64_t ld_y, float *mean,
+                     float *rstd, void *codes, void *scales, int layout, bool packs, void *codes8, void *scales8,
+                     void *stream)
+{
+    if (!type_ok(type) || !type_ok(w_type) || !p_ok(p) || (kind != FP4Q_NORM_LAYER && kind != FP4Q_NORM_RMS) ||
+        (layout != FP4Q_LAYOUT_LINEAR && layout != FP4Q_LAYOUT_TILED) || !(eps >= 0.0f))
+        return FP4Q_EINVAL;
+    if ((codes == nullptr) != (scales == nullptr) || (mean && kind == FP4Q_NORM_RMS)) return FP4Q_EINVAL;
+    if (!rows_cols_ok(rows, cols)) return FP4Q_ESHAPE;
+    if (ld_x < cols || ld_x > kMaxDim || !ld_ok(residual, ld_r, cols) || !ld_ok(h, ld_h, cols) || !ld_ok(y, ld_y, cols))
+        return FP4Q_ESHAPE;
+    const bool tiled = codes && layout == FP4Q_LAYOUT_TILED;
+    if (codes && cols % (tiled ? 128 : 32) != 0) return FP4Q_ESHAPE;
+    if (packs && cols % 32 != 0) return FP4Q_ESHAPE;
+    if (cols > kMaxNormCols || (codes && type != FP4Q_OUT_BF16)) return FP4Q_EUNSUPPORTED;
+    if (rows == 0 || cols == 0) return FP4Q_OK;
+    if (!x || (packs ? !codes8 || !scales8 : !y && !codes)) return FP4Q_EINVAL;
+    const uint64_t es = type_size(type), ws = type_size(w_type);
+    if (!aligned(x, es) || !aligned(residual, es) || !aligned(h, es) || !aligned(y, es) || !aligned(gamma, ws) ||
+        !aligned(beta, ws) || !aligned(mean, 4) || !aligned(rstd, 4) || !aligned(codes, 16) ||
+        (tiled && !aligned(scales, 16)) || !aligned(codes8, 16))
+        return FP4Q_EALIGN;
+    const int64_t rows_out = tiled ? (rows + 31) / 32 * 32 : rows;
+    const Matrix in[2] = {matrix(x, rows, cols, ld_x, es), matrix(residual, rows, cols, ld_r, es)};
+    const Matrix mh = matrix(h, rows, cols, ld_h, es), my = matrix(y, rows, cols, ld_y, es);
+    const Range weights[2] = {bytes(gamma, gamma ? cols * ws : 0), bytes(beta, beta ? cols * ws : 0)};
+    const Range outs[8] = {mh.r, my.r, bytes(mean, mean ? rows * 4 : 0), bytes(rstd, rstd ? rows * 4 : 0),
+                           bytes(codes, codes ? (uint64_t)rows_out * cols / 2 : 0),
+                           bytes(scales, scales ? (uint64_t)rows_out * cols / 32 : 0),
+                           bytes(codes8, packs ? (uint64_t)rows * cols : 0),
+                           bytes(scales8, packs ? (uint64_t)rows * cols / 32 : 0)};
+    for (int i = 0; i < 8; ++i) {
+        for (int j = i + 1; j < 8; ++j)
+            if (i == 0 && j == 1 ? !apart(mh, my) : meet(outs[i], outs[j])) return FP4Q_EINVAL;
+        for (const Range &w : weights)
+            if (meet(outs[i], w)) return FP4Q_EINVAL;
+        for (const Matrix &m : in) {
+            if (i >= 2 && meet(outs[i], m.r)) return FP4Q_EINVAL;
+        }
+    }
+    for (const Matrix &m : in)
+        if (!same_or_apart(mh, m) || !same_or_apart(my, m)) return FP4Q_EINVAL;
+    fp4q::NormArgs a{};
+    a.x = x;
+    a.residual = residual;
+    a.rows = rows;
+    a.cols = cols;
+    a.ld_x = ld_x;
+    a.ld_r = ld_r;
+    a.ld_h = ld_h;
+    a.ld_y = ld_y;
+    a.rows_out = rows_out;
+    a.bf16 = type == FP4Q_OUT_BF16;
+    a.layer = kind == FP4Q_NORM_LAYER;
+    a.gamma = gamma;
+    a.beta = beta;
+    a.w_bf16 = w_type == FP4Q_OUT_BF16;
+    a.eps = eps;
+    a.p = p;
+    a.seed = seed;
+    a.stream_id = stream_id;
+    a.h = h;
+    a.y = y;
+    a.mean = mean;
+    a.rstd = rstd;
+    a.codes = codes;
+    a.scales = scales;
+    a.tiled = tiled;
+    a.codes8 = codes8;
+    a.scales8 = scales8;
+    (void)hipGetLastError();
+    return launched(fp4q::launch_norm(a, as_stream(stream)));
+}
+
+// fp4_norm_grad, or with `packed` fp4_norm_grad_pack8.
+fp4q_status run_norm_grad(const void *dy, int64_t rows, int64_t cols, int64_t ld_dy, int type, const void *h,
+                          int64_t ld_h, bool packed, const void *h_codes, const void *h_scales, const void *dres,
+                          int64_t ld_dres, int kind, const void *gamma, int w_type, const float *mean, const float *rstd,
+                          float p, uint64_t seed, uint32_t stream_id, void *dh, int64_t ld_dh, void *dx, int64_t ld_dx,
+                          float *dgamma, float *dbeta, void *workspace, size_t workspace_bytes, void *stream)
+{
+    if (!type_ok(type) || !type_ok(w_type) || !p_ok(p) || (kind != FP4Q_NORM_LAYER && kind != FP4Q_NORM_RMS))
+        return FP4Q_EINVAL;
+    if (!rows_cols_ok(rows, cols)) return FP4Q_ESHAPE;
+    if (ld_dy < cols || ld_dy > kMaxDim || ld_h < cols || ld_h > kMaxDim || !ld_ok(dres, ld_dres, cols) ||
+        !ld_ok(dh, ld_dh, cols) || !ld_ok(dx, ld_dx, cols))
+        return FP4Q_ESHAPE;
+    if (packed && cols % 32 != 0) return FP4Q_ESHAPE;
+    if (cols > kMaxNormCols) return FP4Q_EUNSUPPORTED;
+    if (cols == 0) return FP4Q_OK;
+    if (!aligned(dgamma, 4) || !aligned(dbeta, 4)) return FP4Q_EALIGN;
+    const bool sums = dgamma || dbeta;
+    if (rows == 0 && !sums) return FP4Q_OK;
+    const uint64_t es = type_size(type), ws = type_size(w_type);
+    if (rows > 0) {
+        if (!dy || (packed ? !h_codes || !h_scales : !h) || !rstd || (kind == FP4Q_NORM_LAYER && !mean) || (!dh && !dx && !sums)) return FP4Q_EINVAL;
+        const size_t need = sums ? fp4q::norm_grad_workspace_bytes(rows, cols, type == FP4Q_OUT_BF16) : 0;
+        if (need > 0 && (!workspace || workspace_bytes < need)) return FP4Q_EINVAL;
+        if (!aligned(dy, es) || !aligned(h, es) || !aligned(dres, es) || !aligned(dh, es) || !aligned(dx, es) ||
+            !aligned(gamma, ws) || !aligned(mean, 4) || !aligned(rstd, 4) || (need > 0 && !aligned(workspace, 16)) || !aligned(h_codes, 16))
+            return FP4Q_EALIGN;
+        const Matrix in[3] = {matrix(dy, rows, cols, ld_dy, es), matrix(h, rows, cols, ld_h, es),
+                              matrix(dres, rows, cols, ld_dres, es)};
+        const Matrix mo[2] = {matrix(dh, rows, cols, ld_dh, es), matrix(dx, rows, cols, ld_dx, es)};
+        const Range small[5] = {bytes(gamma, gamma ? cols * ws : 0), bytes(mean, mean ? rows * 4 : 0), bytes(rstd, rows * 4),
+                                bytes(h_codes, packed ? (uint64_t)rows * cols : 0),
+                                bytes(h_scales, packed ? (uint64_t)rows * cols / 32 : 0)};
+        const Range outs[5] = {mo[0].r, mo[1].r, bytes(dgamma, dgamma ? cols * 4 : 0),
+                               bytes(dbeta, dbeta ? cols * 4 : 0), bytes(workspace, need)};
+        for (int i = 0; i < 5; ++i) {
+            for (int j = i + 1; j < 5; ++j)
+                if (i == 0 && j == 1 ? !apart(mo[0], mo[1]) : meet(outs[i], outs[j])) return FP4Q_EINVAL;
+            for (const Range &r : small)
+                if (meet(outs[i], r)) return FP4Q_EINVAL;
+            for (const Matrix &m : in) {
+                if (i < 2 ? !same_or_apart(mo[i], m) : meet(outs[i], m.r)) return FP4Q_EINVAL;
+            }
+        }
+    }
+    fp4q::NormGradArgs a{};
+    a.dy = dy;
+    a.h = h;
+    a.h_codes = packed ? reinterpret_cast<const uint8_t *>(h_codes) : nullptr;
+    a.h_scales = reinterpret_cast<const uint8_t *>(h_scales);
+    a.dres = dres;
+    a.rows = rows;
+    a.cols = cols;
+    a.ld_dy = ld_dy;
+    a.ld_h = ld_h;
+    a.ld_dres = ld_dres;
+    a.ld_dh = ld_dh;
+    a.ld_dx = ld_dx;
+    a.bf16 = type == FP4Q_OUT_BF16;
+    a.layer = kind == FP4Q_NORM_LAYER;
+    a.gamma = gamma;
+    a.w_bf16 = w_type == FP4Q_OUT_BF16;
+    a.mean = mean;
+    a.rstd = rstd;
+    a.p = p;
+    a.seed = seed;
+    a.stream_id = stream_id;
+    a.dh = dh;
+    a.dx = dx;
+    a.parts = reinterpret_cast<float *>(workspace);
+    (void)hipGetLastError();
+    return launched(fp4q::launch_norm_grad(a, dgamma, dbeta, as_stream(stream)));
+}
+
+// fp4_swiglu_grad_bf16, or with `packed` fp4_swiglu_grad_pack8.
+fp4q_status run_swiglu_grad(const void *dh, int64_t ld_dh, const void *c, int64_t ldc, bool packed, const void *c_codes,
+                            const void *c_scales, int64_t M, int64_t F, int64_t pair, void *dc, int64_t ld_dc, void *h,
+                            int64_t ldh, void *stream)
+{
+    if (M < 0 || F < 0 || M > kMaxDim || F > kMaxDim) return FP4Q_ESHAPE;
+    if (F % 8 != 0 || pair <= 0 || pair % 8 != 0 || (F > 0 && F % pair != 0) || ldc < 2 * F || ld_dc < 2 * F ||
+        ld_dh < F || ldc % 8 != 0 || ld_dc % 8 != 0 || ld_dh % 8 != 0 || ldc > kMaxDim * 2 || ld_dc > kMaxDim * 2 ||
+        ld_dh > kMaxDim || (h && (ldh < F || ldh % 8 != 0 || ldh > kMaxDim)))
+        return FP4Q_ESHAPE;
+    if (packed && F % 16 != 0) return FP4Q_ESHAPE;
+    if (M == 0 || F == 0) return FP4Q_OK;
+    if (!dh || (packed ? !c_codes || !c_scales : !c) || !dc) return FP4Q_EINVAL;
+    if (!aligned(dh, 16) || !aligned(c, 16) || !aligned(dc, 16) || !aligned(h, 16) || !aligned(c_codes, 16))
+        return FP4Q_EALIGN;
+    const Matrix mi = matrix(dh, M, F, ld_dh, 2), mc = matrix(c, M, 2 * F, ldc, 2);
+    const Matrix mo = matrix(dc, M, 2 * F, ld_dc, 2), mh = matrix(h, M, F, ldh, 2);
+    if (!apart(mo, mi) || !same_or_apart(mo, mc) || !apart(mh, mc) || !apart(mh, mo) || !same_or_apart(mh, mi))
+        return FP4Q_EINVAL;
+    for (const Range &r : {bytes(c_codes, packed ? 2ull * M * F : 0), bytes(c_scales, packed ? 2ull * M * F / 32 : 0)})
+        if (meet(mo.r, r) || meet(mh.r, r)) return FP4Q_EINVAL;
+    fp4q::SwigluGradArgs a{};
+    a.dh = dh;
+    a.c = c;
+    a.c_codes = packed ? reinterpret_cast<const uint8_t *>(c_codes) : nullptr;
+    a.c_scales = reinterpret_cast<const uint8_t *>(c_scales);
+    a.M = M;
+    a.F = F;
+    a.ld_dh = ld_dh;
+    a.ldc = ldc;
+    a.ld_dc = ld_dc;
+    a.ldh = ldh;
+    a.pair = pair;
+    a.dc = dc;
+    a.h = h;
+    (void)hipGetLastError();
+    return launched(fp4q::launch_swiglu_grad(a, as_stream(stream)));
+}
+
+// Products of few rows with FP4 weights: x bf16, or with `packed` 8-bit rows.
+fp4q_status run_matvec(const void *x, const void *x_scales, bool packed, int64_t M, int64_t K, int64_t ld_x,
+                       const void *codes, const void *scales, bool nv, const float *tensor_scale, int domain, int64_t N,
+                       float alpha, int layout, void *y, int y_type, int64_t ld_y, void *stream)
+{
+    if (nv && domain != FP4Q_NV_GLOBAL && domain != FP4Q_NV_TILE128) return FP4Q_EINVAL;
+    if ((layout != FP4Q_LAYOUT_LINEAR && layout != FP4Q_LAYOUT_TILED) || !type_ok(y_type)) return FP4Q_EINVAL;
+    if (M < 0 || N < 0 || K < 0 || N > kMaxDim || K > kMaxDim || K % 128 != 0 || ld_x < K || ld_x > kMaxDim ||
+        ld_y < N || ld_y > kMaxDim)
+        return FP4Q_ESHAPE;
+    const uint64_t rows = layout == FP4Q_LAYOUT_TILED ? (uint64_t)(N + 31) / 32 * 32 : (uint64_t)N;
+    if (rows * (uint64_t)K / 2 >= (1ull << 32)) return FP4Q_ESHAPE;
+    if (M > kMaxMatvecRows) return FP4Q_EUNSUPPORTED;
+    if (M == 0 || N == 0) return FP4Q_OK;
+    if (!y) return FP4Q_EINVAL;
+    const uint64_t es = type_size(y_type);
+    if (!aligned(y, es)) return FP4Q_EALIGN;
+    if (K > 0) {
+        if (!x || (packed && !x_scales) || !codes || !scales || (nv && !tensor_scale)) return FP4Q_EINVAL;
+        if (!aligned(x, 16) || (!packed && ld_x % 8 != 0) || !aligned(codes, 16) || !aligned(scales, 4) ||
+            !aligned(tensor_scale, 4))
+            return FP4Q_EALIGN;
+        const Range out = matrix(y, M, N, ld_y, es).r;
+        const uint64_t tiles = domain == FP4Q_NV_GLOBAL ? 1 : (uint64_t)(N + 127) / 128 * (uint64_t)(K / 128);
+        const Range in[5] = {matrix(x, M, K, ld_x, packed ? 1 : 2).r, bytes(x_scales, packed ? (uint64_t)(M * K / 32) : 0),
+                             bytes(codes, rows * (uint64_t)K / 2), bytes(scales, rows * (uint64_t)K / (nv ? 16 : 32)),
+                             bytes(tensor_scale, nv ? tiles * 4 : 0)};
+        for (const Range &r : in)
+            if (meet(out, r)) return FP4Q_EINVAL;
+    }
+    fp4q::MatvecArgs a{};
+    a.x = x;
+    a.x_scales = packed && K > 0 ? x_scales : nullptr;
+    a.M = M;
+    a.N = N;
+    a.K = K;
+    a.ld_x = ld_x;
+    a.ld_y = ld_y;
+    a.codes = codes;
+    a.scales = scales;
+    a.tensor_scale = nv && K > 0 ? tensor_scale : nullptr;
+    a.nv_domain = domain;
+    a.tiled = layout == FP4Q_LAYOUT_TILED;
+    a.alpha = alpha;
+    a.y = y;
+    a.y_bf16 = y_type == FP4Q_OUT_BF16;
+    (void)hipGetLastError();
+    return launched(fp4q::launch_matvec(a, as_stream(stream)));
+}
+
+// fp4_pack8, or with `unpack` fp4_unpack8.
+fp4q_status run_pack8(const void *x, int64_t rows, int64_t cols, int64_t ld, int type, const void *codes,
+                      const void *scales, bool unpack, void *stream)
+{
+    if (!type_ok(type)) return FP4Q_EINVAL;
+    if (!rows_cols_ok(rows, cols) || cols % 32 != 0 || ld < cols || ld > kMaxDim) return FP4Q_ESHAPE;
+    if (rows == 0 || cols == 0) return FP4Q_OK;
+    if (!x || !codes || !scales) return FP4Q_EINVAL;
+    const uint64_t es = type_size(type);
+    if (!aligned(x, es) || !aligned(codes, 16)) return FP4Q_EALIGN;
+    const Range rx = matrix(x, rows, cols, ld, es).r, rc = bytes(codes, (uint64_t)rows * cols),
+                rs = bytes(scales, (uint64_t)rows * cols / 32);
+    if (overlap(rx, rc) || overlap(rx, rs) || (!unpack && overlap(rc, rs))) return FP4Q_EINVAL;
+    fp4q::Pack8Args a{};
+    a.x = const_cast<void *>(x);
+    a.rows = rows;
+    a.cols = cols;
+    a.ld = ld;
+    a.bf16 = type == FP4Q_OUT_BF16;
+    a.unpack = unpack;
+    a.codes = const_cast<void *>(codes);
+    a.scales = const_cast<void *>(scales);
+    (void)hipGetLastError();
+    return launched(fp4q::launch_pack8(a, as_stream(stream)));
+}
+
 }  // namespace
 
 extern "C" {
@@ -618,69 +886,18 @@ fp4q_status fp4_norm(const void *x, int64_t rows, int64_t cols, int64_t ld_x, in
                      const void *gamma, const void *beta, int w_type, float eps, void *y, int64_t ld_y, float *mean,
                      float *rstd, void *codes, void *scales, int layout, void *stream)
 {
-    if (!type_ok(type) || !type_ok(w_type) || !p_ok(p) || (kind != FP4Q_NORM_LAYER && kind != FP4Q_NORM_RMS) ||
-        (layout != FP4Q_LAYOUT_LINEAR && layout != FP4Q_LAYOUT_TILED) || !(eps >= 0.0f))
-        return FP4Q_EINVAL;
-    if ((codes == nullptr) != (scales == nullptr) || (mean && kind == FP4Q_NORM_RMS)) return FP4Q_EINVAL;
-    if (!rows_cols_ok(rows, cols)) return FP4Q_ESHAPE;
-    if (ld_x < cols || ld_x > kMaxDim || !ld_ok(residual, ld_r, cols) || !ld_ok(h, ld_h, cols) || !ld_ok(y, ld_y, cols))
-        return FP4Q_ESHAPE;
-    const bool tiled = codes && layout == FP4Q_LAYOUT_TILED;
-    if (codes && cols % (tiled ? 128 : 32) != 0) return FP4Q_ESHAPE;
-    if (cols > kMaxNormCols || (codes && type != FP4Q_OUT_BF16)) return FP4Q_EUNSUPPORTED;
-    if (rows == 0 || cols == 0) return FP4Q_OK;
-    if (!x || (!y && !codes)) return FP4Q_EINVAL;
-    const uint64_t es = type_size(type), ws = type_size(w_type);
-    if (!aligned(x, es) || !aligned(residual, es) || !aligned(h, es) || !aligned(y, es) || !aligned(gamma, ws) ||
-        !aligned(beta, ws) || !aligned(mean, 4) || !aligned(rstd, 4) || !aligned(codes, 16) ||
-        (tiled && !aligned(scales, 16)))
-        return FP4Q_EALIGN;
-    const int64_t rows_out = tiled ? (rows + 31) / 32 * 32 : rows;
-    const Matrix in[2] = {matrix(x, rows, cols, ld_x, es), matrix(residual, rows, cols, ld_r, es)};
-    const Matrix mh = matrix(h, rows, cols, ld_h, es), my = matrix(y, rows, cols, ld_y, es);
-    const Range weights[2] = {bytes(gamma, gamma ? cols * ws : 0), bytes(beta, beta ? cols * ws : 0)};
-    const Range outs[6] = {mh.r, my.r, bytes(mean, mean ? rows * 4 : 0), bytes(rstd, rstd ? rows * 4 : 0),
-                           bytes(codes, codes ? (uint64_t)rows_out * cols / 2 : 0),
-                           bytes(scales, scales ? (uint64_t)rows_out * cols / 32 : 0)};
-    for (int i = 0; i < 6; ++i) {
-        for (int j = i + 1; j < 6; ++j)
-            if (i == 0 && j == 1 ? !apart(mh, my) : meet(outs[i], outs[j])) return FP4Q_EINVAL;
-        for (const Range &w : weights)
-            if (meet(outs[i], w)) return FP4Q_EINVAL;
-        for (const Matrix &m : in) {
-            if (i >= 2 && meet(outs[i], m.r)) return FP4Q_EINVAL;
-        }
-    }
-    for (const Matrix &m : in)
-        if (!same_or_apart(mh, m) || !same_or_apart(my, m)) return FP4Q_EINVAL;
-    fp4q::NormArgs a{};
-    a.x = x;
-    a.residual = residual;
-    a.rows = rows;
-    a.cols = cols;
-    a.ld_x = ld_x;
-    a.ld_r = ld_r;
-    a.ld_h = ld_h;
-    a.ld_y = ld_y;
-    a.rows_out = rows_out;
-    a.bf16 = type == FP4Q_OUT_BF16;
-    a.layer = kind == FP4Q_NORM_LAYER;
-    a.gamma = gamma;
-    a.beta = beta;
-    a.w_bf16 = w_type == FP4Q_OUT_BF16;
-    a.eps = eps;
-    a.p = p;
-    a.seed = seed;
-    a.stream_id = stream_id;
-    a.h = h;
-    a.y = y;
-    a.mean = mean;
-    a.rstd = rstd;
-    a.codes = codes;
-    a.scales = scales;
-    a.tiled = tiled;
-    (void)hipGetLastError();
-    return launched(fp4q::launch_norm(a, as_stream(stream)));
+    return run_norm(x, rows, cols, ld_x, type, residual, ld_r, p, seed, stream_id, h, ld_h, kind, gamma, beta, w_type,
+                    eps, y, ld_y, mean, rstd, codes, scales, layout, false, nullptr, nullptr, stream);
+}
+
+fp4q_status fp4_norm_pack8(const void *x, int64_t rows, int64_t cols, int64_t ld_x, int type, const void *residual,
+                           int64_t ld_r, float p, uint64_t seed, uint32_t stream_id, void *h, int64_t ld_h, int kind,
+                           const void *gamma, const void *beta, int w_type, float eps, void *y, int64_t ld_y,
+                           float *mean, float *rstd, void *codes, void *scales, int layout, void *codes8,
+                           void *scales8, void *stream)
+{
+    return run_norm(x, rows, cols, ld_x, type, residual, ld_r, p, seed, stream_id, h, ld_h, kind, gamma, beta, w_type,
+                    eps, y, ld_y, mean, rstd, codes, scales, layout, true, codes8, scales8, stream);
 }
 
 size_t fp4q_norm_grad_workspace_bytes(int64_t rows, int64_t cols)
@@ -697,98 +914,69 @@ fp4q_status fp4_norm_grad(const void *dy, int64_t rows, int64_t cols, int64_t ld
                           int64_t ld_dh, void *dx, int64_t ld_dx, float *dgamma, float *dbeta, void *workspace,
                           size_t workspace_bytes, void *stream)
 {
-    if (!type_ok(type) || !type_ok(w_type) || !p_ok(p) || (kind != FP4Q_NORM_LAYER && kind != FP4Q_NORM_RMS))
-        return FP4Q_EINVAL;
-    if (!rows_cols_ok(rows, cols)) return FP4Q_ESHAPE;
-    if (ld_dy < cols || ld_dy > kMaxDim || ld_h < cols || ld_h > kMaxDim || !ld_ok(dres, ld_dres, cols) ||
-        !ld_ok(dh, ld_dh, cols) || !ld_ok(dx, ld_dx, cols))
-        return FP4Q_ESHAPE;
-    if (cols > kMaxNormCols) return FP4Q_EUNSUPPORTED;
-    if (cols == 0) return FP4Q_OK;
-    if (!aligned(dgamma, 4) || !aligned(dbeta, 4)) return FP4Q_EALIGN;
-    const bool sums = dgamma || dbeta;
-    if (rows == 0 && !sums) return FP4Q_OK;
-    const uint64_t es = type_size(type), ws = type_size(w_type);
-    if (rows > 0) {
-        if (!dy || !h || !rstd || (kind == FP4Q_NORM_LAYER && !mean) || (!dh && !dx && !sums)) return FP4Q_EINVAL;
-        const size_t need = sums ? fp4q::norm_grad_workspace_bytes(rows, cols, type == FP4Q_OUT_BF16) : 0;
-        if (need > 0 && (!workspace || workspace_bytes < need)) return FP4Q_EINVAL;
-        if (!aligned(dy, es) || !aligned(h, es) || !aligned(dres, es) || !aligned(dh, es) || !aligned(dx, es) ||
-            !aligned(gamma, ws) || !aligned(mean, 4) || !aligned(rstd, 4) || (need > 0 && !aligned(workspace, 16)))
-            return FP4Q_EALIGN;
-        const Matrix in[3] = {matrix(dy, rows, cols, ld_dy, es), matrix(h, rows, cols, ld_h, es),
-                              matrix(dres, rows, cols, ld_dres, es)};
-        const Matrix mo[2] = {matrix(dh, rows, cols, ld_dh, es), matrix(dx, rows, cols, ld_dx, es)};
-        const Range small[3] = {bytes(gamma, gamma ? cols * ws : 0), bytes(mean, mean ? rows * 4 : 0),
-                                bytes(rstd, rows * 4)};
-        const Range outs[5] = {mo[0].r, mo[1].r, bytes(dgamma, dgamma ? cols * 4 : 0),
-                               bytes(dbeta, dbeta ? cols * 4 : 0), bytes(workspace, need)};
-        for (int i = 0; i < 5; ++i) {
-            for (int j = i + 1; j < 5; ++j)
-                if (i == 0 && j == 1 ? !apart(mo[0], mo[1]) : meet(outs[i], outs[j])) return FP4Q_EINVAL;
-            for (const Range &r : small)
-                if (meet(outs[i], r)) return FP4Q_EINVAL;
-            for (const Matrix &m : in) {
-                if (i < 2 ? !same_or_apart(mo[i], m) : meet(outs[i], m.r)) return FP4Q_EINVAL;
-            }
-        }
-    }
-    fp4q::NormGradArgs a{};
-    a.dy = dy;
-    a.h = h;
-    a.dres = dres;
-    a.rows = rows;
-    a.cols = cols;
-    a.ld_dy = ld_dy;
-    a.ld_h = ld_h;
-    a.ld_dres = ld_dres;
-    a.ld_dh = ld_dh;
-    a.ld_dx = ld_dx;
-    a.bf16 = type == FP4Q_OUT_BF16;
-    a.layer = kind == FP4Q_NORM_LAYER;
-    a.gamma = gamma;
-    a.w_bf16 = w_type == FP4Q_OUT_BF16;
-    a.mean = mean;
-    a.rstd = rstd;
-    a.p = p;
-    a.seed = seed;
-    a.stream_id = stream_id;
-    a.dh = dh;
-    a.dx = dx;
-    a.parts = reinterpret_cast<float *>(workspace);
-    (void)hipGetLastError();
-    return launched(fp4q::launch_norm_grad(a, dgamma, dbeta, as_stream(stream)));
+    return run_norm_grad(dy, rows, cols, ld_dy, type, h, ld_h, false, nullptr, nullptr, dres, ld_dres, kind, gamma,
+                         w_type, mean, rstd, p, seed, stream_id, dh, ld_dh, dx, ld_dx, dgamma, dbeta, workspace,
+                         workspace_bytes, stream);
+}
+
+fp4q_status fp4_norm_grad_pack8(const void *dy, int64_t rows, int64_t cols, int64_t ld_dy, int type,
+                                const void *h_codes, const void *h_scales, const void *dres, int64_t ld_dres, int kind,
+                                const void *gamma, int w_type, const float *mean, const float *rstd, float p,
+                                uint64_t seed, uint32_t stream_id, void *dh, int64_t ld_dh, void *dx, int64_t ld_dx,
+                                float *dgamma, float *dbeta, void *workspace, size_t workspace_bytes, void *stream)
+{
+    return run_norm_grad(dy, rows, cols, ld_dy, type, nullptr, cols, true, h_codes, h_scales, dres, ld_dres, kind,
+                         gamma, w_type, mean, rstd, p, seed, stream_id, dh, ld_dh, dx, ld_dx, dgamma, dbeta, workspace,
+                         workspace_bytes, stream);
 }
 
 fp4q_status fp4_swiglu_grad_bf16(const void *dh, int64_t ld_dh, const void *c, int64_t M, int64_t F, int64_t ldc,
                                  int64_t pair, void *dc, int64_t ld_dc, void *h, int64_t ldh, void *stream)
 {
-    if (M < 0 || F < 0 || M > kMaxDim || F > kMaxDim) return FP4Q_ESHAPE;
-    if (F % 8 != 0 || pair <= 0 || pair % 8 != 0 || (F > 0 && F % pair != 0) || ldc < 2 * F || ld_dc < 2 * F ||
-        ld_dh < F || ldc % 8 != 0 || ld_dc % 8 != 0 || ld_dh % 8 != 0 || ldc > kMaxDim * 2 || ld_dc > kMaxDim * 2 ||
-        ld_dh > kMaxDim || (h && (ldh < F || ldh % 8 != 0 || ldh > kMaxDim)))
-        return FP4Q_ESHAPE;
-    if (M == 0 || F == 0) return FP4Q_OK;
-    if (!dh || !c || !dc) return FP4Q_EINVAL;
-    if (!aligned(dh, 16) || !aligned(c, 16) || !aligned(dc, 16) || !aligned(h, 16)) return FP4Q_EALIGN;
-    const Matrix mi = matrix(dh, M, F, ld_dh, 2), mc = matrix(c, M, 2 * F, ldc, 2);
-    const Matrix mo = matrix(dc, M, 2 * F, ld_dc, 2), mh = matrix(h, M, F, ldh, 2);
-    if (!apart(mo, mi) || !same_or_apart(mo, mc) || !apart(mh, mc) || !apart(mh, mo) || !same_or_apart(mh, mi))
-        return FP4Q_EINVAL;
-    fp4q::SwigluGradArgs a{};
-    a.dh = dh;
-    a.c = c;
-    a.M = M;
-    a.F = F;
-    a.ld_dh = ld_dh;
-    a.ldc = ldc;
-    a.ld_dc = ld_dc;
-    a.ldh = ldh;
-    a.pair = pair;
-    a.dc = dc;
-    a.h = h;
-    (void)hipGetLastError();
-    return launched(fp4q::launch_swiglu_grad(a, as_stream(stream)));
+    return run_swiglu_grad(dh, ld_dh, c, ldc, false, nullptr, nullptr, M, F, pair, dc, ld_dc, h, ldh, stream);
+}
+
+fp4q_status fp4_swiglu_grad_pack8(const void *dh, int64_t ld_dh, const void *c_codes, const void *c_scales, int64_t M,
+                                  int64_t F, int64_t pair, void *dc, int64_t ld_dc, void *h, int64_t ldh, void *stream)
+{
+    // (2F would not fit where F is out of range, which is refused first)
+    return run_swiglu_grad(dh, ld_dh, nullptr, F > 0 && F <= kMaxDim ? 2 * F : 0, true, c_codes, c_scales, M, F, pair,
+                           dc, ld_dc, h, ldh, stream);
+}
+
+fp4q_status fp4_pack8(const void *x, int64_t rows, int64_t cols, int64_t ld_x, int type, void *codes, void *scales,
+                      void *stream)
+{
+    return run_pack8(x, rows, cols, ld_x, type, codes, scales, false, stream);
+}
+
+fp4q_status fp4_unpack8(const void *codes, const void *scales, int64_t rows, int64_t cols, void *y, int64_t ld_y,
+                        int type, void *stream)
+{
+    return run_pack8(y, rows, cols, ld_y, type, codes, scales, true, stream);
+}
+
+fp4q_status fp4_matvec_mx(const void *x, int64_t M, int64_t K, int64_t ld_x, const void *w_codes, const void *w_scales,
+                          int64_t N, float alpha, int layout, void *y, int y_type, int64_t ld_y, void *stream)
+{
+    return run_matvec(x, nullptr, false, M, K, ld_x, w_codes, w_scales, false, nullptr, FP4Q_NV_GLOBAL, N, alpha, layout,
+                      y, y_type, ld_y, stream);
+}
+
+fp4q_status fp4_matvec_mx_pack8(const void *x_codes, const void *x_scales, int64_t M, int64_t K, const void *w_codes,
+                                const void *w_scales, int64_t N, float alpha, int layout, void *y, int y_type,
+                                int64_t ld_y, void *stream)
+{
+    return run_matvec(x_codes, x_scales, true, M, K, K, w_codes, w_scales, false, nullptr, FP4Q_NV_GLOBAL, N, alpha,
+                      layout, y, y_type, ld_y, stream);
+}
+
+fp4q_status fp4_matvec_nv(const void *x, int64_t M, int64_t K, int64_t ld_x, const void *w_codes, const void *w_scales,
+                          const float *w_tensor_scale, int domain, int64_t N, float alpha, int layout, void *y,
+                          int y_type, int64_t ld_y, void *stream)
+{
+    return run_matvec(x, nullptr, false, M, K, ld_x, w_codes, w_scales, true, w_tensor_scale, domain, N, alpha, layout, y,
+                      y_type, ld_y, stream);
 }
 
 fp4q_status fp4_rotary(const void *x, int64_t tokens, int64_t heads, int64_t dim, int64_t x_token, int64_t x_head,

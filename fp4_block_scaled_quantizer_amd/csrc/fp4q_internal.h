@@ -72,10 +72,12 @@ struct NormArgs {
     float *mean, *rstd;  // optional
     void *codes, *scales;  // optional: the MXFP4 operand of a bf16 y
     bool tiled;
+    void *codes8, *scales8;  // optional: y as 8-bit rows
 };
 
 struct NormGradArgs {
     const void *dy, *h, *dres;  // dres: optional
+    const uint8_t *h_codes, *h_scales;  // h as 8-bit rows, in place of h
     int64_t rows, cols, ld_dy, ld_h, ld_dres, ld_dh, ld_dx;
     bool bf16;
     bool layer;
@@ -92,6 +94,7 @@ struct NormGradArgs {
 
 struct SwigluGradArgs {
     const void *dh, *c;
+    const uint8_t *c_codes, *c_scales;  // c as 8-bit rows, in place of c
     int64_t M, F, ld_dh, ldc, ld_dc, ldh, pair;
     void *dc, *h;  // h: optional
 };
@@ -107,6 +110,25 @@ struct RotaryArgs {
     float scale;
     void *y;
     uint32_t tokens_at_once;
+};
+
+struct Pack8Args {
+    void *x;  // the rows, bf16 or binary32: read, or with `unpack` written
+    int64_t rows, cols, ld;
+    bool bf16, unpack;
+    void *codes, *scales;
+};
+
+struct MatvecArgs {
+    const void *x, *x_scales;  // bf16, or with x_scales the codes of 8-bit rows
+    int64_t M, N, K, ld_x, ld_y;
+    const void *codes, *scales;
+    const float *tensor_scale;  // NV only
+    int nv_domain;
+    bool tiled;
+    float alpha;
+    void *y;
+    bool y_bf16;
 };
 
 // Compute units of the current device (the persistent GEMMs' grid), looked
@@ -128,8 +150,12 @@ int launch_swiglu(const void *c, int64_t M, int64_t F, int64_t ldc, int64_t pair
 int launch_dropout(const DropoutArgs &a, hipStream_t st);
 int launch_norm(const NormArgs &a, hipStream_t st);
 size_t norm_grad_workspace_bytes(int64_t rows, int64_t cols, bool bf16);
-int launch_norm_grad(NormGradArgs a, float *dgamma, float *dbeta, hipStream_t st);
+int launch_norm_grad(const NormGradArgs &a, float *dgamma, float *dbeta, hipStream_t st);
+// its rows' part where h comes as 8-bit rows
+int norm_grad_rows_pack8(const NormGradArgs &a, float *dgamma, float *dbeta, hipStream_t st);
 int launch_swiglu_grad(const SwigluGradArgs &a, hipStream_t st);
 int launch_rotary(RotaryArgs a, hipStream_t st);
+int launch_pack8(const Pack8Args &a, hipStream_t st);
+int launch_matvec(const MatvecArgs &a, hipStream_t st);
 
 }  // namespace fp4q

@@ -30,6 +30,14 @@ struct Library {
     decltype(&::fp4_norm_grad) norm_grad;
     decltype(&::fp4_swiglu_grad_bf16) swiglu_grad;
     decltype(&::fp4_rotary) rotary;
+    decltype(&::fp4_pack8) pack8;
+    decltype(&::fp4_unpack8) unpack8;
+    decltype(&::fp4_norm_pack8) norm_pack8;
+    decltype(&::fp4_norm_grad_pack8) norm_grad_pack8;
+    decltype(&::fp4_swiglu_grad_pack8) swiglu_grad_pack8;
+    decltype(&::fp4_matvec_mx) matvec_mx;
+    decltype(&::fp4_matvec_mx_pack8) matvec_mx_pack8;
+    decltype(&::fp4_matvec_nv) matvec_nv;
     PyObject *error;          // Fp4qError
     PyObject *current, *raw, *external;  // torch's current device, its current stream, a stream of a handle
 } lib{};
@@ -217,6 +225,38 @@ struct Like {
     }
 };
 
+// A dense tensor of `type` with exactly these sizes on `like`'s device.
+void *dense(const at::Tensor &t, const char *name, at::ScalarType type, at::IntArrayRef sizes, const at::Tensor &like)
+{
+    if (t.scalar_type() != type || t.sizes() != sizes || t.device() != like.device() || !t.is_contiguous()) {
+        std::string shape;
+        for (const int64_t n : sizes) shape += (shape.empty() ? "" : ", ") + std::to_string(n);
+        throw Refused(std::string(name) + " must be a contiguous " + at::toString(type) + " tensor of shape (" + shape +
+                      ") on the same device");
+    }
+    return t.data_ptr();
+}
+
+// 8-bit rows: codes [rows, cols] and scales [rows, cols / 32], given or (an
+// output's) made.
+struct Packed {
+    void *codes, *scales;
+};
+Packed packed(PyObject *codes, PyObject *scales, const char *names[2], int64_t rows, int64_t cols, const at::Tensor &like,
+              OnStream *on = nullptr, at::Tensor *keep = nullptr)
+{
+    const at::Tensor *c = tensor_or_null(codes, names[0]), *s = tensor_or_null(scales, names[1]);
+    if (on) {
+        const auto bytes = like.options().dtype(at::kByte);
+        keep[0] = c ? *c : on->empty({rows, cols}, bytes);
+        keep[1] = s ? *s : on->empty({rows, cols / 32}, bytes);
+        c = &keep[0];
+        s = &keep[1];
+    }
+    if (!c || !s) throw Refused(std::string(names[0]) + " and " + names[1] + " must be tensors");
+    return Packed{dense(*c, names[0], at::kByte, {rows, cols}, like), dense(*s, names[1], at::kByte, {rows, cols / 32}, like)};
+}
+
 // The handle of the current stream.  The library launches on the current GPU,
 // which the tensors have to be on.
 void *stream_of(const at::Tensor &t)
@@ -271,6 +311,8 @@ PyObject *results(std::initializer_list<const at::Tensor *> ts)
 
 // ---- the calls
 
+const char *kCodes[2] = {"codes", "scales"}, *kCodes8[2] = {"codes8", "scales8"};
+
 PyObject *dropout(PyObject *const *a)
 {
     enum { X, P, SEED, STREAM_ID, RES, Y, STREAM };
@@ -287,37 +329,63 @@ PyObject *dropout(PyObject *const *a)
     return result(y);
 }
 
+template <bool kPack8>
 PyObject *norm(PyObject *const *a)
 {
-    enum { X, GAMMA, BETA, KIND, EPS, RES, P, SEED, STREAM_ID, SAVE, WANT_Y, LAYOUT, Y, H, MEAN, RSTD, CODES, SCALES, STREAM };
+    enum {
+        X, GAMMA, BETA, KIND, EPS, RES, P, SEED, STREAM_ID, SAVE, WANT_Y, LAYOUT, Y, H, MEAN, RSTD, CODES, SCALES, STREAM,
+        CODES8, SCALES8
+    };
     const Like x(a[X], "x");
     OnStream on(a[STREAM], x.t);
     const Matrix mx = x.matrix(x.t, "x"), mr = x.input(a[RES], "residual");
     const double p = real(a[P]);
     const int kind = (int)integer(a[KIND]);
     const bool save = truth(a[SAVE]);
-    at::Tensor y, h, mean, rstd;
+    at::Tensor y, h, mean, rstd, keep8[2];
     const Matrix mh = x.output(on, a[H], "h", a[RES] != Py_None || p > 0, h), my = x.output(on, a[Y], "y", truth(a[WANT_Y]), y);
     float *pm = x.floats(on, a[MEAN], "mean", x.rows, save && kind == FP4Q_NORM_LAYER, mean);
     float *ps = x.floats(on, a[RSTD], "rstd", x.rows, save, rstd);
     int wt = -1;
     const void *pg = x.weight(a[GAMMA], "gamma", wt), *pb = x.weight(a[BETA], "beta", wt);
     const at::Tensor *codes = tensor_or_null(a[CODES], "codes"), *scales = tensor_or_null(a[SCALES], "scales");
+    Packed p8{};
+    if (kPack8) p8 = packed(a[CODES8], a[SCALES8], kCodes8, x.rows, x.cols, x.t, &on, keep8);
     void *st = stream_of(x.t);
-    done("fp4_norm", lib.norm(mx.p, x.rows, x.cols, mx.ld, x.type, mr.p, mr.ld, (float)p, bits64(a[SEED]),
-                              (uint32_t)bits64(a[STREAM_ID]), mh.p, mh.ld, kind, pg, pb, wt < 0 ? FP4Q_OUT_F32 : wt,
-                              (float)real(a[EPS]), my.p, my.ld, pm, ps, codes ? codes->data_ptr() : nullptr,
-                              scales ? scales->data_ptr() : nullptr, (int)integer(a[LAYOUT]), st));
-    on.done();
-    return results({&y, &h, &mean, &rstd});
+    const auto call = [&](auto *fn, auto... more) {
+        return fn(mx.p, x.rows, x.cols, mx.ld, x.type, mr.p, mr.ld, (float)p, bits64(a[SEED]),
+                  (uint32_t)bits64(a[STREAM_ID]), mh.p, mh.ld, kind, pg, pb, wt < 0 ? FP4Q_OUT_F32 : wt,
+                  (float)real(a[EPS]), my.p, my.ld, pm, ps, codes ? codes->data_ptr() : nullptr,
+                  scales ? scales->data_ptr() : nullptr, (int)integer(a[LAYOUT]), more..., st);
+    };
+    if constexpr (kPack8) {
+        done("fp4_norm_pack8", call(lib.norm_pack8, p8.codes, p8.scales));
+        on.done();
+        return results({&y, &h, &mean, &rstd, &keep8[0], &keep8[1]});
+    } else {
+        done("fp4_norm", call(lib.norm));
+        on.done();
+        return results({&y, &h, &mean, &rstd});
+    }
 }
 
+// H: the normed rows, or with kPack8 their codes (and SCALES).
+template <bool kPack8>
 PyObject *norm_grad(PyObject *const *a)
 {
-    enum { DY, H, GAMMA, KIND, MEAN, RSTD, DRES, P, SEED, STREAM_ID, WEIGHTS, DH, DX, DGAMMA, DBETA, WORKSPACE, STREAM };
+    enum {
+        DY, H, GAMMA, KIND, MEAN, RSTD, DRES, P, SEED, STREAM_ID, WEIGHTS, DH, DX, DGAMMA, DBETA, WORKSPACE, STREAM,
+        SCALES
+    };
     const Like x(a[DY], "dy");
     OnStream on(a[STREAM], x.t);
-    const Matrix my = x.matrix(x.t, "dy"), mh = x.matrix(tensor(a[H], "h"), "h"), mr = x.input(a[DRES], "dres");
+    const Matrix my = x.matrix(x.t, "dy"), mr = x.input(a[DRES], "dres");
+    Matrix mh;
+    Packed h8{};
+    if constexpr (kPack8)
+        h8 = packed(a[H], a[SCALES], kCodes, x.rows, x.cols, x.t);
+    else
+        mh = x.matrix(tensor(a[H], "h"), "h");
     const double p = real(a[P]);
     const int kind = (int)integer(a[KIND]);
     const bool weights = truth(a[WEIGHTS]);
@@ -340,17 +408,24 @@ PyObject *norm_grad(PyObject *const *a)
         bytes = lib.norm_grad_workspace(x.rows, x.cols);
         if (bytes) ws = at::empty({(int64_t)bytes}, x.t.options().dtype(at::kByte));
     }
-    done("fp4_norm_grad",
-         lib.norm_grad(my.p, x.rows, x.cols, my.ld, x.type, mh.p, mh.ld, mr.p, mr.ld, kind, gamma,
-                       wt < 0 ? FP4Q_OUT_F32 : wt, pm, ps, (float)p, bits64(a[SEED]), (uint32_t)bits64(a[STREAM_ID]),
-                       md.p, md.ld, mx.p, mx.ld, pg, pb, bytes ? ws.data_ptr() : nullptr, bytes, st));
+    const auto rest = [&](auto *fn, auto... h) {
+        return fn(my.p, x.rows, x.cols, my.ld, x.type, h..., mr.p, mr.ld, kind, gamma, wt < 0 ? FP4Q_OUT_F32 : wt, pm, ps,
+                  (float)p, bits64(a[SEED]), (uint32_t)bits64(a[STREAM_ID]), md.p, md.ld, mx.p, mx.ld, pg, pb,
+                  bytes ? ws.data_ptr() : nullptr, bytes, st);
+    };
+    if constexpr (kPack8)
+        done("fp4_norm_grad_pack8", rest(lib.norm_grad_pack8, h8.codes, h8.scales));
+    else
+        done("fp4_norm_grad", rest(lib.norm_grad, mh.p, mh.ld));
     on.done();
     return results({&dh, &dx, &dgamma, &dbeta});
 }
 
+// C: the gate/up output, or with kPack8 its codes (and SCALES).
+template <bool kPack8>
 PyObject *swiglu_grad(PyObject *const *a)
 {
-    enum { DH, C, PAIR, WANT_H, DC, H, STREAM };
+    enum { DH, C, PAIR, WANT_H, DC, H, STREAM, SCALES };
     const Like x(a[DH], "dh");
     OnStream on(a[STREAM], x.t);
     const Matrix mi = x.matrix(x.t, "dh");
@@ -362,7 +437,12 @@ PyObject *swiglu_grad(PyObject *const *a)
                           std::to_string(2 * F) + "] tensor on its device");
         return rows_of(t, name);
     };
-    const Matrix mc = wide(tensor(a[C], "c"), "c");
+    Matrix mc;
+    Packed c8{};
+    if constexpr (kPack8)
+        c8 = packed(a[C], a[SCALES], kCodes, M, 2 * F, x.t);
+    else
+        mc = wide(tensor(a[C], "c"), "c");
     at::Tensor dc, h;
     if (const at::Tensor *g = tensor_or_null(a[DC], "dc"))
         dc = *g;
@@ -370,8 +450,12 @@ PyObject *swiglu_grad(PyObject *const *a)
         dc = on.empty({M, 2 * F}, x.t.options());
     const Matrix mo = wide(dc, "dc"), mh = x.output(on, a[H], "h", truth(a[WANT_H]), h);
     void *st = stream_of(x.t);
-    done("fp4_swiglu_grad_bf16", lib.swiglu_grad(mi.p, mi.ld, mc.p, M, F, mc.ld, integer(a[PAIR]), mo.p, mo.ld, mh.p,
-                                                 mh.ld, st));
+    if constexpr (kPack8)
+        done("fp4_swiglu_grad_pack8", lib.swiglu_grad_pack8(mi.p, mi.ld, c8.codes, c8.scales, M, F, integer(a[PAIR]),
+                                                            mo.p, mo.ld, mh.p, mh.ld, st));
+    else
+        done("fp4_swiglu_grad_bf16", lib.swiglu_grad(mi.p, mi.ld, mc.p, M, F, mc.ld, integer(a[PAIR]), mo.p, mo.ld, mh.p,
+                                                     mh.ld, st));
     on.done();
     return results({&dc, &h});
 }
@@ -417,6 +501,103 @@ PyObject *rotary(PyObject *const *a)
     return result(y);
 }
 
+PyObject *pack8(PyObject *const *a)
+{
+    enum { X, CODES, SCALES, STREAM };
+    const Like x(a[X], "x");
+    OnStream on(a[STREAM], x.t);
+    const Matrix mx = x.matrix(x.t, "x");
+    at::Tensor keep[2];
+    const Packed p = packed(a[CODES], a[SCALES], kCodes, x.rows, x.cols, x.t, &on, keep);
+    void *st = stream_of(x.t);
+    done("fp4_pack8", lib.pack8(mx.p, x.rows, x.cols, mx.ld, x.type, p.codes, p.scales, st));
+    on.done();
+    return results({&keep[0], &keep[1]});
+}
+
+PyObject *unpack8(PyObject *const *a)
+{
+    enum { CODES, SCALES, TYPE, Y, STREAM };
+    const at::Tensor &codes = tensor(a[CODES], "codes");
+    if (codes.dim() != 2) throw Refused("codes must be a 2-D tensor");
+    OnStream on(a[STREAM], codes);
+    const int64_t rows = codes.size(0), cols = codes.size(1);
+    const Packed p = packed(a[CODES], a[SCALES], kCodes, rows, cols, codes);
+    at::Tensor y;
+    if (const at::Tensor *g = tensor_or_null(a[Y], "y")) {
+        if (g->dim() != 2 || g->sizes() != codes.sizes() || type_of(*g) < 0 || g->device() != codes.device())
+            throw Refused("y must be an fp32 or bf16 tensor of the codes' shape and device");
+        y = *g;
+    } else {
+        y = on.empty({rows, cols}, codes.options().dtype(integer(a[TYPE]) == FP4Q_OUT_BF16 ? at::kBFloat16 : at::kFloat));
+    }
+    const Matrix my = rows_of(y, "y");
+    void *st = stream_of(codes);
+    done("fp4_unpack8", lib.unpack8(p.codes, p.scales, rows, cols, my.p, my.ld, type_of(y), st));
+    on.done();
+    return result(y);
+}
+
+// Products of few rows with FP4 weights.  X: bf16 rows, or where X_SCALES is
+// given the codes of 8-bit rows; TENSOR_SCALE is given where the weights are
+// NVFP4.  N < 0: as many as the codes have rows.
+PyObject *matvec(PyObject *const *a)
+{
+    enum { X, X_SCALES, CODES, SCALES, TENSOR_SCALE, DOMAIN, ALPHA, TYPE, LAYOUT, N, Y, STREAM };
+    const at::Tensor &x = tensor(a[X], "x"), &codes = tensor(a[CODES], "w_codes"), &scales = tensor(a[SCALES], "w_scales");
+    const at::Tensor *ts = tensor_or_null(a[TENSOR_SCALE], "w_tensor_scale");
+    const bool packs = a[X_SCALES] != Py_None;
+    if (x.dim() != 2 || codes.dim() != 2) throw Refused("x and w_codes must be 2-D tensors");
+    if (!packs && x.scalar_type() != at::kBFloat16) throw Refused("x must be bf16");
+    OnStream on(a[STREAM], x);
+    const int64_t m = x.size(0), k = x.size(1), stored = codes.size(0), given = integer(a[N]);
+    const int64_t n = given < 0 ? stored : given;
+    const int layout = (int)integer(a[LAYOUT]), domain = (int)integer(a[DOMAIN]);
+    const int64_t rows = layout == FP4Q_LAYOUT_TILED ? (n + 31) / 32 * 32 : n;  // of the operand
+    dense(codes, "w_codes", at::kByte, {rows, k / 2}, x);
+    if (ts) {
+        dense(scales, "w_scales", at::kByte, {rows, k / 16}, x);
+        const int64_t need = domain == FP4Q_NV_GLOBAL ? 1 : (n + 127) / 128 * (k / 128);
+        if (ts->scalar_type() != at::kFloat || ts->numel() != need || ts->device() != x.device() || !ts->is_contiguous())
+            throw Refused("w_tensor_scale must be " + std::to_string(need) + " contiguous Float elements on the same device");
+    } else if (layout == FP4Q_LAYOUT_TILED) {
+        dense(scales, "w_scales", at::kByte, {k / 128, rows, 4}, x);
+    } else {
+        dense(scales, "w_scales", at::kByte, {rows, k / 32}, x);
+    }
+    Matrix mx{};
+    Packed p{};
+    static const char *names[2] = {"x_codes", "x_scales"};
+    if (packs)
+        p = packed(a[X], a[X_SCALES], names, m, k, x);
+    else
+        mx = rows_of(x, "x");
+    at::Tensor y;
+    if (const at::Tensor *g = tensor_or_null(a[Y], "y")) {
+        if (g->dim() != 2 || g->size(0) != m || g->size(1) != n || type_of(*g) < 0 || g->device() != x.device())
+            throw Refused("y must be an fp32 or bf16 [" + std::to_string(m) + " x " + std::to_string(n) +
+                          "] tensor on the same device");
+        y = *g;
+    } else {
+        y = on.empty({m, n}, x.options().dtype(integer(a[TYPE]) == FP4Q_OUT_BF16 ? at::kBFloat16 : at::kFloat));
+    }
+    const Matrix my = rows_of(y, "y");
+    const float alpha = (float)real(a[ALPHA]);
+    void *st = stream_of(x);
+    if (ts)
+        done("fp4_matvec_nv", lib.matvec_nv(mx.p, m, k, mx.ld, codes.data_ptr(), scales.data_ptr(),
+                                            static_cast<const float *>(ts->data_ptr()), domain, n, alpha, layout, my.p,
+                                            type_of(y), my.ld, st));
+    else if (packs)
+        done("fp4_matvec_mx_pack8", lib.matvec_mx_pack8(p.codes, p.scales, m, k, codes.data_ptr(), scales.data_ptr(), n,
+                                                        alpha, layout, my.p, type_of(y), my.ld, st));
+    else
+        done("fp4_matvec_mx", lib.matvec_mx(mx.p, m, k, mx.ld, codes.data_ptr(), scales.data_ptr(), n, alpha, layout, my.p,
+                                            type_of(y), my.ld, st));
+    on.done();
+    return result(y);
+}
+
 // ---- the module
 
 template <PyObject *(*kCall)(PyObject *const *), Py_ssize_t kArgs>
@@ -439,9 +620,10 @@ PyObject *entry(PyObject *, PyObject *const *args, Py_ssize_t n)
 
 PyObject *bind(PyObject *, PyObject *args)
 {
-    unsigned long long f[6];
+    unsigned long long f[14];
     PyObject *error, *current, *raw, *external;
-    if (!PyArg_ParseTuple(args, "KKKKKKOOOO", &f[0], &f[1], &f[2], &f[3], &f[4], &f[5], &error, &current, &raw, &external))
+    if (!PyArg_ParseTuple(args, "(KKKKKKKKKKKKKK)OOOO", &f[0], &f[1], &f[2], &f[3], &f[4], &f[5], &f[6], &f[7], &f[8],
+                          &f[9], &f[10], &f[11], &f[12], &f[13], &error, &current, &raw, &external))
         return nullptr;
     Py_INCREF(error);
     Py_INCREF(current);
@@ -453,6 +635,14 @@ PyObject *bind(PyObject *, PyObject *args)
     lib.norm_grad = reinterpret_cast<decltype(lib.norm_grad)>(f[3]);
     lib.swiglu_grad = reinterpret_cast<decltype(lib.swiglu_grad)>(f[4]);
     lib.rotary = reinterpret_cast<decltype(lib.rotary)>(f[5]);
+    lib.pack8 = reinterpret_cast<decltype(lib.pack8)>(f[6]);
+    lib.unpack8 = reinterpret_cast<decltype(lib.unpack8)>(f[7]);
+    lib.norm_pack8 = reinterpret_cast<decltype(lib.norm_pack8)>(f[8]);
+    lib.norm_grad_pack8 = reinterpret_cast<decltype(lib.norm_grad_pack8)>(f[9]);
+    lib.swiglu_grad_pack8 = reinterpret_cast<decltype(lib.swiglu_grad_pack8)>(f[10]);
+    lib.matvec_mx = reinterpret_cast<decltype(lib.matvec_mx)>(f[11]);
+    lib.matvec_mx_pack8 = reinterpret_cast<decltype(lib.matvec_mx_pack8)>(f[12]);
+    lib.matvec_nv = reinterpret_cast<decltype(lib.matvec_nv)>(f[13]);
     lib.error = error;
     lib.current = current;
     lib.raw = raw;
@@ -464,10 +654,16 @@ template <typename F> PyCFunction method(F *f) { return reinterpret_cast<PyCFunc
 
 PyMethodDef methods[] = {{"bind", bind, METH_VARARGS, "the library's entry points, Fp4qError, torch's current device and stream, ExternalStream"},
                          {"dropout", method(entry<dropout, 7>), METH_FASTCALL, nullptr},
-                         {"norm", method(entry<norm, 19>), METH_FASTCALL, nullptr},
-                         {"norm_grad", method(entry<norm_grad, 17>), METH_FASTCALL, nullptr},
-                         {"swiglu_grad", method(entry<swiglu_grad, 7>), METH_FASTCALL, nullptr},
+                         {"norm", method(entry<norm<false>, 19>), METH_FASTCALL, nullptr},
+                         {"norm_grad", method(entry<norm_grad<false>, 17>), METH_FASTCALL, nullptr},
+                         {"swiglu_grad", method(entry<swiglu_grad<false>, 7>), METH_FASTCALL, nullptr},
                          {"rotary", method(entry<rotary, 8>), METH_FASTCALL, nullptr},
+                         {"pack8", method(entry<pack8, 4>), METH_FASTCALL, nullptr},
+                         {"unpack8", method(entry<unpack8, 5>), METH_FASTCALL, nullptr},
+                         {"norm_pack8", method(entry<norm<true>, 21>), METH_FASTCALL, nullptr},
+                         {"norm_grad_pack8", method(entry<norm_grad<true>, 18>), METH_FASTCALL, nullptr},
+                         {"swiglu_grad_pack8", method(entry<swiglu_grad<true>, 8>), METH_FASTCALL, nullptr},
+                         {"matvec", method(entry<matvec, 12>), METH_FASTCALL, nullptr},
                          {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_row_calls", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 

@@ -237,6 +237,21 @@ __device__ __forceinline__ void store_chunk(T *row, const Span &s, const Chunk<T
     }
 }
 
+// A chunk of a weight vector of either type, loaded where it is used.
+template <Edge kEdge>
+__device__ __forceinline__ void weights_now(const void *w, bool bf16, const Span &s, uint32_t cols, float v[8])
+{
+    if (bf16) {
+        Chunk<bf16_t> q;
+        load_chunk<bf16_t, kEdge>(reinterpret_cast<const bf16_t *>(w), s, cols, q);
+        q.get(v);
+    } else {
+        Chunk<float> q;
+        load_chunk<float, kEdge>(reinterpret_cast<const float *>(w), s, cols, q);
+        q.get(v);
+    }
+}
+
 // Sums by DPP, in a fixed order and without LDS: shifts inside the rows of 16
 // lanes, then for the whole wave two broadcasts across rows.
 template <int kCtrl, int kRowMask>

@@ -14,6 +14,7 @@
 #include <stdint.h>
 
 #include "fp4q_internal.h"
+#include "pack8.h"
 #include "row_ops.h"
 
 namespace fp4q {
@@ -47,9 +48,10 @@ __device__ __forceinline__ void sigmoid_pair(float x, float &s, float &c)
 // row / chunks run on, with h: 8192 x 14336 237 / 242 us; with the last
 // workgroup of a row part empty / run on, 8192 x 11008 210 / 183, 16384 x
 // 2080 111 / 73, 65536 x 64 55 / 13.
-template <bool kH, bool kRows>
-__global__ __launch_bounds__(kThreads) void swiglu_grad_kernel(const uint16_t *dh, const uint16_t *c, uint16_t *dc,
-                                                               uint16_t *h, int64_t M, int64_t ld_dh, int64_t ldc,
+template <bool kH, bool kRows, bool kPack8>
+__global__ __launch_bounds__(kThreads) void swiglu_grad_kernel(const uint16_t *dh, const uint16_t *c,
+                                                               const uint8_t *codes, const uint8_t *scales,
+                                                               uint16_t *dc, uint16_t *h, int64_t M, int64_t ld_dh, int64_t ldc,
                                                                int64_t ld_dc, int64_t ldh, uint32_t rows,
                                                                uint32_t per_row, FastDiv row_div, uint32_t pair_chunks,
                                                                FastDiv pair_div)
@@ -61,18 +63,27 @@ __global__ __launch_bounds__(kThreads) void swiglu_grad_kernel(const uint16_t *d
     const bool in = r < rows && row0 + r < M;
     const int64_t m = in ? row0 + r : row0;  // past the end: a chunk of the first row, not stored
     const int64_t j = (int64_t)k * 8, gcol = j + (int64_t)fast_div(k, pair_div) * pair;
-    const uint16_t *row = c + m * ldc;
-    const u32x4v g = *reinterpret_cast<const u32x4v *>(row + gcol);
-    const u32x4v u = *reinterpret_cast<const u32x4v *>(row + gcol + pair);
+    typename std::conditional<kPack8, Packed8, Chunk<bf16_t>>::type g, u;
+    if constexpr (kPack8) {  // dense rows
+        const uint64_t at = (uint64_t)(m * ldc + gcol) >> 3;
+        g.template load<false>(codes, scales, at);
+        u.template load<false>(codes, scales, at + pair_chunks);
+    } else {
+        const uint16_t *row = c + m * ldc;
+        g.q = *reinterpret_cast<const u32x4v *>(row + gcol);
+        u.q = *reinterpret_cast<const u32x4v *>(row + gcol + pair);
+    }
     const u32x4v d = *reinterpret_cast<const u32x4v *>(dh + m * ld_dh + j);
     u32x4v og, ou, oh;
+    float gs[8], us[8];
+    g.get(gs);
+    u.get(us);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         float a[2], b[2], e[2];
 #pragma unroll
         for (int n = 0; n < 2; ++n) {
-            const float gv = n ? bf16_hi(g[i]) : bf16_lo(g[i]);
-            const float uv = n ? bf16_hi(u[i]) : bf16_lo(u[i]);
+            const float gv = gs[2 * i + n], uv = us[2 * i + n];
             const float dv = n ? bf16_hi(d[i]) : bf16_lo(d[i]);
             float sg, cg;
             sigmoid_pair(gv, sg, cg);
@@ -92,7 +103,7 @@ __global__ __launch_bounds__(kThreads) void swiglu_grad_kernel(const uint16_t *d
     if (kH) *reinterpret_cast<u32x4v *>(h + m * ldh + j) = oh;
 }
 
-template <bool kH, bool kRows>
+template <bool kH, bool kRows, bool kPack8>
 void run(const SwigluGradArgs &a, hipStream_t st)
 {
     const uint32_t chunks = (uint32_t)(a.F / 8), pair_chunks = (uint32_t)(a.pair / 8);
@@ -100,22 +111,28 @@ void run(const SwigluGradArgs &a, hipStream_t st)
     int64_t rows = ((int64_t)1 << 31) / chunks;
     if (rows > a.M) rows = a.M;
     const dim3 grid((unsigned)((rows * chunks + kThreads - 1) / kThreads), (unsigned)((a.M + rows - 1) / rows));
-    hipLaunchKernelGGL((swiglu_grad_kernel<kH, kRows>), grid, dim3(kThreads), 0, st,
+    hipLaunchKernelGGL((swiglu_grad_kernel<kH, kRows, kPack8>), grid, dim3(kThreads), 0, st,
                        reinterpret_cast<const uint16_t *>(a.dh), reinterpret_cast<const uint16_t *>(a.c),
-                       reinterpret_cast<uint16_t *>(a.dc), reinterpret_cast<uint16_t *>(a.h), a.M, a.ld_dh, a.ldc,
-                       a.ld_dc, a.ldh, (uint32_t)rows, per_row, fast_div_for(per_row), pair_chunks,
+                       a.c_codes, a.c_scales, reinterpret_cast<uint16_t *>(a.dc), reinterpret_cast<uint16_t *>(a.h),
+                       a.M, a.ld_dh, kPack8 ? 2 * a.F : a.ldc, a.ld_dc, a.ldh, (uint32_t)rows, per_row, fast_div_for(per_row), pair_chunks,
                        fast_div_for(pair_chunks));
+}
+
+template <bool kPack8>
+void pick(const SwigluGradArgs &a, hipStream_t st)
+{
+    const bool whole = a.F % (8 * kThreads) == 0;
+    if (a.h)
+        whole ? run<true, true, kPack8>(a, st) : run<true, false, kPack8>(a, st);
+    else
+        whole ? run<false, true, kPack8>(a, st) : run<false, false, kPack8>(a, st);
 }
 
 }  // namespace
 
 int launch_swiglu_grad(const SwigluGradArgs &a, hipStream_t st)
 {
-    const bool whole = a.F % (8 * kThreads) == 0;
-    if (a.h)
-        whole ? run<true, true>(a, st) : run<true, false>(a, st);
-    else
-        whole ? run<false, true>(a, st) : run<false, false>(a, st);
+    a.c_codes ? pick<true>(a, st) : pick<false>(a, st);
     return hipGetLastError() == hipSuccess ? 0 : 1;
 }
 

@@ -460,6 +460,92 @@ FP4Q_API fp4q_status fp4_rotary(const void *x, int64_t tokens, int64_t heads, in
                                 const float *inv_freq, int64_t rot, int style, int inverse, float scale, void *y,
                                 int64_t y_token, int64_t y_head, void *stream);
 
+/* ------------------------------------------------------------------------
+ * 8-bit block-scaled rows: activations in 33/64 of their bf16 bytes, as a norm
+ * leaves them for a decoding step's linear layers, or as a training step keeps
+ * them for its backward pass.
+ *
+ *   codes   [rows x cols] bytes, row-major and dense: OCP FP8 E4M3;
+ *   scales  [rows x cols/32] bytes, row-major and dense: E8M0, byte = E + 127.
+ * Along rows, cols % 32 == 0 (FP4Q_ESHAPE).  An element stands for e4m3(code) *
+ * 2^E.  Of a block of 32, E is the least integer with amax <= 448 * 2^E, amax
+ * being its largest finite magnitude, clamped to [-127, 119] (-127 where amax
+ * is 0); code = E4M3_RNE(x * 2^-E), at E = 119 with magnitudes above 448 *
+ * 2^119 taken as that.  So no finite element saturates below 448 * 2^119 (the
+ * exponent floor(log2 amax) - 8 of OCP MX v1.0 would let those above 448 * 2^E,
+ * off by up to an eighth), and each is off by at most 2^-4 of its value or
+ * 2^(E - 10).  A NaN or an infinity is kept as E4M3's NaN (0x7F with the
+ * element's sign bit) and does not touch the block's other elements.
+ * codes 16-byte aligned (FP4Q_EALIGN), scales at any address.  Sizes and other
+ * errors as for the row-wise operators above.
+ * ------------------------------------------------------------------------ */
+
+/* x (binary32 or bf16 rows) packed. */
+FP4Q_API fp4q_status fp4_pack8(const void *x, int64_t rows, int64_t cols, int64_t ld_x, int type, void *codes,
+                               void *scales, void *stream);
+
+/* The packed rows' values, rounded to `type` (which rounds only bf16 values
+ * below 2^-120). */
+FP4Q_API fp4q_status fp4_unpack8(const void *codes, const void *scales, int64_t rows, int64_t cols, void *y,
+                                 int64_t ld_y, int type, void *stream);
+
+/* fp4_norm, with y packed as well: codes8 and scales8 byte for byte as
+ * fp4_pack8 makes them of y (as rounded to `type`, whether y itself is asked
+ * for or not).  y and the MXFP4 operand (codes, scales: bf16 only) are both
+ * optional.  Errors as fp4_norm, and FP4Q_ESHAPE for cols % 32 != 0. */
+FP4Q_API fp4q_status fp4_norm_pack8(const void *x, int64_t rows, int64_t cols, int64_t ld_x, int type,
+                                    const void *residual, int64_t ld_r, float p, uint64_t seed, uint32_t stream_id,
+                                    void *h, int64_t ld_h, int kind, const void *gamma, const void *beta, int w_type,
+                                    float eps, void *y, int64_t ld_y, float *mean, float *rstd, void *codes,
+                                    void *scales, int layout, void *codes8, void *scales8, void *stream);
+
+/* fp4_norm_grad, with the normed rows h kept by fp4_pack8 (h_codes, h_scales):
+ * every output bit is that of fp4_norm_grad on the rows as binary32 values
+ * (fp4_unpack8).  mean and rstd are the statistics that the forward pass
+ * wrote, those of h before it was packed.  The workspace is
+ * fp4q_norm_grad_workspace_bytes' for these rows and columns.  dh and dx may
+ * each be dy or dres. */
+FP4Q_API fp4q_status fp4_norm_grad_pack8(const void *dy, int64_t rows, int64_t cols, int64_t ld_dy, int type,
+                                         const void *h_codes, const void *h_scales, const void *dres, int64_t ld_dres,
+                                         int kind, const void *gamma, int w_type, const float *mean, const float *rstd,
+                                         float p, uint64_t seed, uint32_t stream_id, void *dh, int64_t ld_dh, void *dx,
+                                         int64_t ld_dx, float *dgamma, float *dbeta, void *workspace,
+                                         size_t workspace_bytes, void *stream);
+
+/* fp4_swiglu_grad_bf16, with the gate/up GEMM's output c kept by fp4_pack8 as
+ * [M x 2F] (c_codes, c_scales; 2F % 32 == 0): dc and h bit for bit as that
+ * call makes them of c's values (h is thus SwiGLU of the packed c, not of the
+ * c that the forward pass had).  h may be dh. */
+FP4Q_API fp4q_status fp4_swiglu_grad_pack8(const void *dh, int64_t ld_dh, const void *c_codes, const void *c_scales,
+                                           int64_t M, int64_t F, int64_t pair, void *dc, int64_t ld_dc, void *h,
+                                           int64_t ldh, void *stream);
+
+/* Products of few rows with FP4 weights, Y[M x N] = alpha * x * W^T: the
+ * linear layers of a decoding step, whose activations stay in 16 or 8 bits.
+ * 0 <= M <= 64 (FP4Q_EUNSUPPORTED above: quantize x and use the GEMM).  W is
+ * the logical [N x K] operand as the producers write it for the GEMMs, in
+ * `layout`; every product of a weight and an element of x is exact, the sums
+ * are binary32 in an order that depends on the sizes alone, alpha (and a
+ * global tensor scale) multiplies them, and one rounding gives Y's type (a
+ * value of fp4q_out, pitch ld_y >= N).  K % 128 == 0 (FP4Q_ESHAPE); K == 0
+ * gives zeros.  NaN and Inf in x stay within their row of Y.
+ * x: bf16, 16-byte aligned, ld_x a multiple of 8 (FP4Q_EALIGN).  Codes, scales
+ * and Y aligned and bounded as the GEMMs' operands and C. */
+FP4Q_API fp4q_status fp4_matvec_mx(const void *x, int64_t M, int64_t K, int64_t ld_x, const void *w_codes,
+                                   const void *w_scales, int64_t N, float alpha, int layout, void *y, int y_type,
+                                   int64_t ld_y, void *stream);
+
+/* The same with x as 8-bit rows [M x K], whose elements count as their bf16
+ * values (those fp4_unpack8 gives). */
+FP4Q_API fp4q_status fp4_matvec_mx_pack8(const void *x_codes, const void *x_scales, int64_t M, int64_t K,
+                                         const void *w_codes, const void *w_scales, int64_t N, float alpha, int layout,
+                                         void *y, int y_type, int64_t ld_y, void *stream);
+
+/* The same with NVFP4 weights of either domain. */
+FP4Q_API fp4q_status fp4_matvec_nv(const void *x, int64_t M, int64_t K, int64_t ld_x, const void *w_codes,
+                                   const void *w_scales, const float *w_tensor_scale, int domain, int64_t N,
+                                   float alpha, int layout, void *y, int y_type, int64_t ld_y, void *stream);
+
 /* Human-readable text for a status code (static storage). */
 FP4Q_API const char *fp4q_status_str(int status);
 
