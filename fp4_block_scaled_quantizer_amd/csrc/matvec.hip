@@ -80,183 +80,277 @@ __device__ __forceinline__ bf16x8v rows8(uint32_t lo, uint32_t hi, float scale)
 
 enum Format { kMx, kNvGlobal, kNvTile };
 
-// What a wave loads of one step.
-template <Format kFormat, bool kX8, int kMT, int kR>
+// Four neighbouring elements of row m of Y.
+__device__ __forceinline__ void store4(const Matvec &a, uint32_t m, uint32_t n, const f32x4v &v)
+{
+    const int64_t at = (int64_t)m * a.ld_y + n;
+    if (a.y_bf16) {
+        bf16_t *y = reinterpret_cast<bf16_t *>(a.y) + at;
+        const u32x2v w = {pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])};
+        if (n + 3u < a.N) {
+            *reinterpret_cast<u32x2_a2 *>(y) = w;
+        } else {
+#pragma unroll
+            for (uint32_t e = 0; e < 4u; ++e)
+                if (n + e < a.N) y[e].bits = (uint16_t)(w[e >> 1] >> (16u * (e & 1u)));
+        }
+    } else {
+        float *y = reinterpret_cast<float *>(a.y) + at;
+        if (n + 3u < a.N) {
+            *reinterpret_cast<u32x4_a4 *>(y) = __builtin_bit_cast(u32x4v, v);
+        } else {
+#pragma unroll
+            for (uint32_t e = 0; e < 4u; ++e)
+                if (n + e < a.N) y[e] = v[e];
+        }
+    }
+}
+
+// What a wave loads of one step of kP * 128 columns.  kMQ: groups of four rows
+// of x, of which a load (16 bytes a lane, 64 lanes) takes one for each 128
+// columns in bf16 and two in 8 bits, whole cache lines either way.
+template <Format kFormat, bool kX8, int kMQ, int kR, int kP>
 struct Step {
-    u32x4v codes[kR];
+    static constexpr int kLoads = kX8 ? (kMQ * kP + 1) / 2 : kMQ * kP;
+    u32x4v x[kLoads];
+    uint32_t x_scale[kX8 ? kLoads : 1];
+    u32x4v codes[kR][kP];
     uint32_t scales[kR];
     float tile[kFormat == kNvTile ? kR : 1];
-    u32x4v x[kMT][kX8 ? 2 : 4];
-    uint32_t x_scale[kX8 ? kMT : 1];
 };
 
-// kMT: 16 rows of x each; kR: 16 rows of W each.  grid.x: groups of 16 kR
-// rows of W.
-template <Format kFormat, bool kX8, int kMT, int kR>
-__global__ __launch_bounds__(kMT <= 2 ? 1024 : 512) void matvec_kernel(const Matvec a)
+// How a kernel is made: rows of x and bytes of each that a wave keeps in LDS,
+// steps that it has in flight, and the most waves of a workgroup.
+template <bool kX8, int kMQ, int kR, int kP>
+struct Shape {
+    static constexpr int kMT = (kMQ + 3) / 4, kTiles = kR * kMT;  // 16 x 16 results
+    static constexpr int kRows = kX8 && kMQ * kP == 1 ? 8 : kMQ * 4;
+    static constexpr uint32_t kPitch = 256 * kP + 16;  // 16 rows' pieces lie in all banks alike
+    static constexpr int kAhead = kR == 1 && kMQ <= 4 && kP == 1 ? 2 : 1;
+    static constexpr int kWaves = kR == 1 && kMQ <= 2 && kP == 1 ? 16 : kRows * kPitch * 8 <= 160 * 1024 ? 8 : 4;
+    static constexpr int kAtOnce = kTiles < 64 / kWaves ? kTiles : 64 / kWaves;  // tiles joined at once, in 64 KiB at most
+    static uint32_t lds_bytes(uint32_t waves)
+    {
+        const uint32_t x = waves * kRows * kPitch, sums = waves * kAtOnce * 1024u;
+        return x > sums ? x : sums;
+    }
+};
+
+// kR: 16 rows of W each; grid.x: groups of 16 kR rows of W.  kP = 2 is for W in
+// rows (the linear layout): a lane then takes 32 neighbouring bytes, so that a
+// wave's two loads are 128 bytes of each row, and all its scales with one.
+template <Format kFormat, bool kX8, int kMQ, int kR, int kP>
+__global__ __launch_bounds__((Shape<kX8, kMQ, kR, kP>::kWaves * 64)) void matvec_kernel(const Matvec a)
 {
-    extern __shared__ __attribute__((aligned(16))) float parts[];  // [waves][kR * kMT][64][4]
-    constexpr int kTiles = kR * kMT;
+    typedef Step<kFormat, kX8, kMQ, kR, kP> S;
+    typedef Shape<kX8, kMQ, kR, kP> H;
+    extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
     const uint32_t lane = threadIdx.x & 63u, r = lane & 15u, q = lane >> 4;
     const uint32_t wave = (uint32_t)__builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6)), waves = blockDim.x >> 6;
-    const uint32_t n0 = blockIdx.x * (16u * kR);
-    const uint32_t from = a.steps * wave / waves, to = a.steps * (wave + 1u) / waves;
+    const uint32_t n0 = blockIdx.x * (16u * kR), steps = a.steps / kP;
+    const uint32_t from = steps * wave / waves, to = steps * (wave + 1u) / waves;
 
-    const uint8_t *codes[kR], *scales[kR], *x[kMT], *x_scales[kX8 ? kMT : 1];
+    const uint8_t *codes[kR], *scales[kR], *x[S::kLoads], *x_scales[kX8 ? S::kLoads : 1];
     const float *tile[kFormat == kNvTile ? kR : 1];
 #pragma unroll
     for (int j = 0; j < kR; ++j) {  // past W's end: its last row again, not stored
         const uint32_t n = min(n0 + 16u * j + r, a.N - 1u);
         codes[j] = a.w.codes + (int64_t)(n >> 5) * a.w.code_group + (int64_t)(n & 31u) * a.w.code_row +
-                   (q >> 1) * a.w.code_pair + (q & 1u) * a.w.code_q;
-        scales[j] = a.w.scales + (int64_t)(n >> 5) * a.w.scale_group + (int64_t)(n & 31u) * a.w.scale_row + q * a.w.scale_q;
+                   (kP == 2 ? q * 32u : (q >> 1) * a.w.code_pair + (q & 1u) * a.w.code_q);
+        scales[j] = a.w.scales + (int64_t)(n >> 5) * a.w.scale_group + (int64_t)(n & 31u) * a.w.scale_row +
+                    q * a.w.scale_q * kP;
         // 16 rows are within one 128 x 128 tile
         if (kFormat == kNvTile) tile[j] = a.tensor_scale + (int64_t)(min(n0 + 16u * j, a.N - 1u) >> 7) * a.steps;
     }
+    constexpr uint32_t kPer = (kX8 ? 8 : 16) * kP;  // lanes of a row of x
 #pragma unroll
-    for (int i = 0; i < kMT; ++i) {  // past x's end: its last row again, in columns of D that are not stored
-        const uint32_t m = min(16u * i + r, a.M - 1u);
-        x[i] = a.x + (int64_t)m * a.ld_x * (kX8 ? 1 : 2) + q * (kX8 ? 32u : 64u);
-        if (kX8) x_scales[i] = a.x_scales + (int64_t)m * (a.steps * 4u) + q;
+    for (int i = 0; i < S::kLoads; ++i) {  // past x's end: its last row again, in columns of the result not stored
+        const uint32_t at = i * 64u + lane, m = min(at / kPer, a.M - 1u);
+        x[i] = a.x + (int64_t)m * a.ld_x * (kX8 ? 1 : 2) + at % kPer * 16u;
+        if (kX8) x_scales[i] = a.x_scales + (int64_t)m * (a.steps * 4u) + at % kPer / 2u;
     }
-    typedef Step<kFormat, kX8, kMT, kR> S;
     const auto fetch = [&](uint32_t step, S &s) {
 #pragma unroll
+        for (int i = 0; i < S::kLoads; ++i) {
+            s.x[i] = *reinterpret_cast<const u32x4v *>(x[i] + step * ((kX8 ? 128u : 256u) * kP));
+            if (kX8) s.x_scale[i] = x_scales[i][step * (4u * kP)];
+        }
+#pragma unroll
         for (int j = 0; j < kR; ++j) {
-            s.codes[j] = __builtin_nontemporal_load(reinterpret_cast<const u32x4v *>(codes[j] + step * a.w.code_step));
-            const uint8_t *p = scales[j] + step * a.w.scale_step;
-            s.scales[j] = kFormat == kMx ? (uint32_t)*p : (uint32_t)*reinterpret_cast<const uint16_t *>(p);
+            const u32x4v *p = reinterpret_cast<const u32x4v *>(codes[j] + step * kP * a.w.code_step);
+#pragma unroll
+            for (int k = 0; k < kP; ++k) s.codes[j][k] = load_vec<kP == 1>(p + k);
+            const uint8_t *b = scales[j] + step * kP * a.w.scale_step;
+            constexpr int kBytes = (kFormat == kMx ? 1 : 2) * kP;
+            if constexpr (kBytes == 1)
+                s.scales[j] = *b;
+            else if constexpr (kBytes == 2)
+                s.scales[j] = *reinterpret_cast<const uint16_t *>(b);
+            else
+                s.scales[j] = *reinterpret_cast<const uint32_t *>(b);
             if (kFormat == kNvTile) s.tile[j] = tile[j][step];
         }
-#pragma unroll
-        for (int i = 0; i < kMT; ++i) {
-            const u32x4v *p = reinterpret_cast<const u32x4v *>(x[i] + step * (kX8 ? 128u : 256u));
-#pragma unroll
-            for (int k = 0; k < (kX8 ? 2 : 4); ++k) s.x[i][k] = p[k];
-            if (kX8) s.x_scale[i] = x_scales[i][step * 4u];
-        }
     };
-    f32x4v acc[kR][kMT];
+    f32x4v acc[kR][H::kMT];
 #pragma unroll
     for (int j = 0; j < kR; ++j) {
 #pragma unroll
-        for (int i = 0; i < kMT; ++i) acc[j][i] = (f32x4v){0.0f, 0.0f, 0.0f, 0.0f};
+        for (int i = 0; i < H::kMT; ++i) acc[j][i] = (f32x4v){0.0f, 0.0f, 0.0f, 0.0f};
     }
+    // A wave's step of x goes through its own part of LDS, as bf16, from the
+    // lanes that loaded it to those that multiply it.  A wave's LDS accesses
+    // are done in their order, so no wait but the fences that keep the
+    // compiler to it.
+    uint8_t *own = lds + wave * (H::kRows * H::kPitch);
+    const uint8_t *mine = own + (kMQ < 4 ? r % (kMQ * 4u) : r) * H::kPitch + q * (64u * kP);
     const auto multiply = [&](const S &s) {
-        bf16x8v b[kMT][4];
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
 #pragma unroll
-        for (int i = 0; i < kMT; ++i) {
-            const float xs = kX8 ? mx_scale_f32(s.x_scale[i]) : 1.0f;
-#pragma unroll
-            for (int k = 0; k < 4; ++k)
-                b[i][k] = kX8 ? rows8(s.x[i][k >> 1][2 * (k & 1)], s.x[i][k >> 1][2 * (k & 1) + 1], xs)
-                              : __builtin_bit_cast(bf16x8v, s.x[i][kX8 ? 0 : k]);
+        for (int i = 0; i < S::kLoads; ++i) {
+            const uint32_t at = i * 64u + lane;
+            uint8_t *to = own + at / kPer * H::kPitch + at % kPer * (kX8 ? 32u : 16u);
+            if constexpr (kX8) {
+                const float scale = mx_scale_f32(s.x_scale[i]);
+                *reinterpret_cast<bf16x8v *>(to) = rows8(s.x[i][0], s.x[i][1], scale);
+                *reinterpret_cast<bf16x8v *>(to + 16) = rows8(s.x[i][2], s.x[i][3], scale);
+            } else {
+                *reinterpret_cast<u32x4v *>(to) = s.x[i];
+            }
         }
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
 #pragma unroll
-        for (int j = 0; j < kR; ++j) {
-            const f32x2v nv = __builtin_amdgcn_cvt_pk_f32_fp8(s.scales[j], false);
-            f32x4v sum[kMT];
+        for (int p = 0; p < kP; ++p) {
+            bf16x8v b[H::kMT][4];
 #pragma unroll
-            for (int i = 0; i < kMT; ++i) sum[i] = kFormat == kNvTile ? (f32x4v){0.0f, 0.0f, 0.0f, 0.0f} : acc[j][i];
+            for (int i = 0; i < H::kMT; ++i) {
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                const bf16x8v w = kFormat == kMx ? weights8_mx(s.codes[j][k], mx_scale_f32(s.scales[j]))
-                                                 : weights8_nv(s.codes[j][k], nv[k >> 1]);
-#pragma unroll
-                for (int i = 0; i < kMT; ++i) sum[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(w, b[i][k], sum[i], 0, 0, 0);
+                for (int k = 0; k < 4; ++k)
+                    b[i][k] = *reinterpret_cast<const bf16x8v *>(mine + i * (16u * H::kPitch) + p * 64u + k * 16u);
             }
 #pragma unroll
-            for (int i = 0; i < kMT; ++i) {
-                if (kFormat == kNvTile) {
+            for (int j = 0; j < kR; ++j) {
+                const uint32_t scales = kFormat == kMx ? s.scales[j] >> (8 * p) & 255u : s.scales[j] >> (16 * p);
+                const f32x2v nv = __builtin_amdgcn_cvt_pk_f32_fp8(scales, false);
+                f32x4v sum[H::kMT];
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) acc[j][i][e] = __builtin_fmaf(sum[i][e], s.tile[kFormat == kNvTile ? j : 0], acc[j][i][e]);
-                } else {
-                    acc[j][i] = sum[i];
+                for (int i = 0; i < H::kMT; ++i)
+                    sum[i] = kFormat == kNvTile ? (f32x4v){0.0f, 0.0f, 0.0f, 0.0f} : acc[j][i];
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const bf16x8v w = kFormat == kMx ? weights8_mx(s.codes[j][p][k], mx_scale_f32(scales))
+                                                     : weights8_nv(s.codes[j][p][k], nv[k >> 1]);
+#pragma unroll
+                    for (int i = 0; i < H::kMT; ++i)
+                        sum[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(w, b[i][k], sum[i], 0, 0, 0);
+                }
+#pragma unroll
+                for (int i = 0; i < H::kMT; ++i) {
+                    if (kFormat == kNvTile) {
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            acc[j][i][e] = __builtin_fmaf(sum[i][e], s.tile[kFormat == kNvTile ? j : 0], acc[j][i][e]);
+                    } else {
+                        acc[j][i] = sum[i];
+                    }
                 }
             }
         }
     };
     if (from < to) {
-        S one, two;
-        fetch(from, one);
-        for (uint32_t step = from; step < to; step += 2u) {  // past the wave's last step: it again, not used
-            fetch(min(step + 1u, to - 1u), two);
-            multiply(one);
-            if (step + 1u >= to) break;
-            fetch(min(step + 2u, to - 1u), one);
-            multiply(two);
+        S s[H::kAhead];
+#pragma unroll
+        for (int d = 0; d < H::kAhead; ++d) fetch(min(from + d, to - 1u), s[d]);
+        for (uint32_t step = from; step < to; step += H::kAhead) {  // past the wave's last step: it again, not used
+#pragma unroll
+            for (int d = 0; d < H::kAhead; ++d) {
+                if (d > 0 && step + d >= to) break;
+                multiply(s[d]);
+                __builtin_amdgcn_sched_barrier(0);
+                fetch(min(step + H::kAhead + d, to - 1u), s[d]);
+                __builtin_amdgcn_sched_barrier(0);
+            }
         }
     }
-    f32x4v *mine = reinterpret_cast<f32x4v *>(parts) + wave * (kTiles * 64u) + lane;
-#pragma unroll
-    for (int j = 0; j < kR; ++j) {
-#pragma unroll
-        for (int i = 0; i < kMT; ++i) mine[(j * kMT + i) * 64] = acc[j][i];
-    }
-    __syncthreads();
+    __syncthreads();  // the sums take x's place
+    f32x4v *parts = reinterpret_cast<f32x4v *>(lds);  // [tiles][waves][64]
     const float scale = kFormat == kNvGlobal ? a.tensor_scale[0] : 1.0f;
-    for (uint32_t t = wave; t < (uint32_t)kTiles; t += waves) {
-        const f32x4v *p = reinterpret_cast<const f32x4v *>(parts) + t * 64u + lane;
-        f32x4v sum = p[0];
-        for (uint32_t k = 1; k < waves; ++k) sum += p[k * (kTiles * 64u)];
-        // lane l has rows 4 (l / 16) .. + 3 of the tile's 16 of W, row l mod 16 of x
-        const uint32_t n = n0 + t / kMT * 16u + q * 4u, m = t % kMT * 16u + r;
-        if (m >= a.M) continue;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) sum[e] = sum[e] * scale * a.alpha;
-        const int64_t at = (int64_t)m * a.ld_y + n;
-        if (a.y_bf16) {
-            bf16_t *y = reinterpret_cast<bf16_t *>(a.y) + at;
-            const u32x2v v = {pack_bf16x2(sum[0], sum[1]), pack_bf16x2(sum[2], sum[3])};
-            if (n + 3u < a.N) {
-                *reinterpret_cast<u32x2_a2 *>(y) = v;
-            } else {
+    for (int t0 = 0; t0 < H::kTiles; t0 += H::kAtOnce) {
+        if (t0 > 0) __syncthreads();
 #pragma unroll
-                for (uint32_t e = 0; e < 4u; ++e)
-                    if (n + e < a.N) y[e].bits = (uint16_t)(v[e >> 1] >> (16u * (e & 1u)));
-            }
-        } else {
-            float *y = reinterpret_cast<float *>(a.y) + at;
-            if (n + 3u < a.N) {
-                *reinterpret_cast<u32x4_a4 *>(y) = __builtin_bit_cast(u32x4v, sum);
-            } else {
+        for (int t = t0; t < t0 + H::kAtOnce && t < H::kTiles; ++t)
+            parts[((t - t0) * waves + wave) * 64u + lane] = acc[t / H::kMT][t % H::kMT];
+        __syncthreads();
+        for (uint32_t t = wave; t < (uint32_t)H::kAtOnce && t + t0 < (uint32_t)H::kTiles; t += waves) {
+            const f32x4v *p = parts + t * waves * 64u + lane;
+            f32x4v sum = p[0];
+            for (uint32_t k = 1; k < waves; ++k) sum += p[k * 64u];
+            // lane l has rows 4 (l / 16) .. + 3 of the tile's 16 of W, row l mod 16 of x
+            const uint32_t n = n0 + (t + t0) / H::kMT * 16u + q * 4u, m = (t + t0) % H::kMT * 16u + r;
+            if (m >= a.M) continue;
 #pragma unroll
-                for (uint32_t e = 0; e < 4u; ++e)
-                    if (n + e < a.N) y[e] = sum[e];
-            }
+            for (int e = 0; e < 4; ++e) sum[e] = sum[e] * scale * a.alpha;
+            store4(a, m, n, sum);
         }
     }
 }
 
-template <Format kFormat, bool kX8, int kMT, int kR>
-void run_matvec(const Matvec &a, uint32_t waves, hipStream_t st)
+template <Format kFormat, bool kX8, int kMQ, int kR, int kP>
+void run_matvec(const Matvec &a, uint32_t most, hipStream_t st)
 {
+    typedef Shape<kX8, kMQ, kR, kP> H;
+    const uint32_t steps = a.steps / kP, limit = most < (uint32_t)H::kWaves ? most : (uint32_t)H::kWaves;
+    const uint32_t waves = steps < limit ? (steps > 0u ? steps : 1u) : limit;
     const unsigned grid = (a.N + 16u * kR - 1u) / (16u * kR);
-    hipLaunchKernelGGL((matvec_kernel<kFormat, kX8, kMT, kR>), dim3(grid), dim3(waves * 64u), waves * kR * kMT * 1024u, st, a);
+    hipLaunchKernelGGL((matvec_kernel<kFormat, kX8, kMQ, kR, kP>), dim3(grid), dim3(waves * 64u), H::lds_bytes(waves), st, a);
+}
+
+// Rows of W to a wave: as many as leave each compute unit a workgroup, up to
+// 64, since x is loaded, and goes through LDS, once for them; with at most
+// four rows of x, which cost little, 16 until there are four times as many
+// workgroups.  Waves: 8 where a unit has one workgroup, 4 where it has more;
+// 16 for few rows of x and long rows of W, whose loads are then all that is
+// under way.  MXFP4 tiled, us: 4096 x 4096 of 1 row, 4 / 8 / 16 waves 6.0 / 5.2
+// / 5.3, 4096 x 14336 - / 9.7 / 8.8, but of 16 rows 16.1 / 13.9 / 15.4; 16 rows
+// of 8192 x 4096, 16 / 32 / 64 rows of W to a wave 9.1 / 8.5 / 9.9, of 14336 x
+// 4096 - / 10.9 / 10.5, 64 of 28672 x 4096 with 4 / 8 waves 15.8 / 18.2; 1 row
+// of 14336 x 4096 8.6 / 8.9 / 9.2, of 65536 x 4096 27.8 / 29.1 / 27.4.
+template <Format kFormat, bool kX8, int kMQ, int kP>
+void pick_rows(const Matvec &a, uint32_t units, hipStream_t st)
+{
+    const uint32_t blocks = (a.N + 15u) / 16u;
+    if (kMQ == 1 ? blocks <= 4u * units : blocks <= units) {
+        const uint32_t waves = blocks > 2u * units ? 4u : blocks <= units && a.steps >= 64u ? 16u : 8u;
+        run_matvec<kFormat, kX8, kMQ, 1, kP>(a, waves, st);
+    } else if (kMQ > 1 && blocks <= 2u * units) {
+        if constexpr (kMQ > 1) run_matvec<kFormat, kX8, kMQ, 2, kP>(a, 8u, st);
+    } else {
+        run_matvec<kFormat, kX8, kMQ, 4, kP>(a, blocks <= 4u * units ? 8u : 4u, st);
+    }
+}
+
+template <Format kFormat, bool kX8, int kMQ>
+void pick_layout(const Matvec &a, bool linear, uint32_t units, hipStream_t st)
+{
+    if constexpr (kFormat != kNvTile) {  // (a lane's 64 columns side by side: four lanes meet two tiles)
+        if (linear && a.steps % 2 == 0) return pick_rows<kFormat, kX8, kMQ, 2>(a, units, st);
+    }
+    pick_rows<kFormat, kX8, kMQ, 1>(a, units, st);
 }
 
 template <Format kFormat, bool kX8>
-void pick_matvec(const Matvec &a, hipStream_t st)
+void pick_matvec(const Matvec &a, bool linear, uint32_t units, hipStream_t st)
 {
-    const uint32_t blocks = (a.N + 15u) / 16u;
-    uint32_t waves = a.steps < 16u ? (a.steps > 0u ? a.steps : 1u) : 16u;
-    if (a.M <= 16) {
-        if (blocks >= 1024u)
-            run_matvec<kFormat, kX8, 1, 2>(a, waves, st);
-        else
-            run_matvec<kFormat, kX8, 1, 1>(a, waves, st);
-    } else if (a.M <= 32) {
-        if (blocks >= 1024u)
-            run_matvec<kFormat, kX8, 2, 2>(a, waves, st);
-        else
-            run_matvec<kFormat, kX8, 2, 1>(a, waves, st);
-    } else {
-        if (waves > 8u) waves = 8u;
-        if (blocks >= 1024u)
-            run_matvec<kFormat, kX8, 4, 2>(a, waves, st);
-        else
-            run_matvec<kFormat, kX8, 4, 1>(a, waves, st);
-    }
+    if (a.M <= 4)
+        pick_layout<kFormat, kX8, 1>(a, linear, units, st);
+    else if (a.M <= 8)
+        pick_layout<kFormat, kX8, 2>(a, linear, units, st);
+    else if (a.M <= 16)
+        pick_layout<kFormat, kX8, 4>(a, linear, units, st);
+    else if (a.M <= 32)
+        pick_layout<kFormat, kX8, 8>(a, linear, units, st);
+    else
+        pick_layout<kFormat, kX8, 16>(a, linear, units, st);
 }
 
 Matvec matvec_of(const MatvecArgs &g)
@@ -308,15 +402,18 @@ Matvec matvec_of(const MatvecArgs &g)
 
 int launch_matvec(const MatvecArgs &g, hipStream_t st)
 {
+    const int cus = device_cu_count();
+    if (cus <= 0) return 1;
     const Matvec a = matvec_of(g);
+    const uint32_t units = (uint32_t)cus;
     if (g.tensor_scale && g.nv_domain == 0)
-        pick_matvec<kNvGlobal, false>(a, st);
+        pick_matvec<kNvGlobal, false>(a, !g.tiled, units, st);
     else if (g.tensor_scale)
-        pick_matvec<kNvTile, false>(a, st);
+        pick_matvec<kNvTile, false>(a, !g.tiled, units, st);
     else if (g.x_scales)
-        pick_matvec<kMx, true>(a, st);
+        pick_matvec<kMx, true>(a, !g.tiled, units, st);
     else
-        pick_matvec<kMx, false>(a, st);
+        pick_matvec<kMx, false>(a, !g.tiled, units, st);
     return hipGetLastError() == hipSuccess ? 0 : 1;
 }
 
