@@ -4,9 +4,10 @@ Everything between the GEMMs is the library's: the norms write the MXFP4
 operand that the next GEMM loads, rotary positions are applied where the QKV
 GEMM left the heads, dropout is drawn again instead of stored, and the MLP's
 hidden activations are recomputed by SwiGLU's gradient. Attention itself is
-written out in torch (binary32). Synthetic data, random weights:
+written out in torch (binary32). With --keep8 what the backward pass reads of
+the activations is kept in 8 bits. Synthetic data, random weights:
 
-    python examples/block_step.py [--steps 8] [--tokens 512] [--width 1024]
+    python examples/block_step.py [--steps 8] [--tokens 512] [--width 1024] [--keep8]
 """
 from __future__ import annotations
 
@@ -61,11 +62,43 @@ def attention(q, k, v, sequence):
     return torch.matmul(torch.softmax(s.masked_fill(hidden, float("-inf")), -1), v).transpose(0, 1)
 
 
+class Rows:
+    """Activations that the backward pass reads again: as they are."""
+
+    def __init__(self, x):
+        self.x = x
+
+    def values(self):
+        return self.x
+
+    def norm_grad(self, dy, w, **args):
+        return B.fp4_norm_grad(dy, self.x, w, kind=B.NORM_RMS, **args)
+
+    def swiglu_grad(self, dh):
+        return B.fp4_swiglu_grad_bf16(dh, self.x, want_h=True)
+
+
+class Rows8:
+    """The same in 8 bits, 33/64 of the bytes."""
+
+    def __init__(self, x, packed=None):
+        self.packed = B.fp4_pack8(x) if packed is None else packed
+
+    def values(self):
+        return B.fp4_unpack8(*self.packed)
+
+    def norm_grad(self, dy, w, **args):
+        return B.fp4_norm_grad_pack8(dy, *self.packed, w, kind=B.NORM_RMS, **args)
+
+    def swiglu_grad(self, dh):
+        return B.fp4_swiglu_grad_pack8(dh, *self.packed, want_h=True)
+
+
 class Block:
-    def __init__(self, width, heads, kv_heads, hidden, p, positions, sequence, seed=0, dim=128):
+    def __init__(self, width, heads, kv_heads, hidden, p, positions, sequence, seed=0, dim=128, keep8=False):
         g = torch.Generator().manual_seed(seed)
         self.heads, self.kv, self.dim, self.hidden, self.p = heads, kv_heads, dim, hidden, p
-        self.positions, self.sequence = positions, sequence
+        self.positions, self.sequence, self.keep = positions, sequence, Rows8 if keep8 else Rows
         dev = positions.device
 
         def weight(n, k):
@@ -82,58 +115,68 @@ class Block:
         n = self.heads + self.kv
         return qkv[:, :n * self.dim].unflatten(1, (n, self.dim))
 
+    def norm(self, x, w, **args):
+        """The norm's outputs, and its result as the backward pass reads it."""
+        args = dict(args, kind=B.NORM_RMS, save=True, mx=True, layout=TILED)
+        if self.keep is Rows8:
+            n = B.fp4_norm_pack8(x, w, **args)
+            return n, Rows8(None, (n.codes8, n.scales8))
+        n = B.fp4_norm(x, w, **args)
+        return n, Rows(n.y)
+
     def forward(self, x, seed):
         w = {k: v.bfloat16() for k, v in self.params.items()}
-        m, s = x.shape[0], {"x": x, "seed": seed, "w": w}
-        s["n1"] = B.fp4_norm(x, w["norm1"], kind=B.NORM_RMS, save=True, mx=True, layout=TILED)
-        qkv = linear((s["n1"].codes, s["n1"].scales), w["qkv"], m)
+        m, s = x.shape[0], {"x": self.keep(x), "seed": seed, "w": w}
+        n1, s["y1"] = self.norm(x, w["norm1"])
+        qkv = linear((n1.codes, n1.scales), w["qkv"], m)
         t = self.turned(qkv)
         B.fp4_rotary(t, self.positions, self.freq, scale=self.scale, y=t)
         heads = qkv.float().unflatten(1, (-1, self.dim)).split([self.heads, self.kv, self.kv], 1)
         s["qkv"] = [h.detach().requires_grad_() for h in heads]
         with torch.enable_grad():
             s["attention"] = attention(*s["qkv"], self.sequence)
-        s["o"] = s["attention"].detach().flatten(1).bfloat16()
-        a = linear(B.fp4_quantize_mx(s["o"], layout=TILED), w["o"], m)
-        s["n2"] = B.fp4_norm(a, w["norm2"], kind=B.NORM_RMS, residual=x, p=self.p, seed=seed, stream_id=0, save=True,
-                             mx=True, layout=TILED)
-        s["c"] = linear((s["n2"].codes, s["n2"].scales), w["gate_up"], m)
-        h = B.fp4_swiglu_bf16(s["c"], self.hidden)
+        o = s["attention"].detach().flatten(1).bfloat16()
+        a = linear(B.fp4_quantize_mx(o, layout=TILED), w["o"], m)
+        n2, s["y2"] = self.norm(a, w["norm2"], residual=x, p=self.p, seed=seed, stream_id=0)
+        c = linear((n2.codes, n2.scales), w["gate_up"], m)
+        h = B.fp4_swiglu_bf16(c, self.hidden)
         d = linear(B.fp4_quantize_mx(h, layout=TILED), w["down"], m)
-        return B.fp4_dropout(d, self.p, seed=seed, stream_id=1, residual=s["n2"].h), s
+        s.update(o=self.keep(o), h2=self.keep(n2.h), c=self.keep(c), rstd1=n1.rstd, rstd2=n2.rstd)
+        return B.fp4_dropout(d, self.p, seed=seed, stream_id=1, residual=n2.h), s
 
     def backward(self, dy, s):
         """(gradient of x, gradients of the parameters)."""
         w, seed, grad = s["w"], s["seed"], {}
         down = LinearGrad(B.fp4_dropout(dy, self.p, seed=seed, stream_id=1), seed + 1)
-        dc, h = B.fp4_swiglu_grad_bf16(down.x(w["down"]), s["c"], want_h=True)
+        dc, h = s["c"].swiglu_grad(down.x(w["down"]))
         grad["down"] = down.w(h)
         up = LinearGrad(dc, seed + 2)
-        grad["gate_up"] = up.w(s["n2"].y)
-        g = B.fp4_norm_grad(up.x(w["gate_up"]), s["n2"].h, w["norm2"], kind=B.NORM_RMS, rstd=s["n2"].rstd, dres=dy,
-                            p=self.p, seed=seed, stream_id=0)
+        grad["gate_up"] = up.w(s["y2"].values())
+        g = s["h2"].norm_grad(up.x(w["gate_up"]), w["norm2"], rstd=s["rstd2"], dres=dy, p=self.p, seed=seed, stream_id=0)
         grad["norm2"] = g.dgamma
         o = LinearGrad(g.dx if self.p > 0 else g.dh, seed + 3)
-        grad["o"] = o.w(s["o"])
+        grad["o"] = o.w(s["o"].values())
         s["attention"].backward(o.x(w["o"]).float().unflatten(1, (self.heads, self.dim)))
         dqkv = torch.cat([t.grad for t in s["qkv"]], 1).flatten(1).bfloat16()
         t = self.turned(dqkv)
         B.fp4_rotary(t, self.positions, self.freq, scale=self.scale, inverse=True, y=t)
         qkv = LinearGrad(dqkv, seed + 4)
-        grad["qkv"] = qkv.w(s["n1"].y)
-        g = B.fp4_norm_grad(qkv.x(w["qkv"]), s["x"], w["norm1"], kind=B.NORM_RMS, rstd=s["n1"].rstd, dres=g.dh)
+        grad["qkv"] = qkv.w(s["y1"].values())
+        g = s["x"].norm_grad(qkv.x(w["qkv"]), w["norm1"], rstd=s["rstd1"], dres=g.dh)
         grad["norm1"] = g.dgamma
         return g.dh, grad
 
 
-def train(steps=8, tokens=512, width=1024, hidden=2816, heads=8, kv_heads=2, p=0.1, lr=0.5, seed=0, device="cuda"):
+def train(steps=8, tokens=512, width=1024, hidden=2816, heads=8, kv_heads=2, p=0.1, lr=0.5, seed=0, device="cuda",
+          keep8=False):
     """Losses of `steps` steps that fit a fixed random target."""
     g = torch.Generator().manual_seed(seed)
     x = torch.randn((tokens, width), generator=g).bfloat16().to(device)
     target = torch.randn((tokens, width), generator=g).to(device)
     at = torch.arange(tokens, device=device)
     cut = tokens * 5 // 8  # two packed sequences
-    block = Block(width, heads, kv_heads, hidden, p, torch.where(at < cut, at, at - cut), (at >= cut).long(), seed)
+    block = Block(width, heads, kv_heads, hidden, p, torch.where(at < cut, at, at - cut), (at >= cut).long(), seed,
+                  keep8=keep8)
     losses = []
     for i in range(steps):
         y, saved = block.forward(x, 1000 * (seed + 1) + 10 * i)
@@ -150,8 +193,9 @@ def main():
     ap.add_argument("--steps", type=int, default=8)
     ap.add_argument("--tokens", type=int, default=512)
     ap.add_argument("--width", type=int, default=1024)
+    ap.add_argument("--keep8", action="store_true")
     a = ap.parse_args()
-    for i, v in enumerate(train(a.steps, a.tokens, a.width)):
+    for i, v in enumerate(train(a.steps, a.tokens, a.width, keep8=a.keep8)):
         print(f"step {i}: loss {v:.4f}")
 
 

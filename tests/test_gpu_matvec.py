@@ -131,6 +131,27 @@ def test_weights_are_exact():
     assert np.array_equal(got.cpu().double().numpy()[0], want)
 
 
+def test_8_bit_rows_of_all_scales():
+    """Rows of blocks from the smallest to the largest scale: as their bf16 values, subnormal ones among them."""
+    dev = device()
+    announce("matvec of 8-bit rows of all scales")
+    k = 128 * 62
+    x8 = torch.randint(0, 127, (3, k), generator=torch.Generator().manual_seed(1), dtype=torch.uint8)
+    s8 = (torch.arange(3 * k // 32) % 247).to(torch.uint8).reshape(3, k // 32)
+    x8, s8 = x8.to(dev), s8.to(dev)
+    codes = torch.zeros((k // 128, k // 2), dtype=torch.uint8)
+    for i in range(k // 128):
+        codes[i, 64 * i + 5] = 0x02  # a one at column 128 i + 10
+        codes[i, 64 * i + 40] = 0x20  # and at 128 i + 81
+    scales = torch.full((k // 128, k // 32), 127, dtype=torch.uint8)
+    y = B.fp4_matvec_mx_pack8(x8, s8, codes.to(dev), scales.to(dev))
+    v = B.fp4_unpack8(x8, s8).float().view(3, -1, 128)
+    want = v[:, :, 10] + v[:, :, 81]
+    assert torch.equal(y, want)
+    read = v[:, :, [10, 81]]
+    assert float(read[read > 0].min()) < 2.0 ** -126 and float(read.max()) > 2.0 ** 120
+
+
 @pytest.mark.parametrize("fmt", FORMATS)
 def test_nan_and_inf_stay_in_their_row(fmt):
     dev = device()

@@ -86,6 +86,8 @@ def test_every_bf16_value():
     wide = B.fp4_pack8(x.float().to(dev))
     assert torch.equal(wide[0], got[0]) and torch.equal(wide[1], got[1])
     same(B.fp4_unpack8(*got, out_dtype=F32), torch.from_numpy(P.values(codes, scales)).float(), "values")
+    # (values in binary32 are exact; bf16 rounds below 2^-120 only)
+    same(B.fp4_unpack8(*got), torch.from_numpy(P.values(codes, scales)).float().to(BF), "bf16 values")
     back = B.fp4_unpack8(*got).float().cpu()
     finite = x.isfinite()
     assert bool(back[finite].isfinite().all()) and bool(back[~finite].isnan().all())
