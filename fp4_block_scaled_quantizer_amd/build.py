@@ -25,8 +25,9 @@ ROOT = os.path.dirname(HERE)
 OUT = os.path.join(HERE, "libfp4q.so")
 BUILD_DIR = os.path.join(ROOT, "_build")
 
-SOURCES = ["quant.hip", "gemm_mx.hip", "gemm_nv.hip", "swiglu.hip", "swiglu_grad.hip", "dropout.hip", "norm_grad.hip",
-           "norm_grad_pack8.hip", "norm.hip", "rotary.hip", "pack8.hip", "matvec.hip", "fp4q_api.hip"]
+SOURCES = ["matvec_mx.hip", "matvec_nv.hip", "norm_grad.hip", "norm_grad_pack8.hip", "norm.hip", "quant.hip",
+           "gemm_mx.hip", "gemm_nv.hip", "swiglu.hip", "swiglu_grad.hip", "dropout.hip", "rotary.hip", "pack8.hip",
+           "fp4q_api.hip"]
 
 HIPCC_FLAGS = [
     "--offload-arch=gfx950",

@@ -650,7 +650,7 @@ fp4q_status run_matvec(const void *x, const void *x_scales, bool packed, int64_t
     a.y = y;
     a.y_bf16 = y_type == FP4Q_OUT_BF16;
     (void)hipGetLastError();
-    return launched(fp4q::launch_matvec(a, as_stream(stream)));
+    return launched(a.tensor_scale ? fp4q::launch_matvec_nv(a, as_stream(stream)) : fp4q::launch_matvec_mx(a, as_stream(stream)));
 }
 
 // fp4_pack8, or with `unpack` fp4_unpack8.

@@ -1,4 +1,4 @@
-// matvec.hip -- products of few rows with FP4 weights, y = alpha x W^T: the
+// matvec.h -- products of few rows with FP4 weights, y = alpha x W^T: the
 // linear layers of a decoding step, x a token's activations (or a few tokens')
 // in bf16 or as 8-bit rows, W an MXFP4 or NVFP4 operand as the GEMMs take it.
 //
@@ -14,6 +14,8 @@
 // order of the columns inside an MFMA's sum does not matter as long as both
 // operands have the same, so neither is rearranged.  The waves of a workgroup
 // split the columns and join their sums through LDS in a fixed order.
+#pragma once
+
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -124,10 +126,10 @@ struct Step {
 template <bool kX8, int kMQ, int kR, int kP>
 struct Shape {
     static constexpr int kMT = (kMQ + 3) / 4, kTiles = kR * kMT;  // 16 x 16 results
-    static constexpr int kRows = kX8 && kMQ * kP == 1 ? 8 : kMQ * 4;
+    static constexpr int kRows = kMQ * 4;
     static constexpr uint32_t kPitch = 256 * kP + 16;  // 16 rows' pieces lie in all banks alike
-    static constexpr int kAhead = kR == 1 && kMQ <= 4 && kP == 1 ? 2 : 1;
-    static constexpr int kWaves = kR == 1 && kMQ <= 2 && kP == 1 ? 16 : kRows * kPitch * 8 <= 160 * 1024 ? 8 : 4;
+    static constexpr int kAhead = kMQ == 1 && kP == 1 ? 2 : 1;
+    static constexpr int kWaves = kR == 1 && kMQ <= 4 && kP == 1 ? 16 : kRows * kPitch * 8 <= 160 * 1024 ? 8 : 4;
     static constexpr int kAtOnce = kTiles < 64 / kWaves ? kTiles : 64 / kWaves;  // tiles joined at once, in 64 KiB at most
     static uint32_t lds_bytes(uint32_t waves)
     {
@@ -150,7 +152,7 @@ __global__ __launch_bounds__((Shape<kX8, kMQ, kR, kP>::kWaves * 64)) void matvec
     const uint32_t n0 = blockIdx.x * (16u * kR), steps = a.steps / kP;
     const uint32_t from = steps * wave / waves, to = steps * (wave + 1u) / waves;
 
-    const uint8_t *codes[kR], *scales[kR], *x[S::kLoads], *x_scales[kX8 ? S::kLoads : 1];
+    const uint8_t *codes[kR], *scales[kR];
     const float *tile[kFormat == kNvTile ? kR : 1];
 #pragma unroll
     for (int j = 0; j < kR; ++j) {  // past W's end: its last row again, not stored
@@ -162,18 +164,29 @@ __global__ __launch_bounds__((Shape<kX8, kMQ, kR, kP>::kWaves * 64)) void matvec
         // 16 rows are within one 128 x 128 tile
         if (kFormat == kNvTile) tile[j] = a.tensor_scale + (int64_t)(min(n0 + 16u * j, a.N - 1u) >> 7) * a.steps;
     }
-    constexpr uint32_t kPer = (kX8 ? 8 : 16) * kP;  // lanes of a row of x
-#pragma unroll
-    for (int i = 0; i < S::kLoads; ++i) {  // past x's end: its last row again, in columns of the result not stored
-        const uint32_t at = i * 64u + lane, m = min(at / kPer, a.M - 1u);
-        x[i] = a.x + (int64_t)m * a.ld_x * (kX8 ? 1 : 2) + at % kPer * 16u;
-        if (kX8) x_scales[i] = a.x_scales + (int64_t)m * (a.steps * 4u) + at % kPer / 2u;
-    }
+    // A load of x takes 64 / kPer rows, the last ones of M where it would go
+    // past them (the rows before M are then there twice, the same; those of
+    // LDS from M on hold anything, for columns of the result not stored): the
+    // rows' place is the same for the wave, a lane's own part of the address
+    // the same for all loads.
+    constexpr uint32_t kPer = (kX8 ? 8 : 16) * kP, kOnce = 64u / kPer;
+    const uint32_t row = min(lane / kPer, a.M - 1u), piece = lane % kPer;
+    const uint32_t last = a.M > kOnce ? a.M - kOnce : 0u;
+    // made anew in each step: kept over the loop, the loads' addresses spill
+    const auto fresh = [](uint32_t v) {
+        v = (uint32_t)__builtin_amdgcn_readfirstlane((int)v);
+        asm volatile("" : "+s"(v));
+        return v;
+    };
+    const int64_t x_row = a.ld_x * (kX8 ? 1 : 2), x_scale_row = a.steps * 4u;
+    const uint8_t *x = a.x + row * x_row + piece * 16u, *x_scales = kX8 ? a.x_scales + row * x_scale_row + piece / 2u : nullptr;
     const auto fetch = [&](uint32_t step, S &s) {
+        const uint32_t end = fresh(last);
 #pragma unroll
         for (int i = 0; i < S::kLoads; ++i) {
-            s.x[i] = *reinterpret_cast<const u32x4v *>(x[i] + step * ((kX8 ? 128u : 256u) * kP));
-            if (kX8) s.x_scale[i] = x_scales[i][step * (4u * kP)];
+            const uint32_t m = min(i * kOnce, end);
+            s.x[i] = *reinterpret_cast<const u32x4v *>(x + (m * x_row + step * ((kX8 ? 128u : 256u) * kP)));
+            if (kX8) s.x_scale[i] = x_scales[m * x_scale_row + step * (4u * kP)];
         }
 #pragma unroll
         for (int j = 0; j < kR; ++j) {
@@ -202,13 +215,14 @@ __global__ __launch_bounds__((Shape<kX8, kMQ, kR, kP>::kWaves * 64)) void matvec
     // are done in their order, so no wait but the fences that keep the
     // compiler to it.
     uint8_t *own = lds + wave * (H::kRows * H::kPitch);
+    uint8_t *to0 = own + row * H::kPitch + piece * (kX8 ? 32u : 16u);
     const uint8_t *mine = own + (kMQ < 4 ? r % (kMQ * 4u) : r) * H::kPitch + q * (64u * kP);
     const auto multiply = [&](const S &s) {
         __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+        const uint32_t end = fresh(last);
 #pragma unroll
         for (int i = 0; i < S::kLoads; ++i) {
-            const uint32_t at = i * 64u + lane;
-            uint8_t *to = own + at / kPer * H::kPitch + at % kPer * (kX8 ? 32u : 16u);
+            uint8_t *to = to0 + min(i * kOnce, end) * H::kPitch;
             if constexpr (kX8) {
                 const float scale = mx_scale_f32(s.x_scale[i]);
                 *reinterpret_cast<bf16x8v *>(to) = rows8(s.x[i][0], s.x[i][1], scale);
@@ -259,14 +273,15 @@ __global__ __launch_bounds__((Shape<kX8, kMQ, kR, kP>::kWaves * 64)) void matvec
     if (from < to) {
         S s[H::kAhead];
 #pragma unroll
-        for (int d = 0; d < H::kAhead; ++d) fetch(min(from + d, to - 1u), s[d]);
-        for (uint32_t step = from; step < to; step += H::kAhead) {  // past the wave's last step: it again, not used
+        for (int d = 0; d < H::kAhead; ++d)
+            if (d == 0 || from + d < to) fetch(from + d, s[d]);
+        for (uint32_t step = from; step < to; step += H::kAhead) {
 #pragma unroll
             for (int d = 0; d < H::kAhead; ++d) {
                 if (d > 0 && step + d >= to) break;
                 multiply(s[d]);
                 __builtin_amdgcn_sched_barrier(0);
-                fetch(min(step + H::kAhead + d, to - 1u), s[d]);
+                if (step + d + H::kAhead < to) fetch(step + d + H::kAhead, s[d]);
                 __builtin_amdgcn_sched_barrier(0);
             }
         }
@@ -305,27 +320,41 @@ void run_matvec(const Matvec &a, uint32_t most, hipStream_t st)
     hipLaunchKernelGGL((matvec_kernel<kFormat, kX8, kMQ, kR, kP>), dim3(grid), dim3(waves * 64u), H::lds_bytes(waves), st, a);
 }
 
-// Rows of W to a wave: as many as leave each compute unit a workgroup, up to
-// 64, since x is loaded, and goes through LDS, once for them; with at most
-// four rows of x, which cost little, 16 until there are four times as many
-// workgroups.  Waves: 8 where a unit has one workgroup, 4 where it has more;
-// 16 for few rows of x and long rows of W, whose loads are then all that is
-// under way.  MXFP4 tiled, us: 4096 x 4096 of 1 row, 4 / 8 / 16 waves 6.0 / 5.2
-// / 5.3, 4096 x 14336 - / 9.7 / 8.8, but of 16 rows 16.1 / 13.9 / 15.4; 16 rows
-// of 8192 x 4096, 16 / 32 / 64 rows of W to a wave 9.1 / 8.5 / 9.9, of 14336 x
-// 4096 - / 10.9 / 10.5, 64 of 28672 x 4096 with 4 / 8 waves 15.8 / 18.2; 1 row
-// of 14336 x 4096 8.6 / 8.9 / 9.2, of 65536 x 4096 27.8 / 29.1 / 27.4.
-template <Format kFormat, bool kX8, int kMQ, int kP>
-void pick_rows(const Matvec &a, uint32_t units, hipStream_t st)
+template <Format kFormat, bool kX8, int kMQ, int kP, int kR>
+void pick_rows(const Matvec &a, uint32_t r, uint32_t most, hipStream_t st)
 {
-    const uint32_t blocks = (a.N + 15u) / 16u;
-    if (kMQ == 1 ? blocks <= 4u * units : blocks <= units) {
-        const uint32_t waves = blocks > 2u * units ? 4u : blocks <= units && a.steps >= 64u ? 16u : 8u;
-        run_matvec<kFormat, kX8, kMQ, 1, kP>(a, waves, st);
-    } else if (kMQ > 1 && blocks <= 2u * units) {
-        if constexpr (kMQ > 1) run_matvec<kFormat, kX8, kMQ, 2, kP>(a, 8u, st);
+    if constexpr (kR > 1) {
+        if (r < (uint32_t)kR) return pick_rows<kFormat, kX8, kMQ, kP, kR - 1>(a, r, most, st);
+    }
+    run_matvec<kFormat, kX8, kMQ, kR, kP>(a, most, st);
+}
+
+// Rows of W to a wave: x is loaded, and goes through LDS, once for them, so a
+// compute unit gets one workgroup of as many rows as it has to do, or where
+// those are more than registers hold as few workgroups of the same rows.
+// Waves: 16 where a unit has 16 rows, whose loads are then all that is under
+// way (8 with kP = 2, whose loads are twice as many: five rows, 4096 x 14336
+// NVFP4 12.8, with 16 13.8), else 8 where it has one workgroup, 4 where more.  us on MXFP4 tiled
+// weights from memory (at a lower clock than the figures above), 16 rows of W
+// to a wave / 32 / 48 / 64 / 80 / 112: 16 rows of x, 4096 x 4096 10.7 / 11.3,
+// 8192 x 4096 14 / 12.7 / 13.1 / 14.4, 11008 x 4096 - / 16.6 / 13.7 / 14.9 /
+// 16.3, 28672 x 4096 56 / - / 28.8 / 24.8 / 26.8 / 23.2, 40000 x 4096 (80 each
+// for two workgroups) - / - / - / 35.0 / 30.0 / 34.5.  At most four rows of x
+// cost little: 16 rows of W each are as good at any size (28672 x 4096 21.1 / -
+// / - / 21.9 / - / 21.8).  8 / 16 waves, 4096 x 14336: one row 16.5 / 13.4,
+// eight 18.1 / 16.5, sixteen 22.9 / 22.8, 4096 x 4096 of sixteen 10.7 / 10.4.
+// The waves, and so the order of the sums, do not depend on x's rows up to 16.
+template <Format kFormat, bool kX8, int kMQ, int kP>
+void pick_waves(const Matvec &a, uint32_t units, hipStream_t st)
+{
+    constexpr uint32_t kMost = kMQ == 16 ? (kFormat == kNvTile ? 2 : 4) : kMQ == 8 && (kP == 2 || kFormat == kNvTile) ? 5 : 7;
+    const uint32_t blocks = (a.N + 15u) / 16u, each = (blocks + units - 1u) / units;
+    const uint32_t waves = each == 1u && kP == 1 ? 16u : each <= 7u ? 8u : 4u;
+    if constexpr (kMQ == 1) {
+        run_matvec<kFormat, kX8, 1, 1, kP>(a, waves, st);
     } else {
-        run_matvec<kFormat, kX8, kMQ, 4, kP>(a, blocks <= 4u * units ? 8u : 4u, st);
+        const uint32_t groups = (each + kMost - 1u) / kMost;
+        pick_rows<kFormat, kX8, kMQ, kP, kMost>(a, (each + groups - 1u) / groups, groups > 1u ? 4u : waves, st);
     }
 }
 
@@ -333,9 +362,9 @@ template <Format kFormat, bool kX8, int kMQ>
 void pick_layout(const Matvec &a, bool linear, uint32_t units, hipStream_t st)
 {
     if constexpr (kFormat != kNvTile) {  // (a lane's 64 columns side by side: four lanes meet two tiles)
-        if (linear && a.steps % 2 == 0) return pick_rows<kFormat, kX8, kMQ, 2>(a, units, st);
+        if (linear && a.steps % 2 == 0) return pick_waves<kFormat, kX8, kMQ, 2>(a, units, st);
     }
-    pick_rows<kFormat, kX8, kMQ, 1>(a, units, st);
+    pick_waves<kFormat, kX8, kMQ, 1>(a, units, st);
 }
 
 template <Format kFormat, bool kX8>
@@ -399,22 +428,5 @@ Matvec matvec_of(const MatvecArgs &g)
 }
 
 }  // namespace
-
-int launch_matvec(const MatvecArgs &g, hipStream_t st)
-{
-    const int cus = device_cu_count();
-    if (cus <= 0) return 1;
-    const Matvec a = matvec_of(g);
-    const uint32_t units = (uint32_t)cus;
-    if (g.tensor_scale && g.nv_domain == 0)
-        pick_matvec<kNvGlobal, false>(a, !g.tiled, units, st);
-    else if (g.tensor_scale)
-        pick_matvec<kNvTile, false>(a, !g.tiled, units, st);
-    else if (g.x_scales)
-        pick_matvec<kMx, true>(a, !g.tiled, units, st);
-    else
-        pick_matvec<kMx, false>(a, !g.tiled, units, st);
-    return hipGetLastError() == hipSuccess ? 0 : 1;
-}
 
 }  // namespace fp4q

@@ -1,0 +1,18 @@
+// matvec_nv.hip -- products of few rows with NVFP4 weights (matvec.h).
+#include "matvec.h"
+
+namespace fp4q {
+
+int launch_matvec_nv(const MatvecArgs &g, hipStream_t st)
+{
+    const int units = device_cu_count();
+    if (units <= 0) return 1;
+    const Matvec a = matvec_of(g);
+    if (g.nv_domain == 0)
+        pick_matvec<kNvGlobal, false>(a, !g.tiled, (uint32_t)units, st);
+    else
+        pick_matvec<kNvTile, false>(a, !g.tiled, (uint32_t)units, st);
+    return hipGetLastError() == hipSuccess ? 0 : 1;
+}
+
+}  // namespace fp4q
