@@ -172,10 +172,13 @@ __global__ __launch_bounds__((Shape<kX8, kMQ, kR, kP>::kWaves * 64)) void matvec
     constexpr uint32_t kPer = (kX8 ? 8 : 16) * kP, kOnce = 64u / kPer;
     const uint32_t row = min(lane / kPer, a.M - 1u), piece = lane % kPer;
     const uint32_t last = a.M > kOnce ? a.M - kOnce : 0u;
-    // made anew in each step: kept over the loop, the loads' addresses spill
+    // made anew in each step where the loads are many: kept over the loop, their
+    // addresses spill
     const auto fresh = [](uint32_t v) {
-        v = (uint32_t)__builtin_amdgcn_readfirstlane((int)v);
-        asm volatile("" : "+s"(v));
+        if constexpr (kMQ >= 4) {
+            v = (uint32_t)__builtin_amdgcn_readfirstlane((int)v);
+            asm volatile("" : "+s"(v));
+        }
         return v;
     };
     const int64_t x_row = a.ld_x * (kX8 ? 1 : 2), x_scale_row = a.steps * 4u;
