@@ -128,7 +128,7 @@ struct Shape {
     static constexpr int kMT = (kMQ + 3) / 4, kTiles = kR * kMT;  // 16 x 16 results
     static constexpr int kRows = kMQ * 4;
     static constexpr uint32_t kPitch = 256 * kP + 16;  // 16 rows' pieces lie in all banks alike
-    static constexpr int kAhead = kMQ == 1 && kP == 1 ? 2 : 1;
+    static constexpr int kAhead = kMQ <= 4 || (kMQ == 8 && kR * kP <= 4) ? 2 : 1;
     static constexpr int kWaves = kR == 1 && kMQ <= 4 && kP == 1 ? 16 : kRows * kPitch * 8 <= 160 * 1024 ? 8 : 4;
     static constexpr int kAtOnce = kTiles < 64 / kWaves ? kTiles : 64 / kWaves;  // tiles joined at once, in 64 KiB at most
     static uint32_t lds_bytes(uint32_t waves)
@@ -152,14 +152,16 @@ __global__ __launch_bounds__((Shape<kX8, kMQ, kR, kP>::kWaves * 64)) void matvec
     const uint32_t n0 = blockIdx.x * (16u * kR), steps = a.steps / kP;
     const uint32_t from = steps * wave / waves, to = steps * (wave + 1u) / waves;
 
-    const uint8_t *codes[kR], *scales[kR];
+    // bytes from the step's start, below 2^32 as all of W is: the start is the
+    // wave's, in scalar registers
+    uint32_t codes[kR], scales[kR];
     const float *tile[kFormat == kNvTile ? kR : 1];
 #pragma unroll
     for (int j = 0; j < kR; ++j) {  // past W's end: its last row again, not stored
         const uint32_t n = min(n0 + 16u * j + r, a.N - 1u);
-        codes[j] = a.w.codes + (int64_t)(n >> 5) * a.w.code_group + (int64_t)(n & 31u) * a.w.code_row +
+        codes[j] = (uint32_t)((int64_t)(n >> 5) * a.w.code_group + (int64_t)(n & 31u) * a.w.code_row) +
                    (kP == 2 ? q * 32u : (q >> 1) * a.w.code_pair + (q & 1u) * a.w.code_q);
-        scales[j] = a.w.scales + (int64_t)(n >> 5) * a.w.scale_group + (int64_t)(n & 31u) * a.w.scale_row +
+        scales[j] = (uint32_t)((int64_t)(n >> 5) * a.w.scale_group + (int64_t)(n & 31u) * a.w.scale_row) +
                     q * a.w.scale_q * kP;
         // 16 rows are within one 128 x 128 tile
         if (kFormat == kNvTile) tile[j] = a.tensor_scale + (int64_t)(min(n0 + 16u * j, a.N - 1u) >> 7) * a.steps;
@@ -175,7 +177,7 @@ __global__ __launch_bounds__((Shape<kX8, kMQ, kR, kP>::kWaves * 64)) void matvec
     // made anew in each step where the loads are many: kept over the loop, their
     // addresses spill
     const auto fresh = [](uint32_t v) {
-        if constexpr (kMQ >= 4) {
+        if constexpr (kMQ >= 2) {
             v = (uint32_t)__builtin_amdgcn_readfirstlane((int)v);
             asm volatile("" : "+s"(v));
         }
@@ -184,6 +186,7 @@ __global__ __launch_bounds__((Shape<kX8, kMQ, kR, kP>::kWaves * 64)) void matvec
     const int64_t x_row = a.ld_x * (kX8 ? 1 : 2), x_scale_row = a.steps * 4u;
     const uint8_t *x = a.x + row * x_row + piece * 16u, *x_scales = kX8 ? a.x_scales + row * x_scale_row + piece / 2u : nullptr;
     const auto fetch = [&](uint32_t step, S &s) {
+        const uint8_t *step_codes = a.w.codes + step * kP * a.w.code_step, *step_scales = a.w.scales + step * kP * a.w.scale_step;
         const uint32_t end = fresh(last);
 #pragma unroll
         for (int i = 0; i < S::kLoads; ++i) {
@@ -193,10 +196,10 @@ __global__ __launch_bounds__((Shape<kX8, kMQ, kR, kP>::kWaves * 64)) void matvec
         }
 #pragma unroll
         for (int j = 0; j < kR; ++j) {
-            const u32x4v *p = reinterpret_cast<const u32x4v *>(codes[j] + step * kP * a.w.code_step);
+            const u32x4v *p = reinterpret_cast<const u32x4v *>(step_codes + codes[j]);
 #pragma unroll
             for (int k = 0; k < kP; ++k) s.codes[j][k] = load_vec<kP == 1>(p + k);
-            const uint8_t *b = scales[j] + step * kP * a.w.scale_step;
+            const uint8_t *b = step_scales + scales[j];
             constexpr int kBytes = (kFormat == kMx ? 1 : 2) * kP;
             if constexpr (kBytes == 1)
                 s.scales[j] = *b;
@@ -273,20 +276,38 @@ __global__ __launch_bounds__((Shape<kX8, kMQ, kR, kP>::kWaves * 64)) void matvec
             }
         }
     };
-    if (from < to) {
-        S s[H::kAhead];
+    // kA steps in flight.  The main loop's loads are under no condition: under
+    // one, the wait for a step could not tell how many loads came after it, and
+    // waited for all of them.
+    constexpr uint32_t kA = H::kAhead;
+    S s[kA];
+    uint32_t step = from;
+    if (to - from >= kA) {
 #pragma unroll
-        for (int d = 0; d < H::kAhead; ++d)
-            if (d == 0 || from + d < to) fetch(from + d, s[d]);
-        for (uint32_t step = from; step < to; step += H::kAhead) {
+        for (uint32_t d = 0; d < kA; ++d) fetch(from + d, s[d]);
+        for (; step + 2u * kA <= to; step += kA) {
 #pragma unroll
-            for (int d = 0; d < H::kAhead; ++d) {
-                if (d > 0 && step + d >= to) break;
+            for (uint32_t d = 0; d < kA; ++d) {
                 multiply(s[d]);
                 __builtin_amdgcn_sched_barrier(0);
-                if (step + d + H::kAhead < to) fetch(step + d + H::kAhead, s[d]);
+                fetch(step + kA + d, s[d]);
                 __builtin_amdgcn_sched_barrier(0);
             }
+        }
+#pragma unroll
+        for (uint32_t d = 0; d < kA; ++d) {  // fewer than kA steps are not loaded yet
+            multiply(s[d]);
+            __builtin_amdgcn_sched_barrier(0);
+            if (step + kA + d < to) fetch(step + kA + d, s[d]);
+            __builtin_amdgcn_sched_barrier(0);
+        }
+#pragma unroll
+        for (uint32_t d = 0; d + 1u < kA; ++d)
+            if (step + kA + d < to) multiply(s[d]);
+    } else {
+        for (; step < to; ++step) {
+            fetch(step, s[0]);
+            multiply(s[0]);
         }
     }
     __syncthreads();  // the sums take x's place
@@ -334,30 +355,36 @@ void pick_rows(const Matvec &a, uint32_t r, uint32_t most, hipStream_t st)
 
 // Rows of W to a wave: x is loaded, and goes through LDS, once for them, so a
 // compute unit gets one workgroup of as many rows as it has to do, or where
-// those are more than registers hold as few workgroups of the same rows.
-// Waves: 16 where a unit has 16 rows, whose loads are then all that is under
-// way (8 with kP = 2, whose loads are twice as many: five rows, 4096 x 14336
-// NVFP4 12.8, with 16 13.8), else 8 where it has one workgroup, 4 where more.  us on MXFP4 tiled
-// weights from memory (at a lower clock than the figures above), 16 rows of W
-// to a wave / 32 / 48 / 64 / 80 / 112: 16 rows of x, 4096 x 4096 10.7 / 11.3,
-// 8192 x 4096 14 / 12.7 / 13.1 / 14.4, 11008 x 4096 - / 16.6 / 13.7 / 14.9 /
-// 16.3, 28672 x 4096 56 / - / 28.8 / 24.8 / 26.8 / 23.2, 40000 x 4096 (80 each
-// for two workgroups) - / - / - / 35.0 / 30.0 / 34.5.  At most four rows of x
-// cost little: 16 rows of W each are as good at any size (28672 x 4096 21.1 / -
-// / - / 21.9 / - / 21.8).  8 / 16 waves, 4096 x 14336: one row 16.5 / 13.4,
-// eight 18.1 / 16.5, sixteen 22.9 / 22.8, 4096 x 4096 of sixteen 10.7 / 10.4.
-// The waves, and so the order of the sums, do not depend on x's rows up to 16.
+// those are more than registers hold as few workgroups of the same rows.  With
+// at most four rows of x, which cost little, 16 rows of W each are as good at
+// any size.  Waves: four, of two steps in flight each; eight where a unit has
+// only 16 rows of W, or (with more than 16 rows of x) registers for one step in
+// flight; 16 with at most 16 rows of x on few but long rows of W, whose loads
+// are all that is under way.  The waves, and so the order of the sums, do not
+// depend on x's rows up to 16.
+//   Measured in us on MXFP4 tiled weights from memory, K = 4096 (at a lower
+// clock than the figures above).  16 rows of x, 16 rows of W to a wave / 32 /
+// 48 / 64 / 80 / 112: 8192 rows of W 14 / 11.6 / 12.5, 11008 - / 16.6 / 13.2 /
+// 14.1 / 16.3, 28672 - / - / 28.8 / 24.6 / 26.8 / 23.1, 40000 (80 each for two
+// workgroups) - / - / - / 33.7 / 29.9 / 34.8.  One row of x, 16 / 32: 11008 11.1 /
+// 12.1, 28672 20.7 / 21.6, 60000 38.2 / 38.3.  Four waves of two steps / eight
+// of two / eight of one, 16 rows of x: 8192 11.6 / 12.0 / 12.5, 14336 14.7 / 15.6
+// / 15.8, 28672 23.1 / 24.3 / 23.3; 32 rows of x: 14336 18.5 / 19.3 / 19.4, but
+// 28672 30.1 / 33.3 / 27.7; 4096 rows of W: 9.8 / 9.5 / 10.5, and with K = 14336
+// 23.3 / 21.5 / 23.3 and sixteen of two 21.7; one row of x there 19.4 / 14.1 / -
+// / 13.3.
 template <Format kFormat, bool kX8, int kMQ, int kP>
 void pick_waves(const Matvec &a, uint32_t units, hipStream_t st)
 {
-    constexpr uint32_t kMost = kMQ == 16 ? (kFormat == kNvTile ? 2 : 4) : kMQ == 8 && (kP == 2 || kFormat == kNvTile) ? 5 : 7;
+    constexpr uint32_t kMost = kMQ == 16 ? (kFormat == kNvTile ? 2 : 4) : kMQ == 8 && (kP == 2 || kFormat == kNvTile) ? 5 : kMQ == 4 && kP == 2 ? 6 : 7;
     const uint32_t blocks = (a.N + 15u) / 16u, each = (blocks + units - 1u) / units;
-    const uint32_t waves = each == 1u && kP == 1 ? 16u : each <= 7u ? 8u : 4u;
+    const uint32_t waves = each > 1u ? 4u : kP == 1 && a.steps >= 64u ? 16u : 8u;
     if constexpr (kMQ == 1) {
         run_matvec<kFormat, kX8, 1, 1, kP>(a, waves, st);
     } else {
-        const uint32_t groups = (each + kMost - 1u) / kMost;
-        pick_rows<kFormat, kX8, kMQ, kP, kMost>(a, (each + groups - 1u) / groups, groups > 1u ? 4u : waves, st);
+        const uint32_t groups = (each + kMost - 1u) / kMost, r = (each + groups - 1u) / groups;
+        const bool eight = groups == 1u && ((kMQ == 8 && r * kP > 4u) || (kMQ == 16 && r <= 3u));
+        pick_rows<kFormat, kX8, kMQ, kP, kMost>(a, r, eight ? 8u : waves, st);
     }
 }
 
