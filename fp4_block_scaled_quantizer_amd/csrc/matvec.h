@@ -282,7 +282,15 @@ __global__ __launch_bounds__((Shape<kX8, kMQ, kR, kP>::kWaves * 64)) void matvec
     constexpr uint32_t kA = H::kAhead;
     S s[kA];
     uint32_t step = from;
-    if (to - from >= kA) {
+    if (kA == 1u) {
+        if (from < to) fetch(from, s[0]);
+        for (; step < to; ++step) {
+            multiply(s[0]);
+            __builtin_amdgcn_sched_barrier(0);
+            if (step + 1u < to) fetch(step + 1u, s[0]);
+            __builtin_amdgcn_sched_barrier(0);
+        }
+    } else if (to - from >= kA) {
 #pragma unroll
         for (uint32_t d = 0; d < kA; ++d) fetch(from + d, s[d]);
         for (; step + 2u * kA <= to; step += kA) {
