@@ -150,7 +150,7 @@ __global__ __launch_bounds__((Shape<kX8, kMQ, kR, kP>::kWaves * 64)) void matvec
     const uint32_t lane = threadIdx.x & 63u, r = lane & 15u, q = lane >> 4;
     const uint32_t wave = (uint32_t)__builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6)), waves = blockDim.x >> 6;
     const uint32_t n0 = blockIdx.x * (16u * kR), steps = a.steps / kP;
-    const uint32_t from = steps * wave / waves, to = steps * (wave + 1u) / waves;
+    const uint32_t count = (steps + waves - 1u - wave) / waves;  // the wave's: step `wave` and every `waves`-th after it
 
     // bytes from the step's start, below 2^32 as all of W is: the start is the
     // wave's, in scalar registers
@@ -185,7 +185,8 @@ __global__ __launch_bounds__((Shape<kX8, kMQ, kR, kP>::kWaves * 64)) void matvec
     };
     const int64_t x_row = a.ld_x * (kX8 ? 1 : 2), x_scale_row = a.steps * 4u;
     const uint8_t *x = a.x + row * x_row + piece * 16u, *x_scales = kX8 ? a.x_scales + row * x_scale_row + piece / 2u : nullptr;
-    const auto fetch = [&](uint32_t step, S &s) {
+    const auto fetch = [&](uint32_t i, S &s) {
+        const uint32_t step = wave + i * waves;
         const uint8_t *step_codes = a.w.codes + step * kP * a.w.code_step, *step_scales = a.w.scales + step * kP * a.w.scale_step;
         const uint32_t end = fresh(last);
 #pragma unroll
@@ -281,19 +282,19 @@ __global__ __launch_bounds__((Shape<kX8, kMQ, kR, kP>::kWaves * 64)) void matvec
     // waited for all of them.
     constexpr uint32_t kA = H::kAhead;
     S s[kA];
-    uint32_t step = from;
+    uint32_t step = 0;
     if (kA == 1u) {
-        if (from < to) fetch(from, s[0]);
-        for (; step < to; ++step) {
+        if (count > 0u) fetch(0, s[0]);
+        for (; step < count; ++step) {
             multiply(s[0]);
             __builtin_amdgcn_sched_barrier(0);
-            if (step + 1u < to) fetch(step + 1u, s[0]);
+            if (step + 1u < count) fetch(step + 1u, s[0]);
             __builtin_amdgcn_sched_barrier(0);
         }
-    } else if (to - from >= kA) {
+    } else if (count >= kA) {
 #pragma unroll
-        for (uint32_t d = 0; d < kA; ++d) fetch(from + d, s[d]);
-        for (; step + 2u * kA <= to; step += kA) {
+        for (uint32_t d = 0; d < kA; ++d) fetch(d, s[d]);
+        for (; step + 2u * kA <= count; step += kA) {
 #pragma unroll
             for (uint32_t d = 0; d < kA; ++d) {
                 multiply(s[d]);
@@ -306,14 +307,14 @@ __global__ __launch_bounds__((Shape<kX8, kMQ, kR, kP>::kWaves * 64)) void matvec
         for (uint32_t d = 0; d < kA; ++d) {  // fewer than kA steps are not loaded yet
             multiply(s[d]);
             __builtin_amdgcn_sched_barrier(0);
-            if (step + kA + d < to) fetch(step + kA + d, s[d]);
+            if (step + kA + d < count) fetch(step + kA + d, s[d]);
             __builtin_amdgcn_sched_barrier(0);
         }
 #pragma unroll
         for (uint32_t d = 0; d + 1u < kA; ++d)
-            if (step + kA + d < to) multiply(s[d]);
+            if (step + kA + d < count) multiply(s[d]);
     } else {
-        for (; step < to; ++step) {
+        for (; step < count; ++step) {
             fetch(step, s[0]);
             multiply(s[0]);
         }
