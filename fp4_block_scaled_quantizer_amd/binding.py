@@ -703,8 +703,7 @@ def fp4_matvec_mx(x: torch.Tensor, w_codes: torch.Tensor, w_scales: torch.Tensor
     """Y = alpha * x W^T for at most 64 rows of bf16 x [M x K] and an MXFP4
     operand W [N x K], in y's type or out_dtype. In the tiled layout the code
     tensor carries rows padded to a multiple of 32, so pass the logical n."""
-    return _rows().matvec(x, None, w_codes, w_scales, None, 0, alpha, _out_type(out_dtype), layout, -1 if n is None else n,
-                          y, stream)
+    return _rows().matvec(x, None, w_codes, w_scales, None, 0, alpha, _out_type(out_dtype), layout, n, y, stream)
 
 
 def fp4_matvec_mx_pack8(x_codes: torch.Tensor, x_scales: torch.Tensor, w_codes: torch.Tensor, w_scales: torch.Tensor, *,
@@ -713,8 +712,8 @@ def fp4_matvec_mx_pack8(x_codes: torch.Tensor, x_scales: torch.Tensor, w_codes: 
     """fp4_matvec_mx of 8-bit rows x, as fp4_norm_pack8 or fp4_pack8 left them."""
     if x_scales is None:
         raise ValueError("x_scales must be a tensor")
-    return _rows().matvec(x_codes, x_scales, w_codes, w_scales, None, 0, alpha, _out_type(out_dtype), layout,
-                          -1 if n is None else n, y, stream)
+    return _rows().matvec(x_codes, x_scales, w_codes, w_scales, None, 0, alpha, _out_type(out_dtype), layout, n, y,
+                          stream)
 
 
 def fp4_matvec_nv(x: torch.Tensor, w_codes: torch.Tensor, w_scales: torch.Tensor, w_tensor_scale: torch.Tensor,
@@ -724,5 +723,5 @@ def fp4_matvec_nv(x: torch.Tensor, w_codes: torch.Tensor, w_scales: torch.Tensor
     """fp4_matvec_mx with an NVFP4 operand W of either domain."""
     if w_tensor_scale is None:
         raise ValueError("w_tensor_scale must be a tensor")
-    return _rows().matvec(x, None, w_codes, w_scales, w_tensor_scale, domain, alpha, _out_type(out_dtype), layout,
-                          -1 if n is None else n, y, stream)
+    return _rows().matvec(x, None, w_codes, w_scales, w_tensor_scale, domain, alpha, _out_type(out_dtype), layout, n, y,
+                          stream)

@@ -540,7 +540,7 @@ PyObject *unpack8(PyObject *const *a)
 
 // Products of few rows with FP4 weights.  X: bf16 rows, or where X_SCALES is
 // given the codes of 8-bit rows; TENSOR_SCALE is given where the weights are
-// NVFP4.  N < 0: as many as the codes have rows.
+// NVFP4.  N None: as many as the codes have rows.
 PyObject *matvec(PyObject *const *a)
 {
     enum { X, X_SCALES, CODES, SCALES, TENSOR_SCALE, DOMAIN, ALPHA, TYPE, LAYOUT, N, Y, STREAM };
@@ -550,8 +550,8 @@ PyObject *matvec(PyObject *const *a)
     if (x.dim() != 2 || codes.dim() != 2) throw Refused("x and w_codes must be 2-D tensors");
     if (!packs && x.scalar_type() != at::kBFloat16) throw Refused("x must be bf16");
     OnStream on(a[STREAM], x);
-    const int64_t m = x.size(0), k = x.size(1), stored = codes.size(0), given = integer(a[N]);
-    const int64_t n = given < 0 ? stored : given;
+    const int64_t m = x.size(0), k = x.size(1), n = a[N] == Py_None ? codes.size(0) : integer(a[N]);
+    if (n < 0 || n > INT32_MAX) throw Refused("n must be the operand's rows");
     const int layout = (int)integer(a[LAYOUT]), domain = (int)integer(a[DOMAIN]);
     const int64_t rows = layout == FP4Q_LAYOUT_TILED ? (n + 31) / 32 * 32 : n;  // of the operand
     dense(codes, "w_codes", at::kByte, {rows, k / 2}, x);

@@ -211,3 +211,16 @@ def test_binding_refusals():
                                          B.NV_TILE128)):
         with pytest.raises(ValueError, match="current GPU"):  # nothing wrong but the place
             call()
+
+
+def test_binding_refuses_row_counts():
+    """n has to be the operand's: a negative one is no request for all of them."""
+    u8 = lambda *s: torch.zeros(s, dtype=torch.uint8)  # noqa: E731
+    x = torch.zeros((2, 128), dtype=torch.bfloat16)
+    for n in (-1, -5, -40, 39, 41, 2**40, 2**62):
+        for layout, ws in ((B.LAYOUT_LINEAR, u8(40, 4)), (B.LAYOUT_TILED, u8(1, 40, 4))):
+            with pytest.raises(ValueError) as e:
+                B.fp4_matvec_mx(x, u8(40, 64), ws, layout=layout, n=n)
+            assert "current GPU" not in str(e.value), n
+    with pytest.raises(ValueError, match="current GPU"):
+        B.fp4_matvec_mx(x, u8(40, 64), u8(40, 4), n=40)
