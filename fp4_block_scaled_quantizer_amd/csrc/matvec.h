@@ -122,14 +122,17 @@ struct Step {
 };
 
 // How a kernel is made: rows of x and bytes of each that a wave keeps in LDS,
-// steps that it has in flight, and the most waves of a workgroup.
-template <bool kX8, int kMQ, int kR, int kP>
+// steps that it has in flight, and the most waves of a workgroup (four where
+// a wave needs more than half of its registers).
+template <Format kFormat, bool kX8, int kMQ, int kR, int kP>
 struct Shape {
     static constexpr int kMT = (kMQ + 3) / 4, kTiles = kR * kMT;  // 16 x 16 results
     static constexpr int kRows = kMQ * 4;
     static constexpr uint32_t kPitch = 256 * kP + 16;  // 16 rows' pieces lie in all banks alike
     static constexpr int kAhead = kMQ <= 4 || (kMQ == 8 && kR * kP <= 4) ? 2 : 1;
-    static constexpr int kWaves = kR == 1 && kMQ <= 4 && kP == 1 ? 16 : kRows * kPitch * 8 <= 160 * 1024 ? 8 : 4;
+    static constexpr bool kWide = (kMQ == 16 && kR > (kFormat == kNvTile ? 2 : 4)) ||
+                                  (kP == 2 && ((kMQ == 8 && kR > 5) || (kMQ == 4 && kR > 6)));
+    static constexpr int kWaves = kR == 1 && kMQ <= 4 && kP == 1 ? 16 : !kWide && kRows * kPitch * 8 <= 160 * 1024 ? 8 : 4;
     static constexpr int kAtOnce = kTiles < 64 / kWaves ? kTiles : 64 / kWaves;  // tiles joined at once, in 64 KiB at most
     static uint32_t lds_bytes(uint32_t waves)
     {
@@ -142,10 +145,10 @@ struct Shape {
 // rows (the linear layout): a lane then takes 32 neighbouring bytes, so that a
 // wave's two loads are 128 bytes of each row, and all its scales with one.
 template <Format kFormat, bool kX8, int kMQ, int kR, int kP>
-__global__ __launch_bounds__((Shape<kX8, kMQ, kR, kP>::kWaves * 64)) void matvec_kernel(const Matvec a)
+__global__ __launch_bounds__((Shape<kFormat, kX8, kMQ, kR, kP>::kWaves * 64)) void matvec_kernel(const Matvec a)
 {
     typedef Step<kFormat, kX8, kMQ, kR, kP> S;
-    typedef Shape<kX8, kMQ, kR, kP> H;
+    typedef Shape<kFormat, kX8, kMQ, kR, kP> H;
     extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
     const uint32_t lane = threadIdx.x & 63u, r = lane & 15u, q = lane >> 4;
     const uint32_t wave = (uint32_t)__builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6)), waves = blockDim.x >> 6;
@@ -346,7 +349,7 @@ __global__ __launch_bounds__((Shape<kX8, kMQ, kR, kP>::kWaves * 64)) void matvec
 template <Format kFormat, bool kX8, int kMQ, int kR, int kP>
 void run_matvec(const Matvec &a, uint32_t most, hipStream_t st)
 {
-    typedef Shape<kX8, kMQ, kR, kP> H;
+    typedef Shape<kFormat, kX8, kMQ, kR, kP> H;
     const uint32_t steps = a.steps / kP, limit = most < (uint32_t)H::kWaves ? most : (uint32_t)H::kWaves;
     const uint32_t waves = steps < limit ? (steps > 0u ? steps : 1u) : limit;
     const unsigned grid = (a.N + 16u * kR - 1u) / (16u * kR);
@@ -367,16 +370,22 @@ void pick_rows(const Matvec &a, uint32_t r, uint32_t most, hipStream_t st)
 // those are more than registers hold as few workgroups of the same rows.  With
 // at most four rows of x, which cost little, 16 rows of W each are as good at
 // any size.  Waves: four, of two steps in flight each; eight where a unit has
-// only 16 rows of W, or (with more than 16 rows of x) registers for one step in
-// flight; 16 with at most 16 rows of x on few but long rows of W, whose loads
-// are all that is under way.  The waves, and so the order of the sums, do not
-// depend on x's rows up to 16.
-//   Measured in us on MXFP4 tiled weights from memory, K = 4096 (at a lower
-// clock than the figures above).  16 rows of x, 16 rows of W to a wave / 32 /
-// 48 / 64 / 80 / 112: 8192 rows of W 14 / 11.6 / 12.5, 11008 - / 16.6 / 13.2 /
-// 14.1 / 16.3, 28672 - / - / 28.8 / 24.6 / 26.8 / 23.1, 40000 (80 each for two
-// workgroups) - / - / - / 33.7 / 29.9 / 34.8.  One row of x, 16 / 32: 11008 11.1 /
-// 12.1, 28672 20.7 / 21.6, 60000 38.2 / 38.3.  Four waves of two steps / eight
+// only 16 rows of W, or (with more than 16 rows of x, and registers for them)
+// only one step fits in flight; 16 with at most 16 rows of x on few but long
+// rows of W, whose loads are all that is under way.  The waves, and so the
+// order of the sums, do not depend on x's rows up to 16.
+//   Measured in us on weights from memory, K = 4096, MXFP4 tiled unless named.
+// Rows of W to a wave: 64 rows of x, 28672 rows of W, two workgroups of 64 /
+// one of 112 with four waves 26.4 / 23.1 (in rows 35.5 / 27.8, NVFP4 tiles 32
+// / 112 41.2 / 29.9); 32 rows of x, W in rows, 64 / 112 24.6 / 21.6 (NVFP4
+// tiles 80 / 112 21.5 / 22.9); 16 rows of x, in rows 64 / 112 19.2 / 18.2.
+//   At a lower clock: 16 rows of x, 16 / 32 / 48 / 64 / 80 / 112 rows of W to a
+// wave: 8192 rows of W 14 / 11.6 / 12.5, 11008 - / 16.6 / 13.2 / 14.1 / 16.3,
+// 28672 - / - / 28.8 / 24.6 / 26.8 / 23.1, 40000 (80 each for two workgroups) -
+// / - / - / 33.7 / 29.9 / 34.8.  One row of x, 16 / 32: 11008 11.1 / 12.1, 28672
+// 20.7 / 21.6, 60000 38.2 / 38.3.
+//   Waves: 64 rows of x, eight / four with one step in flight, 4096 rows of W
+// 11.3 / 13.0, 8192 12.3 / 13.7.  At the lower clock four of two steps / eight
 // of two / eight of one, 16 rows of x: 8192 11.6 / 12.0 / 12.5, 14336 14.7 / 15.6
 // / 15.8, 28672 23.1 / 24.3 / 23.3; 32 rows of x: 14336 18.5 / 19.3 / 19.4, but
 // 28672 30.1 / 33.3 / 27.7; 4096 rows of W: 9.8 / 9.5 / 10.5, and with K = 14336
@@ -385,7 +394,7 @@ void pick_rows(const Matvec &a, uint32_t r, uint32_t most, hipStream_t st)
 template <Format kFormat, bool kX8, int kMQ, int kP>
 void pick_waves(const Matvec &a, uint32_t units, hipStream_t st)
 {
-    constexpr uint32_t kMost = kMQ == 16 ? (kFormat == kNvTile ? 2 : 4) : kMQ == 8 && (kP == 2 || kFormat == kNvTile) ? 5 : kMQ == 4 && kP == 2 ? 6 : 7;
+    constexpr uint32_t kMost = kMQ == 8 && kFormat == kNvTile ? 5 : 7;
     const uint32_t blocks = (a.N + 15u) / 16u, each = (blocks + units - 1u) / units;
     const uint32_t waves = each > 1u ? 4u : kP == 1 && a.steps >= 64u ? 16u : 8u;
     if constexpr (kMQ == 1) {

@@ -400,9 +400,8 @@ __global__ __launch_bounds__(1024) void norm_weight_sums_kernel(const NormGradAr
 // there is little to walk, each workgroup has its first rows only (kNoSums).
 // Walked / not, us, bf16: 8192 x 4096 36.2 / 50.7, 2048 x 4096 11.8 / 14.7,
 // 365 x 8192 6.8 / 7.1 (with dres and dropout 9.4 / 8.8), 2048 x 1024 5.5 /
-// 4.7, but 3072 x 1024 6.1 / 7.2, 10000 x 256 6.2 / 5.9; two chunks a thread
-// 400 x 9000 7.4 / 8.3, 219 x 14336 7.6 / 5.9; binary32 512 x 4096 8.0 / 7.7,
-// 768 x 4096 10.9 / 11.7.
+// 4.7, 10000 x 256 6.2 / 5.9; two chunks a thread 400 x 9000 7.4 / 8.3, 219 x
+// 14336 7.6 / 5.9; binary32 512 x 4096 8.0 / 7.7, 768 x 4096 10.9 / 11.7.
 enum How { kNoSums, kRowsWalked, kInRows, kBeside, kApart };
 struct GradPlan {
     How sums;

@@ -109,6 +109,22 @@ def test_many_weight_rows(fmt, tiled, m, n):
         check(got, P.values(x8[0].cpu(), x8[1].cpu()), v, "y of 8-bit rows")
 
 
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("tiled", [False, True])
+@pytest.mark.parametrize("m,n", [(64, 28641), (49, 24570), (33, 20490), (32, 28641), (29, 24570), (16, 28641), (16, 24570)])
+def test_many_rows_of_both(fmt, tiled, m, n):
+    """Up to 112 rows of W to a wave."""
+    dev = device()
+    announce(f"matvec {fmt} tiled {tiled} {m} x {n} x 512")
+    k = 512
+    part, _ = operand(fmt, 256, k, 3, tiled)
+    rows = torch.from_numpy(part).repeat(n // 256 + 1, 1)[:n] * torch.exp2(torch.arange(n) % 5 - 2.0)[:, None]
+    v, w = operand(fmt, n, k, 3, tiled, rows.float())
+    x = draw((m, k), 4, BF)
+    got = matvec(fmt, x.to(dev), [t.to(dev) for t in w], tiled, n=n)
+    check(got, x.double().numpy(), v, "y")
+
+
 def test_weights_are_exact():
     """Each code times each MXFP4 scale that keeps it finite, and times each E4M3 scale, alone in its row."""
     dev = device()
