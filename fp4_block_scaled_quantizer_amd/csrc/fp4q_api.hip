@@ -511,16 +511,20 @@ fp4q_status run_norm_grad(const void *dy, int64_t rows, int64_t cols, int64_t ld
     if (rows == 0 && !sums) return FP4Q_OK;
     const uint64_t es = type_size(type), ws = type_size(w_type);
     if (rows > 0) {
-        if (!dy || (packed ? !h_codes || !h_scales : !h) || !rstd || (kind == FP4Q_NORM_LAYER && !mean) || (!dh && !dx && !sums)) return FP4Q_EINVAL;
+        if (!dy || (packed ? !h_codes || !h_scales : !h) || !rstd || (kind == FP4Q_NORM_LAYER && !mean) ||
+            (!dh && !dx && !sums))
+            return FP4Q_EINVAL;
         const size_t need = sums ? fp4q::norm_grad_workspace_bytes(rows, cols, type == FP4Q_OUT_BF16) : 0;
         if (need > 0 && (!workspace || workspace_bytes < need)) return FP4Q_EINVAL;
         if (!aligned(dy, es) || !aligned(h, es) || !aligned(dres, es) || !aligned(dh, es) || !aligned(dx, es) ||
-            !aligned(gamma, ws) || !aligned(mean, 4) || !aligned(rstd, 4) || (need > 0 && !aligned(workspace, 16)) || !aligned(h_codes, 16))
+            !aligned(gamma, ws) || !aligned(mean, 4) || !aligned(rstd, 4) || (need > 0 && !aligned(workspace, 16)) ||
+            !aligned(h_codes, 16))
             return FP4Q_EALIGN;
         const Matrix in[3] = {matrix(dy, rows, cols, ld_dy, es), matrix(h, rows, cols, ld_h, es),
                               matrix(dres, rows, cols, ld_dres, es)};
         const Matrix mo[2] = {matrix(dh, rows, cols, ld_dh, es), matrix(dx, rows, cols, ld_dx, es)};
-        const Range small[5] = {bytes(gamma, gamma ? cols * ws : 0), bytes(mean, mean ? rows * 4 : 0), bytes(rstd, rows * 4),
+        const Range small[5] = {bytes(gamma, gamma ? cols * ws : 0), bytes(mean, mean ? rows * 4 : 0),
+                                bytes(rstd, rows * 4),
                                 bytes(h_codes, packed ? (uint64_t)rows * cols : 0),
                                 bytes(h_scales, packed ? (uint64_t)rows * cols / 32 : 0)};
         const Range outs[5] = {mo[0].r, mo[1].r, bytes(dgamma, dgamma ? cols * 4 : 0),
@@ -650,7 +654,8 @@ fp4q_status run_matvec(const void *x, const void *x_scales, bool packed, int64_t
     a.y = y;
     a.y_bf16 = y_type == FP4Q_OUT_BF16;
     (void)hipGetLastError();
-    return launched(a.tensor_scale ? fp4q::launch_matvec_nv(a, as_stream(stream)) : fp4q::launch_matvec_mx(a, as_stream(stream)));
+    return launched(a.tensor_scale ? fp4q::launch_matvec_nv(a, as_stream(stream))
+                                   : fp4q::launch_matvec_mx(a, as_stream(stream)));
 }
 
 // fp4_pack8, or with `unpack` fp4_unpack8.

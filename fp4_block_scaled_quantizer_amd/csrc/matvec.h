@@ -13,7 +13,19 @@
 // bits: up to 8e-5 of sum |x w| off, measured, against 1e-7.)  The
 // order of the columns inside an MFMA's sum does not matter as long as both
 // operands have the same, so neither is rearranged.  The waves of a workgroup
-// split the columns and join their sums through LDS in a fixed order.
+// take the columns' steps in turn and join their sums through LDS in a fixed
+// order.
+//   Weights from memory (where a copy reads and writes 6.3 TB/s), us a call:
+// one row of x, MXFP4 tiled 4096 x 4096 4.7 (launch), 28672 x 4096 12.1 (5.2
+// TB/s, HBM; in rows 14.6, NVFP4 tiles 13.7), 4096 x 14336 8.0; 5 rows, NVFP4 4096
+// x 14336 tiled 9.8, in rows 12.0 (a compute unit has 16 rows of W, whose start,
+// 85 vector instructions a step of 128 columns and join are not hidden: four
+// fifths of those are the products of codes and scales, twice MXFP4's); 28672 x
+// 4096 MXFP4 with 16 rows 12.9, 32 8-bit rows 15.3, 64 rows 22.9 (x's way from
+// the L2 through LDS, the converts and the MFMAs, about 6 us each, overlap in
+// part); 32 rows, 4096 x 14336 18.4 (there each compute unit reads seven times
+// as much x as W).  The first kernel, whose lanes loaded x in the MFMA's layout
+// instead of whole lines, took 33 us for the 32 rows and 81 for the 64.
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -132,8 +144,9 @@ struct Shape {
     static constexpr int kAhead = kMQ <= 4 || (kMQ == 8 && kR * kP <= 4) ? 2 : 1;
     static constexpr bool kWide = (kMQ == 16 && kR > (kFormat == kNvTile ? 2 : 4)) ||
                                   (kP == 2 && ((kMQ == 8 && kR > 5) || (kMQ == 4 && kR > 6)));
-    static constexpr int kWaves = kR == 1 && kMQ <= 4 && kP == 1 ? 16 : !kWide && kRows * kPitch * 8 <= 160 * 1024 ? 8 : 4;
-    static constexpr int kAtOnce = kTiles < 64 / kWaves ? kTiles : 64 / kWaves;  // tiles joined at once, in 64 KiB at most
+    static constexpr int kMost = !kWide && kRows * kPitch * 8 <= 160 * 1024 ? 8 : 4;
+    static constexpr int kWaves = kR == 1 && kMQ <= 4 && kP == 1 ? 16 : kMost;
+    static constexpr int kAtOnce = kTiles < 64 / kWaves ? kTiles : 64 / kWaves;  // tiles joined, in 64 KiB at most
     static uint32_t lds_bytes(uint32_t waves)
     {
         const uint32_t x = waves * kRows * kPitch, sums = waves * kAtOnce * 1024u;
@@ -153,7 +166,10 @@ __global__ __launch_bounds__((Shape<kFormat, kX8, kMQ, kR, kP>::kWaves * 64)) vo
     const uint32_t lane = threadIdx.x & 63u, r = lane & 15u, q = lane >> 4;
     const uint32_t wave = (uint32_t)__builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6)), waves = blockDim.x >> 6;
     const uint32_t n0 = blockIdx.x * (16u * kR), steps = a.steps / kP;
-    const uint32_t count = (steps + waves - 1u - wave) / waves;  // the wave's: step `wave` and every `waves`-th after it
+    // the wave's steps: `wave` and every `waves`-th after it, so that those of
+    // the workgroup that are under way are neighbours (each wave a run of its
+    // own: 5 x 4096 x 14336 NVFP4 in rows 12.7 us instead of 12.2)
+    const uint32_t count = (steps + waves - 1u - wave) / waves;
 
     // bytes from the step's start, below 2^32 as all of W is: the start is the
     // wave's, in scalar registers
@@ -187,10 +203,12 @@ __global__ __launch_bounds__((Shape<kFormat, kX8, kMQ, kR, kP>::kWaves * 64)) vo
         return v;
     };
     const int64_t x_row = a.ld_x * (kX8 ? 1 : 2), x_scale_row = a.steps * 4u;
-    const uint8_t *x = a.x + row * x_row + piece * 16u, *x_scales = kX8 ? a.x_scales + row * x_scale_row + piece / 2u : nullptr;
+    const uint8_t *x = a.x + row * x_row + piece * 16u;
+    const uint8_t *x_scales = kX8 ? a.x_scales + row * x_scale_row + piece / 2u : nullptr;
     const auto fetch = [&](uint32_t i, S &s) {
         const uint32_t step = wave + i * waves;
-        const uint8_t *step_codes = a.w.codes + step * kP * a.w.code_step, *step_scales = a.w.scales + step * kP * a.w.scale_step;
+        const uint8_t *step_codes = a.w.codes + step * kP * a.w.code_step;
+        const uint8_t *step_scales = a.w.scales + step * kP * a.w.scale_step;
         const uint32_t end = fresh(last);
 #pragma unroll
         for (int i = 0; i < S::kLoads; ++i) {
@@ -353,7 +371,8 @@ void run_matvec(const Matvec &a, uint32_t most, hipStream_t st)
     const uint32_t steps = a.steps / kP, limit = most < (uint32_t)H::kWaves ? most : (uint32_t)H::kWaves;
     const uint32_t waves = steps < limit ? (steps > 0u ? steps : 1u) : limit;
     const unsigned grid = (a.N + 16u * kR - 1u) / (16u * kR);
-    hipLaunchKernelGGL((matvec_kernel<kFormat, kX8, kMQ, kR, kP>), dim3(grid), dim3(waves * 64u), H::lds_bytes(waves), st, a);
+    hipLaunchKernelGGL((matvec_kernel<kFormat, kX8, kMQ, kR, kP>), dim3(grid), dim3(waves * 64u), H::lds_bytes(waves),
+                       st, a);
 }
 
 template <Format kFormat, bool kX8, int kMQ, int kP, int kR>

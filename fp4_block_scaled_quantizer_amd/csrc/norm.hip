@@ -6,7 +6,8 @@
 //   h = [residual +] dropout(x), rounded to the element type;
 //   mean = sum h / n (RMS: 0), rstd = 1 / sqrt(sum (h - mean)^2 / n + eps);
 //   y = (h - mean) rstd gamma + beta, rounded; optionally the MXFP4 operand
-//   of y along rows, byte for byte what the row producer makes of y.
+//   of y along rows and its 8-bit rows, byte for byte what the row producer
+//   and the packing make of y.
 // A row stays in registers between its two sums (the second one of the
 // centred values, so that a large mean costs no precision), and each input
 // is read and each output written once: HBM-bound.  One workgroup per row, a
@@ -23,7 +24,9 @@
 //   to a compute unit: the loads of all, the stores of all, and one row more);
 //   4097 x 4099 bf16: 23.9 us, 2.8 TB/s (rows share cache lines, and two chunks
 //   a thread leave a fifth of the places empty);
-//   1 x 4096 bf16: 4.8 us a call, launch and latency.
+//   1 x 4096 bf16: 4.8 us a call, launch and latency;
+//   8192 x 4096 to 8-bit rows and no y: bf16 RMS norm with residual 38.5 us, 6.1
+//   TB/s; binary32 layer norm 36.5, 4.6; 1 x 4096 5.8 us a call.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 

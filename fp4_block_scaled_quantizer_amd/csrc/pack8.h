@@ -39,9 +39,9 @@ struct Packed8 {
     u32x2v q;
     uint32_t scale;
     // chunk `c` of all rows' (eight elements each, rows being dense)
-    template <bool kNt> __device__ __forceinline__ void load(const uint8_t *codes, const uint8_t *scales, uint64_t c)
+    __device__ __forceinline__ void load(const uint8_t *codes, const uint8_t *scales, uint64_t c)
     {
-        q = load_vec<kNt>(reinterpret_cast<const u32x2v *>(codes + c * 8u));
+        q = load_vec<false>(reinterpret_cast<const u32x2v *>(codes + c * 8u));
         scale = scales[c >> 2];
     }
     __device__ __forceinline__ void get(float v[8]) const

@@ -4,12 +4,16 @@
 // gradient of the down projection needs it and then need not keep it).
 // C's columns interleave gate and up as in swiglu.hip; dC has the same order.
 //
-// HBM-bound: 6 bytes read and 4 (6 with h) written per hidden element.  A
-// thread takes eight hidden columns of one row: three 16-byte loads and two
-// or three stores, whose pieces of 64 bytes (pair = 32) the caches join, so
-// nothing is streamed past them (non-temporal loads: 250 us instead of 237).
+// C may come as 8-bit rows: its values through the same steps.
+//
+// HBM-bound: 6 bytes read (4.06 with 8-bit rows) and 4 (6 with h) written per
+// hidden element.  A thread takes eight hidden columns of one row: three loads
+// (16 bytes each, of 8-bit rows 8) and two or three stores, whose pieces of 64
+// bytes (pair = 32) the caches join, so nothing is streamed past them
+// (non-temporal loads: 250 us instead of 237).
 // 8192 x 14336 with h: 238 us, 5.9 TB/s; without h 196 us, 6.0 TB/s; 64 x
-// 14336: 4.2 us a call, launch and latency.
+// 14336: 4.2 us a call, launch and latency.  C as 8-bit rows: 8192 x 14336 with
+// h 202 us, without 164, 5.8 TB/s; 64 x 14336 4.7.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -51,8 +55,8 @@ __device__ __forceinline__ void sigmoid_pair(float x, float &s, float &c)
 template <bool kH, bool kRows, bool kPack8>
 __global__ __launch_bounds__(kThreads) void swiglu_grad_kernel(const uint16_t *dh, const uint16_t *c,
                                                                const uint8_t *codes, const uint8_t *scales,
-                                                               uint16_t *dc, uint16_t *h, int64_t M, int64_t ld_dh, int64_t ldc,
-                                                               int64_t ld_dc, int64_t ldh, uint32_t rows,
+                                                               uint16_t *dc, uint16_t *h, int64_t M, int64_t ld_dh,
+                                                               int64_t ldc, int64_t ld_dc, int64_t ldh, uint32_t rows,
                                                                uint32_t per_row, FastDiv row_div, uint32_t pair_chunks,
                                                                FastDiv pair_div)
 {
@@ -66,8 +70,8 @@ __global__ __launch_bounds__(kThreads) void swiglu_grad_kernel(const uint16_t *d
     typename std::conditional<kPack8, Packed8, Chunk<bf16_t>>::type g, u;
     if constexpr (kPack8) {  // dense rows
         const uint64_t at = (uint64_t)(m * ldc + gcol) >> 3;
-        g.template load<false>(codes, scales, at);
-        u.template load<false>(codes, scales, at + pair_chunks);
+        g.load(codes, scales, at);
+        u.load(codes, scales, at + pair_chunks);
     } else {
         const uint16_t *row = c + m * ldc;
         g.q = *reinterpret_cast<const u32x4v *>(row + gcol);
@@ -114,7 +118,8 @@ void run(const SwigluGradArgs &a, hipStream_t st)
     hipLaunchKernelGGL((swiglu_grad_kernel<kH, kRows, kPack8>), grid, dim3(kThreads), 0, st,
                        reinterpret_cast<const uint16_t *>(a.dh), reinterpret_cast<const uint16_t *>(a.c),
                        a.c_codes, a.c_scales, reinterpret_cast<uint16_t *>(a.dc), reinterpret_cast<uint16_t *>(a.h),
-                       a.M, a.ld_dh, kPack8 ? 2 * a.F : a.ldc, a.ld_dc, a.ldh, (uint32_t)rows, per_row, fast_div_for(per_row), pair_chunks,
+                       a.M, a.ld_dh, kPack8 ? 2 * a.F : a.ldc, a.ld_dc, a.ldh, (uint32_t)rows, per_row, fast_div_for(per_row),
+                       pair_chunks,
                        fast_div_for(pair_chunks));
 }
 

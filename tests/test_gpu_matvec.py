@@ -125,6 +125,24 @@ def test_many_rows_of_both(fmt, tiled, m, n):
     check(got, x.double().numpy(), v, "y")
 
 
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("tiled", [False, True])
+@pytest.mark.parametrize("each", [2, 3, 4, 5, 6, 7, 8])
+def test_weight_rows_of_a_wave(fmt, tiled, each):
+    """16 rows of W to a compute unit, twice that, and so on: every count of them to a wave."""
+    dev = device()
+    units, k = torch.cuda.get_device_properties(dev).multi_processor_count, 768 if each % 2 else 256
+    n = 16 * units * each - 21
+    announce(f"matvec {fmt} tiled {tiled} {n} x {k}")
+    part, _ = operand(fmt, 256, k, each, tiled)
+    rows = torch.from_numpy(part).repeat(n // 256 + 1, 1)[:n] * torch.exp2(torch.arange(n) % 3 - 1.0)[:, None]
+    v, w = operand(fmt, n, k, each, tiled, rows.float())
+    w = [t.to(dev) for t in w]
+    for m in (4, 8, 16, 32, 64):
+        x = draw((m, k), m, BF)
+        check(matvec(fmt, x.to(dev), w, tiled, n=n), x.double().numpy(), v, f"y of {m} rows")
+
+
 def test_weights_are_exact():
     """Each code times each MXFP4 scale that keeps it finite, and times each E4M3 scale, alone in its row."""
     dev = device()
