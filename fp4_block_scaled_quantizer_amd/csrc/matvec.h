@@ -22,7 +22,7 @@
 // 85 vector instructions a step of 128 columns and join are not hidden: four
 // fifths of those are the products of codes and scales, twice MXFP4's); 28672 x
 // 4096 MXFP4 with 16 rows 12.9, 32 8-bit rows 15.3, 64 rows 22.9 (x's way from
-// the L2 through LDS, the converts and the MFMAs, about 6 us each, overlap in
+// the L2 through LDS, the converts and the MFMAs, 5 to 7 us each, overlap in
 // part); 32 rows, 4096 x 14336 18.4 (there each compute unit reads seven times
 // as much x as W).  The first kernel, whose lanes loaded x in the MFMA's layout
 // instead of whole lines, took 33 us for the 32 rows and 81 for the 64.
