@@ -23,8 +23,8 @@
 // fifths of those are the products of codes and scales, twice MXFP4's); 28672 x
 // 4096 MXFP4 with 16 rows 12.9, 32 8-bit rows 15.3, 64 rows 22.9 (x's way from
 // the L2 through LDS, the converts and the MFMAs, 5 to 7 us each, overlap in
-// part); 32 rows, 4096 x 14336 18.4 (there each compute unit reads seven times
-// as much x as W).  The first kernel, whose lanes loaded x in the MFMA's layout
+// part); 32 rows, 4096 x 14336 14.3 (where a compute unit reads as much of x as
+// of W).  The first kernel, whose lanes loaded x in the MFMA's layout
 // instead of whole lines, took 33 us for the 32 rows and 81 for the 64.
 #pragma once
 
@@ -43,22 +43,24 @@ typedef float f32x4v __attribute__((ext_vector_type(4)));
 
 // Where the layouts have row n's piece q of step s: codes at n / 32 *
 // code_group + n mod 32 * code_row + q / 2 * code_pair + q mod 2 * code_q + s *
-// code_step, scales alike.
+// code_step, scales alike (modulo 2^32 but for the steps).
 struct Weights4 {
     const uint8_t *codes, *scales;
-    int64_t code_group, code_row, scale_group, scale_row;
-    uint32_t code_pair, code_q, scale_q;
+    uint32_t code_group, code_row, scale_group, scale_row;
     int64_t code_step, scale_step;
+    uint32_t code_pair, code_q, scale_q, N;
 };
 struct Matvec {
     Weights4 w;
     const uint8_t *x, *x_scales;
     const float *tensor_scale;
-    int64_t ld_x, ld_y;  // elements
-    uint32_t M, N, steps;
-    float alpha;
+    int64_t ld_x;  // elements
+    uint32_t M, steps;
+    int64_t ld_y;
     void *y;
+    float alpha;
     bool y_bf16;
+    uint32_t groups;  // of rows of x, each a workgroup's
 };
 
 // Eight weights, a word of codes, as bf16.
@@ -101,21 +103,21 @@ __device__ __forceinline__ void store4(const Matvec &a, uint32_t m, uint32_t n, 
     if (a.y_bf16) {
         bf16_t *y = reinterpret_cast<bf16_t *>(a.y) + at;
         const u32x2v w = {pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])};
-        if (n + 3u < a.N) {
+        if (n + 3u < a.w.N) {
             *reinterpret_cast<u32x2_a2 *>(y) = w;
         } else {
 #pragma unroll
             for (uint32_t e = 0; e < 4u; ++e)
-                if (n + e < a.N) y[e].bits = (uint16_t)(w[e >> 1] >> (16u * (e & 1u)));
+                if (n + e < a.w.N) y[e].bits = (uint16_t)(w[e >> 1] >> (16u * (e & 1u)));
         }
     } else {
         float *y = reinterpret_cast<float *>(a.y) + at;
-        if (n + 3u < a.N) {
+        if (n + 3u < a.w.N) {
             *reinterpret_cast<u32x4_a4 *>(y) = __builtin_bit_cast(u32x4v, v);
         } else {
 #pragma unroll
             for (uint32_t e = 0; e < 4u; ++e)
-                if (n + e < a.N) y[e] = v[e];
+                if (n + e < a.w.N) y[e] = v[e];
         }
     }
 }
@@ -154,7 +156,8 @@ struct Shape {
     }
 };
 
-// kR: 16 rows of W each; grid.x: groups of 16 kR rows of W.  kP = 2 is for W in
+// kR: 16 rows of W each; grid.x: groups of 16 kR rows of W (or a few more, with
+// nothing to store), grid.y: of 4 kMQ rows of x.  kP = 2 is for W in
 // rows (the linear layout): a lane then takes 32 neighbouring bytes, so that a
 // wave's two loads are 128 bytes of each row, and all its scales with one.
 template <Format kFormat, bool kX8, int kMQ, int kR, int kP>
@@ -163,9 +166,17 @@ __global__ __launch_bounds__((Shape<kFormat, kX8, kMQ, kR, kP>::kWaves * 64)) vo
     typedef Step<kFormat, kX8, kMQ, kR, kP> S;
     typedef Shape<kFormat, kX8, kMQ, kR, kP> H;
     extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
+    // all arguments wanted at once, and none between them that is not: the
+    // compiler loads others over those it does not need, and waits for them one
+    // after the other (0.25 us a call and wait)
+    asm volatile("" ::"s"(a.w.codes), "s"(a.w.scales), "s"(a.w.code_group), "s"(a.w.code_row), "s"(a.w.scale_group),
+                 "s"(a.w.scale_row), "s"(a.w.code_step), "s"(a.w.scale_step), "s"(a.x), "s"(a.ld_x), "s"(a.M),
+                 "s"(a.w.N), "s"(a.steps), "s"(a.w.scale_q), "s"(a.w.code_pair), "s"(a.w.code_q), "s"(a.x_scales),
+                 "s"(a.tensor_scale), "s"((uint32_t)blockDim.x));
     const uint32_t lane = threadIdx.x & 63u, r = lane & 15u, q = lane >> 4;
     const uint32_t wave = (uint32_t)__builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6)), waves = blockDim.x >> 6;
-    const uint32_t n0 = blockIdx.x * (16u * kR), steps = a.steps / kP;
+    const uint32_t n0 = blockIdx.x * (16u * kR), m0 = blockIdx.y * H::kRows, M = min(a.M - m0, (uint32_t)H::kRows);
+    const uint32_t steps = a.steps / kP;
     // the wave's steps: `wave` and every `waves`-th after it, so that those of
     // the workgroup that are under way are neighbours (each wave a run of its
     // own: 5 x 4096 x 14336 NVFP4 in rows 12.7 us instead of 12.2)
@@ -177,13 +188,13 @@ __global__ __launch_bounds__((Shape<kFormat, kX8, kMQ, kR, kP>::kWaves * 64)) vo
     const float *tile[kFormat == kNvTile ? kR : 1];
 #pragma unroll
     for (int j = 0; j < kR; ++j) {  // past W's end: its last row again, not stored
-        const uint32_t n = min(n0 + 16u * j + r, a.N - 1u);
-        codes[j] = (uint32_t)((int64_t)(n >> 5) * a.w.code_group + (int64_t)(n & 31u) * a.w.code_row) +
+        const uint32_t n = min(n0 + 16u * j + r, a.w.N - 1u);
+        codes[j] = (n >> 5) * a.w.code_group + (n & 31u) * a.w.code_row +
                    (kP == 2 ? q * 32u : (q >> 1) * a.w.code_pair + (q & 1u) * a.w.code_q);
-        scales[j] = (uint32_t)((int64_t)(n >> 5) * a.w.scale_group + (int64_t)(n & 31u) * a.w.scale_row) +
+        scales[j] = (n >> 5) * a.w.scale_group + (n & 31u) * a.w.scale_row +
                     q * a.w.scale_q * kP;
         // 16 rows are within one 128 x 128 tile
-        if (kFormat == kNvTile) tile[j] = a.tensor_scale + (int64_t)(min(n0 + 16u * j, a.N - 1u) >> 7) * a.steps;
+        if (kFormat == kNvTile) tile[j] = a.tensor_scale + (int64_t)(min(n0 + 16u * j, a.w.N - 1u) >> 7) * a.steps;
     }
     // A load of x takes 64 / kPer rows, the last ones of M where it would go
     // past them (the rows before M are then there twice, the same; those of
@@ -191,8 +202,8 @@ __global__ __launch_bounds__((Shape<kFormat, kX8, kMQ, kR, kP>::kWaves * 64)) vo
     // rows' place is the same for the wave, a lane's own part of the address
     // the same for all loads.
     constexpr uint32_t kPer = (kX8 ? 8 : 16) * kP, kOnce = 64u / kPer;
-    const uint32_t row = min(lane / kPer, a.M - 1u), piece = lane % kPer;
-    const uint32_t last = a.M > kOnce ? a.M - kOnce : 0u;
+    const uint32_t row = min(lane / kPer, M - 1u), piece = lane % kPer;
+    const uint32_t last = M > kOnce ? M - kOnce : 0u;
     // made anew in each step where the loads are many: kept over the loop, their
     // addresses spill
     const auto fresh = [](uint32_t v) {
@@ -203,8 +214,8 @@ __global__ __launch_bounds__((Shape<kFormat, kX8, kMQ, kR, kP>::kWaves * 64)) vo
         return v;
     };
     const int64_t x_row = a.ld_x * (kX8 ? 1 : 2), x_scale_row = a.steps * 4u;
-    const uint8_t *x = a.x + row * x_row + piece * 16u;
-    const uint8_t *x_scales = kX8 ? a.x_scales + row * x_scale_row + piece / 2u : nullptr;
+    const uint8_t *x = a.x + (m0 + row) * x_row + piece * 16u;
+    const uint8_t *x_scales = kX8 ? a.x_scales + (m0 + row) * x_scale_row + piece / 2u : nullptr;
     const auto fetch = [&](uint32_t i, S &s) {
         const uint32_t step = wave + i * waves;
         const uint8_t *step_codes = a.w.codes + step * kP * a.w.code_step;
@@ -356,10 +367,10 @@ __global__ __launch_bounds__((Shape<kFormat, kX8, kMQ, kR, kP>::kWaves * 64)) vo
             for (uint32_t k = 1; k < waves; ++k) sum += p[k * 64u];
             // lane l has rows 4 (l / 16) .. + 3 of the tile's 16 of W, row l mod 16 of x
             const uint32_t n = n0 + (t + t0) / H::kMT * 16u + q * 4u, m = (t + t0) % H::kMT * 16u + r;
-            if (m >= a.M) continue;
+            if (m >= M) continue;
 #pragma unroll
             for (int e = 0; e < 4; ++e) sum[e] = sum[e] * scale * a.alpha;
-            store4(a, m, n, sum);
+            store4(a, m0 + m, n, sum);
         }
     }
 }
@@ -370,15 +381,17 @@ void run_matvec(const Matvec &a, uint32_t most, hipStream_t st)
     typedef Shape<kFormat, kX8, kMQ, kR, kP> H;
     const uint32_t steps = a.steps / kP, limit = most < (uint32_t)H::kWaves ? most : (uint32_t)H::kWaves;
     const uint32_t waves = steps < limit ? (steps > 0u ? steps : 1u) : limit;
-    const unsigned grid = (a.N + 16u * kR - 1u) / (16u * kR);
-    hipLaunchKernelGGL((matvec_kernel<kFormat, kX8, kMQ, kR, kP>), dim3(grid), dim3(waves * 64u), H::lds_bytes(waves),
+    unsigned grid = (a.w.N + 16u * kR - 1u) / (16u * kR);
+    // workgroup i runs on XCD i mod 8: the groups that read the same rows of W on one
+    if (a.groups > 1u) grid = (grid + 7u) / 8u * 8u;
+    hipLaunchKernelGGL((matvec_kernel<kFormat, kX8, kMQ, kR, kP>), dim3(grid, a.groups), dim3(waves * 64u), H::lds_bytes(waves),
                        st, a);
 }
 
 template <Format kFormat, bool kX8, int kMQ, int kP, int kR>
 void pick_rows(const Matvec &a, uint32_t r, uint32_t most, hipStream_t st)
 {
-    if constexpr (kR > 1) {
+    if constexpr (kR > (kMQ == 16 ? 2 : 1)) {  // (16 rows of W alone get at most 32 of x)
         if (r < (uint32_t)kR) return pick_rows<kFormat, kX8, kMQ, kP, kR - 1>(a, r, most, st);
     }
     run_matvec<kFormat, kX8, kMQ, kR, kP>(a, most, st);
@@ -403,8 +416,8 @@ void pick_rows(const Matvec &a, uint32_t r, uint32_t most, hipStream_t st)
 // 28672 - / - / 28.8 / 24.6 / 26.8 / 23.1, 40000 (80 each for two workgroups) -
 // / - / - / 33.7 / 29.9 / 34.8.  One row of x, 16 / 32: 11008 11.1 / 12.1, 28672
 // 20.7 / 21.6, 60000 38.2 / 38.3.
-//   Waves: 64 rows of x, eight / four with one step in flight, 4096 rows of W
-// 11.3 / 13.0, 8192 12.3 / 13.7.  At the lower clock four of two steps / eight
+//   Waves: 64 rows of x in one workgroup, eight / four with one step in flight,
+// 4096 rows of W 11.3 / 13.0, 8192 12.3 / 13.7.  At the lower clock four of two steps / eight
 // of two / eight of one, 16 rows of x: 8192 11.6 / 12.0 / 12.5, 14336 14.7 / 15.6
 // / 15.8, 28672 23.1 / 24.3 / 23.3; 32 rows of x: 14336 18.5 / 19.3 / 19.4, but
 // 28672 30.1 / 33.3 / 27.7; 4096 rows of W: 9.8 / 9.5 / 10.5, and with K = 14336
@@ -414,7 +427,7 @@ template <Format kFormat, bool kX8, int kMQ, int kP>
 void pick_waves(const Matvec &a, uint32_t units, hipStream_t st)
 {
     constexpr uint32_t kMost = kMQ == 8 && kFormat == kNvTile ? 5 : 7;
-    const uint32_t blocks = (a.N + 15u) / 16u, each = (blocks + units - 1u) / units;
+    const uint32_t blocks = (a.w.N + 15u) / 16u, each = (blocks * a.groups + units - 1u) / units;
     const uint32_t waves = each > 1u ? 4u : kP == 1 && a.steps >= 64u ? 16u : 8u;
     if constexpr (kMQ == 1) {
         run_matvec<kFormat, kX8, 1, 1, kP>(a, waves, st);
@@ -434,19 +447,50 @@ void pick_layout(const Matvec &a, bool linear, uint32_t units, hipStream_t st)
     pick_waves<kFormat, kX8, kMQ, 1>(a, units, st);
 }
 
+// Rows of x to a workgroup.  Where a unit has few rows of W, x of many rows is
+// most of what it reads and stages; groups of x's rows in workgroups of their
+// own read W again (from the L2, being on one XCD and under way together).
+// The cost of a unit's rows of W (16 each) and of x (four each) is weighed as
+// measured: NVFP4's converts, and W in rows, count for more.
+//   us from memory, one group / as many as this gives: 32 rows of x, MXFP4 tiled
+// 512 x 8192 11.1 / 5.2, 4096 x 4096 7.5 / 6.0, 4096 x 14336 18.4 / 14.3, 8192 x
+// 4096 8.4 / 7.7, NVFP4 2000 x 14336 18.6 / 12.5; 64 rows, MXFP4 4096 x 4096 11.2 /
+// 7.2; 16 rows 512 x 8192 7.7 / 5.3.  24 rows, in two groups where this gives
+// one: MXFP4 12000 x 8192 15.1 / 16.2, in rows 20.4 / 23.8.
+uint32_t group_rows(const Matvec &a, bool nv, bool x8, bool linear, uint32_t units)
+{
+    uint32_t whole = 4u;
+    while (whole < a.M) whole *= 2u;
+    const uint32_t blocks = (a.w.N + 15u) / 16u, of_w = nv ? 24u : linear ? 14u : 9u, of_x = x8 && linear ? 4u : 8u;
+    uint32_t best = whole, least = 0u;
+    for (uint32_t rows = whole; rows >= 4u; rows /= 2u) {
+        const uint32_t groups = (a.M + rows - 1u) / rows, each = (blocks * groups + units - 1u) / units;
+        // up to 16 rows the order of the sums stays that of one row, whose waves are chosen by `each`
+        if (groups > 1u && each > 1u && (a.M <= 16u || rows == 4u)) break;
+        const uint32_t r = (each + (each + 6u) / 7u - 1u) / ((each + 6u) / 7u), wide = (blocks + r - 1u) / r;
+        const uint32_t workgroups = groups > 1u ? (wide + 7u) / 8u * 8u * groups : wide;
+        const uint32_t cost = (workgroups + units - 1u) / units * (r * of_w + rows / 4u * of_x);
+        if (rows == whole || cost * 16u < least * 15u) least = cost, best = rows;
+    }
+    return best;
+}
+
 template <Format kFormat, bool kX8>
 void pick_matvec(const Matvec &a, bool linear, uint32_t units, hipStream_t st)
 {
-    if (a.M <= 4)
-        pick_layout<kFormat, kX8, 1>(a, linear, units, st);
-    else if (a.M <= 8)
-        pick_layout<kFormat, kX8, 2>(a, linear, units, st);
-    else if (a.M <= 16)
-        pick_layout<kFormat, kX8, 4>(a, linear, units, st);
-    else if (a.M <= 32)
-        pick_layout<kFormat, kX8, 8>(a, linear, units, st);
+    Matvec g = a;
+    const uint32_t rows = group_rows(a, kFormat != kMx, kX8, linear, units);
+    g.groups = (a.M + rows - 1u) / rows;
+    if (rows <= 4u)
+        pick_layout<kFormat, kX8, 1>(g, linear, units, st);
+    else if (rows <= 8u)
+        pick_layout<kFormat, kX8, 2>(g, linear, units, st);
+    else if (rows <= 16u)
+        pick_layout<kFormat, kX8, 4>(g, linear, units, st);
+    else if (rows <= 32u)
+        pick_layout<kFormat, kX8, 8>(g, linear, units, st);
     else
-        pick_layout<kFormat, kX8, 16>(a, linear, units, st);
+        pick_layout<kFormat, kX8, 16>(g, linear, units, st);
 }
 
 Matvec matvec_of(const MatvecArgs &g)
@@ -461,8 +505,8 @@ Matvec matvec_of(const MatvecArgs &g)
     a.w.code_q = 16;
     a.w.scale_q = nv ? 2 : 1;
     if (!g.tiled) {
-        a.w.code_row = K / 2;
-        a.w.scale_row = scale_bytes;
+        a.w.code_row = (uint32_t)(K / 2);
+        a.w.scale_row = (uint32_t)scale_bytes;
         a.w.code_step = 64;
         a.w.scale_step = nv ? 8 : 4;
     } else if (nv) {  // [Rp/32][K/128][32][64] and [Rp/32][K/128][32][8]
@@ -478,15 +522,15 @@ Matvec matvec_of(const MatvecArgs &g)
         a.w.code_step = 2048;
         a.w.scale_step = (g.N + 31) / 32 * 128;
     }
-    a.w.code_group = 16 * K;
-    a.w.scale_group = g.tiled && !nv ? 128 : 32 * scale_bytes;
+    a.w.code_group = (uint32_t)(16 * K);
+    a.w.scale_group = g.tiled && !nv ? 128u : (uint32_t)(32 * scale_bytes);
     a.x = reinterpret_cast<const uint8_t *>(g.x);
     a.x_scales = reinterpret_cast<const uint8_t *>(g.x_scales);
     a.tensor_scale = g.tensor_scale;
     a.ld_x = g.ld_x;
     a.ld_y = g.ld_y;
     a.M = (uint32_t)g.M;
-    a.N = (uint32_t)g.N;
+    a.w.N = (uint32_t)g.N;
     a.steps = (uint32_t)(K / 128);
     a.alpha = g.alpha;
     a.y = g.y;

@@ -267,6 +267,39 @@ def test_same_bits_whatever_the_other_rows():
         assert torch.equal(B.fp4_matvec_mx(x[i:i + 1], *w, layout=B.LAYOUT_TILED, n=200), y[i:i + 1])
 
 
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("n,k", [(200, 8192), (33, 14336), (2100, 1024), (4096, 512), (9000, 256)])
+def test_same_bits_at_other_sizes(fmt, n, k):
+    dev = device()
+    tiled = n != 2100
+    announce(f"matvec batched and alone {fmt} {n} x {k}")
+    _, w = operand(fmt, n, k, 5, tiled)
+    w = [t.to(dev) for t in w]
+    x = draw((16, k), 6, BF).to(dev)
+    y = matvec(fmt, x, w, tiled, n=n)
+    for m in (1, 3, 4, 5, 8, 9, 13):
+        assert torch.equal(matvec(fmt, x[16 - m:], w, tiled, n=n), y[16 - m:]), m
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("m", [9, 17, 24, 31, 33, 47, 49, 63])
+def test_groups_of_rows(fmt, m):
+    """Rows of x in several workgroups, the last of them short; rows and columns of W that end inside one."""
+    dev = device()
+    for n, k, tiled in ((130, 2048, True), (999, 512, False), (4100, 384, True), (4096, 256, False)):
+        announce(f"matvec {fmt} groups of {m} rows {n} x {k}")
+        v, w = operand(fmt, n, k, m + n, tiled)
+        w = [t.to(dev) for t in w]
+        x = draw((m, k), n, BF)
+        px, py = Padded(m, k, BF, dev, 8, 0, x), Padded(m, n, BF, dev, 3, 1)
+        check(matvec(fmt, px.view, w, tiled, n=n, y=py.view), x.double().numpy(), v, "y")
+        assert py.untouched()
+        if fmt == "mx":
+            x8 = B.fp4_pack8(x.to(dev))
+            got = B.fp4_matvec_mx_pack8(*x8, *w, n=n, layout=B.LAYOUT_TILED if tiled else B.LAYOUT_LINEAR)
+            check(got, P.values(x8[0].cpu(), x8[1].cpu()), v, "y of 8-bit rows")
+
+
 def test_streams_and_graph():
     dev = device()
     announce("matvec on other streams and in a graph")
