@@ -348,7 +348,7 @@ def _own_matvec(s):
     if s["weights"] != "mx":
         return {"y": B.fp4_matvec_nv(s["x"], s["codes"], s["scales"], s["tensor_scale"],
                                      B.NV_GLOBAL if s["weights"] == "nv" else B.NV_TILE128, layout=layout, n=s["n"], y=s["y"])}
-    if "x_codes" in s:
+    if s["x"] == "pack8":
         return {"y": B.fp4_matvec_mx_pack8(s["x_codes"], s["x_scales"], s["codes"], s["scales"], layout=layout,
                                            n=s["n"], y=s["y"])}
     return {"y": B.fp4_matvec_mx(s["x"], s["codes"], s["scales"], layout=layout, n=s["n"], y=s["y"])}
