@@ -639,7 +639,7 @@ fp4q_status run_matvec(const void *x, const void *x_scales, bool packed, int64_t
     }
     fp4q::MatvecArgs a{};
     a.x = x;
-    a.x_scales = packed && K > 0 ? x_scales : nullptr;
+    a.x_scales = packed ? x_scales : nullptr;
     a.M = M;
     a.N = N;
     a.K = K;
@@ -647,15 +647,17 @@ fp4q_status run_matvec(const void *x, const void *x_scales, bool packed, int64_t
     a.ld_y = ld_y;
     a.codes = codes;
     a.scales = scales;
-    a.tensor_scale = nv && K > 0 ? tensor_scale : nullptr;
+    a.tensor_scale = nv ? tensor_scale : nullptr;
     a.nv_domain = domain;
     a.tiled = layout == FP4Q_LAYOUT_TILED;
     a.alpha = alpha;
     a.y = y;
     a.y_bf16 = y_type == FP4Q_OUT_BF16;
     (void)hipGetLastError();
-    return launched(a.tensor_scale ? fp4q::launch_matvec_nv(a, as_stream(stream))
-                                   : fp4q::launch_matvec_mx(a, as_stream(stream)));
+    hipStream_t st = as_stream(stream);
+    return launched(K == 0 ? fp4q::launch_matvec_zero(a, st)
+                    : nv   ? fp4q::launch_matvec_nv(a, st)
+                           : fp4q::launch_matvec_mx(a, st));
 }
 
 // fp4_pack8, or with `unpack` fp4_unpack8.

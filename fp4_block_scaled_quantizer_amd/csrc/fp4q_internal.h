@@ -156,6 +156,7 @@ int norm_grad_rows_pack8(const NormGradArgs &a, float *dgamma, float *dbeta, hip
 int launch_swiglu_grad(const SwigluGradArgs &a, hipStream_t st);
 int launch_rotary(RotaryArgs a, hipStream_t st);
 int launch_pack8(const Pack8Args &a, hipStream_t st);
+int launch_matvec_zero(const MatvecArgs &a, hipStream_t st);  // K == 0: only M, N and Y are looked at
 int launch_matvec_mx(const MatvecArgs &a, hipStream_t st);
 int launch_matvec_nv(const MatvecArgs &a, hipStream_t st);
 

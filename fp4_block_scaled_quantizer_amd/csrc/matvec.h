@@ -380,7 +380,7 @@ void run_matvec(const Matvec &a, uint32_t most, hipStream_t st)
 {
     typedef Shape<kFormat, kX8, kMQ, kR, kP> H;
     const uint32_t steps = a.steps / kP, limit = most < (uint32_t)H::kWaves ? most : (uint32_t)H::kWaves;
-    const uint32_t waves = steps < limit ? (steps > 0u ? steps : 1u) : limit;
+    const uint32_t waves = steps < limit ? steps : limit;  // at least one of each
     unsigned grid = (a.w.N + 16u * kR - 1u) / (16u * kR);
     // workgroup i runs on XCD i mod 8: the groups that read the same rows of W on one
     if (a.groups > 1u) grid = (grid + 7u) / 8u * 8u;
