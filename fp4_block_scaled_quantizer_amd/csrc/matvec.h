@@ -7,8 +7,9 @@
 // the 16 bytes of row l mod 16, columns 32 (l / 16) .. + 31, which is a run of
 // whole scale blocks in every layout, makes the 32 weights' exact bf16 values
 // (an E2M1 code times a power of two, or times an E4M3 scale, has at most six
-// significant bits) and multiplies them on v_mfma_f32_16x16x32_bf16 with the
-// same columns of 16 rows of x, in binary32 sums.  (The scaled FP4 x FP8
+// significant bits; those of 2^128 and more: large_rows) and multiplies them
+// on v_mfma_f32_16x16x32_bf16 with the same columns of 16 rows of x, in
+// binary32 sums.  (The scaled FP4 x FP8
 // MFMA would take both without a convert, but sums 8-bit products with fewer
 // bits: up to 8e-5 of sum |x w| off, measured, against 1e-7.)  The
 // order of the columns inside an MFMA's sum does not matter as long as both
@@ -119,6 +120,73 @@ __device__ __forceinline__ void store4(const Matvec &a, uint32_t m, uint32_t n, 
             for (uint32_t e = 0; e < 4u; ++e)
                 if (n + e < a.w.N) y[e] = v[e];
         }
+    }
+}
+
+// bf16 ends at 2^128, and an MXFP4 weight of a scale byte above 252 (which the
+// producers do not write) may reach 1.5 * 2^129: it was infinite in the MFMA,
+// and NaN times a zero.  So where a sum is not finite, the wave looks through
+// the scales of the tile's 16 rows of W for such a byte (large_rows), and the
+// elements of those rows that are not finite are summed again, each by its
+// lane in binary64 (again4).  What an element becomes is thus a matter of its
+// own row of x and of W, and the loop over W has no part in it.
+//   28672 x 4096 tiled, us without / with this: one row of x 12.0 / 12.1, 64
+// rows 22.7 / 23.1; with a NaN in a row of x (W from the caches) 11.1 / 13.0 and
+// 22.6 / 33.3.
+
+// Bit r: row n + r of W has a scale byte of 253 or 254.  The whole wave must
+// call it.
+__device__ __forceinline__ uint32_t large_rows(const Matvec &a, uint32_t n, uint32_t r, uint32_t q)
+{
+    const uint32_t row = min(n + r, a.w.N - 1u);
+    const uint8_t *scales = a.w.scales + ((row >> 5) * a.w.scale_group + (row & 31u) * a.w.scale_row);
+    bool large = false;
+    for (uint32_t s = q; s < a.steps; s += 4u) {  // a step's four bytes side by side
+        const uint32_t four = *reinterpret_cast<const uint32_t *>(scales + s * a.w.scale_step);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const uint32_t byte = four >> (8 * k) & 255u;
+            large |= byte == 253u || byte == 254u;
+        }
+    }
+    const uint64_t b = __ballot(large);
+    return (uint32_t)(b | b >> 16 | b >> 32 | b >> 48) & 0xFFFFu;
+}
+
+// Elements (m, n + j) of Y, bit j of `which` set, where they are not finite.
+template <bool kX8>
+__device__ __forceinline__ void again4(const Matvec &a, uint32_t m, uint32_t n, uint32_t which)
+{
+    const uint8_t *x = a.x + m * (a.ld_x * (kX8 ? 1 : 2)), *x_scales = kX8 ? a.x_scales + m * (a.steps * 4ull) : nullptr;
+    for (uint32_t i = n; i < n + 4u && i < a.w.N; ++i) {
+        if (!(which >> (i - n) & 1u)) continue;
+        const int64_t to = (int64_t)m * a.ld_y + i;
+        const float was = a.y_bf16 ? as_float(reinterpret_cast<const bf16_t *>(a.y)[to]) : reinterpret_cast<const float *>(a.y)[to];
+        if (was - was == 0.0f) continue;
+        const uint8_t *codes = a.w.codes + ((i >> 5) * a.w.code_group + (i & 31u) * a.w.code_row);
+        const uint8_t *scales = a.w.scales + ((i >> 5) * a.w.scale_group + (i & 31u) * a.w.scale_row);
+        double v = 0.0;
+        for (uint32_t at = 0; at < a.steps * 16u; ++at) {  // eight columns, a word of codes
+            const uint32_t s = at >> 4, q = at >> 2 & 3u, byte = scales[s * a.w.scale_step + q];
+            const double unit = byte == 255u ? (double)__builtin_nanf("") : __builtin_ldexp(1.0, (int)byte - 127);
+            const uint32_t w = *reinterpret_cast<const uint32_t *>(
+                codes + s * a.w.code_step + (q >> 1) * a.w.code_pair + (q & 1u) * a.w.code_q + (at & 3u) * 4u);
+            bf16x8v e;
+            if constexpr (kX8) {
+                const u32x2v b = *reinterpret_cast<const u32x2v *>(x + at * 8ull);
+                e = rows8(b[0], b[1], mx_scale_f32(x_scales[at >> 2]));
+            } else {
+                e = *reinterpret_cast<const bf16x8v *>(x + at * 16ull);
+            }
+            const bf16x8v f = weights8_mx(w, 1.0f);
+#pragma unroll
+            for (int k = 0; k < 8; ++k) v = __builtin_fma((double)(float)f[k] * unit, (double)(float)e[k], v);
+        }
+        const float y = (float)v * a.alpha;
+        if (a.y_bf16)
+            reinterpret_cast<bf16_t *>(a.y)[to].bits = (uint16_t)pack_bf16x2(y, y);
+        else
+            reinterpret_cast<float *>(a.y)[to] = y;
     }
 }
 
@@ -354,6 +422,7 @@ __global__ __launch_bounds__((Shape<kFormat, kX8, kMQ, kR, kP>::kWaves * 64)) vo
     __syncthreads();  // the sums take x's place
     f32x4v *parts = reinterpret_cast<f32x4v *>(lds);  // [tiles][waves][64]
     const float scale = kFormat == kNvGlobal ? a.tensor_scale[0] : 1.0f;
+    uint32_t again = 0;  // bit j kMT + i: this lane's part of that tile has a sum that is not finite
 #pragma unroll
     for (int t0 = 0; t0 < H::kTiles; t0 += H::kAtOnce) {
         if (t0 > 0) __syncthreads();
@@ -368,9 +437,25 @@ __global__ __launch_bounds__((Shape<kFormat, kX8, kMQ, kR, kP>::kWaves * 64)) vo
             // lane l has rows 4 (l / 16) .. + 3 of the tile's 16 of W, row l mod 16 of x
             const uint32_t n = n0 + (t + t0) / H::kMT * 16u + q * 4u, m = (t + t0) % H::kMT * 16u + r;
             if (m >= M) continue;
+            if (kFormat == kMx) {
+                float any = 0.0f;  // NaN where one is not finite
+#pragma unroll
+                for (int e = 0; e < 4; ++e) any = __builtin_fmaf(sum[e], 0.0f, any);
+                again |= any != any ? 1u << (t + t0) : 0u;
+            }
 #pragma unroll
             for (int e = 0; e < 4; ++e) sum[e] = sum[e] * scale * a.alpha;
             store4(a, m0 + m, n, sum);
+        }
+    }
+    if constexpr (kFormat == kMx) {
+        if (__ballot(again != 0u) == 0u) return;
+        for (uint32_t j = 0; j < (uint32_t)kR; ++j) {
+            const uint32_t mine_again = again >> (j * H::kMT) & ((1u << H::kMT) - 1u), n = n0 + 16u * j;
+            if (__ballot(mine_again != 0u) == 0u) continue;
+            const uint32_t which = large_rows(a, n, r, q) >> (4u * q) & 15u;
+            for (uint32_t i = 0; i < (uint32_t)H::kMT; ++i)
+                if (mine_again >> i & 1u) again4<kX8>(a, m0 + 16u * i + r, n + 4u * q, which);
         }
     }
 }

@@ -525,9 +525,10 @@ FP4Q_API fp4q_status fp4_swiglu_grad_pack8(const void *dh, int64_t ld_dh, const 
  * 0 <= M <= 64 (FP4Q_EUNSUPPORTED above: quantize x and use the GEMM).  W is
  * the logical [N x K] operand as the producers write it for the GEMMs, in
  * `layout`; every product of a weight and an element of x is exact (as far as
- * binary32 holds it), the sums are binary32 in an order that depends on the
- * sizes and the card alone (and up to M = 16 not on M: a row's bits are then
- * those of the row by itself), alpha (and a global tensor scale) multiplies
+ * binary32 holds it), the sums are binary32 (binary64 where MXFP4 weights of
+ * 2^128 or more, scale bytes 253 and 254, are in them) in an order that
+ * depends on the sizes and the card alone (and up to M = 16 not on M: a row's
+ * bits are then those of the row by itself), alpha (and a global tensor scale) multiplies
  * them, and one rounding gives Y's type (a value of fp4q_out, pitch ld_y >=
  * N).  K % 128 == 0 (FP4Q_ESHAPE); K == 0 gives zeros.  NaN and Inf in x stay
  * within their row of Y.
