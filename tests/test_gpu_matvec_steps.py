@@ -145,3 +145,17 @@ def test_8_bit_rows_at_ordinary_sizes(tiled, m, n, k):
     w.check(same, v.to(F64), "the rows unpacked")
     if m <= 16:
         assert torch.equal(y, same)
+
+
+@pytest.mark.parametrize("tiled", [False, True])
+@pytest.mark.parametrize("n,k", [(4096, 4096), (9000, 2560), (28641, 4096)])
+def test_8_bit_rows_have_the_bits_of_the_rows_unpacked(tiled, n, k):
+    """Up to 16 rows, where the order of the sums does not depend on x's type."""
+    dev = device()
+    announce(f"matvec of 8-bit rows and of the rows unpacked, tiled {tiled} {n} x {k}")
+    w = Weights("mx", n, k, tiled, dev, 5)
+    args = w.call()
+    x = draw((16, k), 3, BF, 5.0).to(dev)
+    v = B.fp4_unpack8(*B.fp4_pack8(x))
+    for m in (1, 3, 5, 8, 12, 16):
+        assert torch.equal(product(w, x[:m], args, x8=True), product(w, v[:m], args)), m
