@@ -536,17 +536,23 @@ void pick_layout(const Matvec &a, bool linear, uint32_t units, hipStream_t st)
 // most of what it reads and stages; groups of x's rows in workgroups of their
 // own read W again (from the L2, being on one XCD and under way together).
 // The cost of a unit's rows of W (16 each) and of x (four each) is weighed as
-// measured: NVFP4's converts, and W in rows, count for more.
+// measured: NVFP4's converts, and W in rows, count for more.  x's type does not
+// (8-bit rows may not be summed in another order than the rows unpacked; four
+// for them with W in rows instead of eight: 32 x 4096 x 4096 7.0 us instead of
+// 6.1, 64 x 8192 x 4096 13.9 instead of 11.2).  More groups have to win a
+// sixteenth: any less, and 20 x 2000 x 4096 in rows takes 5.7 us instead of 5.1,
+// 48 x 6144 x 4096 11.0 instead of 9.9, 20 x 11008 x 4096 tiled 9.6 instead of 8.7
+// (the other way, 48 x 5000 x 4096 NVFP4 tiled 9.4 instead of 10.7).
 //   us from memory, one group / as many as this gives: 32 rows of x, MXFP4 tiled
 // 512 x 8192 11.1 / 5.2, 4096 x 4096 7.5 / 6.0, 4096 x 14336 18.4 / 14.3, 8192 x
 // 4096 8.4 / 7.7, NVFP4 2000 x 14336 18.6 / 12.5; 64 rows, MXFP4 4096 x 4096 11.2 /
 // 7.2; 16 rows 512 x 8192 7.7 / 5.3.  24 rows, in two groups where this gives
 // one: MXFP4 12000 x 8192 15.1 / 16.2, in rows 20.4 / 23.8.
-uint32_t group_rows(const Matvec &a, bool nv, bool x8, bool linear, uint32_t units)
+uint32_t group_rows(const Matvec &a, bool nv, bool linear, uint32_t units)
 {
     uint32_t whole = 4u;
     while (whole < a.M) whole *= 2u;
-    const uint32_t blocks = (a.w.N + 15u) / 16u, of_w = nv ? 24u : linear ? 14u : 9u, of_x = x8 && linear ? 4u : 8u;
+    const uint32_t blocks = (a.w.N + 15u) / 16u, of_w = nv ? 24u : linear ? 14u : 9u, of_x = 8u;
     uint32_t best = whole, least = 0u;
     for (uint32_t rows = whole; rows >= 4u; rows /= 2u) {
         const uint32_t groups = (a.M + rows - 1u) / rows, each = (blocks * groups + units - 1u) / units;
@@ -564,7 +570,7 @@ template <Format kFormat, bool kX8>
 void pick_matvec(const Matvec &a, bool linear, uint32_t units, hipStream_t st)
 {
     Matvec g = a;
-    const uint32_t rows = group_rows(a, kFormat != kMx, kX8, linear, units);
+    const uint32_t rows = group_rows(a, kFormat != kMx, linear, units);
     g.groups = (a.M + rows - 1u) / rows;
     if (rows <= 4u)
         pick_layout<kFormat, kX8, 1>(g, linear, units, st);

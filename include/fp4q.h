@@ -527,10 +527,10 @@ FP4Q_API fp4q_status fp4_swiglu_grad_pack8(const void *dh, int64_t ld_dh, const 
  * `layout`; every product of a weight and an element of x is exact (as far as
  * binary32 holds it), the sums are binary32 (binary64 where MXFP4 weights of
  * 2^128 or more, scale bytes 253 and 254, are in them) in an order that
- * depends on the sizes, W's format and layout, x's type and the card alone,
- * and up to M = 16 neither on M nor on x's type: a row's bits are then those of
- * the row by itself, and of an 8-bit row those of the row unpacked.  alpha (and
- * a global tensor scale) multiplies them, and one rounding gives Y's type (a
+ * depends on the sizes, W's format and layout and the card alone, and up to
+ * M = 16 not on M (a row's bits are then those of the row by itself; 8-bit
+ * rows always give the bits of the rows unpacked).  alpha (and a global
+ * tensor scale) multiplies them, and one rounding gives Y's type (a
  * value of fp4q_out, pitch ld_y >= N).  K % 128 == 0 (FP4Q_ESHAPE); K == 0
  * gives zeros whatever alpha is.  NaN and Inf in x stay within their row of Y.
  * x: bf16, 16-byte aligned, ld_x a multiple of 8 (FP4Q_EALIGN).  Codes, scales

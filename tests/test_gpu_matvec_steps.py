@@ -131,8 +131,7 @@ def test_same_bits_from_other_kernels(fmt, tiled, n, k):
 @pytest.mark.parametrize("tiled", [False, True])
 @pytest.mark.parametrize("m,n,k", [(1, 4096, 14336), (17, 4096, 4096), (32, 4096, 4096), (64, 9000, 2560)])
 def test_8_bit_rows_at_ordinary_sizes(tiled, m, n, k):
-    """Against binary64; and up to 16 rows with the bits of the rows unpacked (above, the two types of x may be summed in
-    another order)."""
+    """Against binary64, 8-bit rows and the same rows unpacked."""
     dev = device()
     announce(f"matvec of 8-bit rows tiled {tiled} {m} x {n} x {k}")
     w = Weights("mx", n, k, tiled, dev, m)
@@ -143,19 +142,17 @@ def test_8_bit_rows_at_ordinary_sizes(tiled, m, n, k):
     w.check(y, v.to(F64), "8-bit rows")
     same = product(w, v, args)
     w.check(same, v.to(F64), "the rows unpacked")
-    if m <= 16:
-        assert torch.equal(y, same)
 
 
 @pytest.mark.parametrize("tiled", [False, True])
-@pytest.mark.parametrize("n,k", [(4096, 4096), (9000, 2560), (28641, 4096)])
+@pytest.mark.parametrize("n,k", [(2000, 4096), (4096, 4096), (8192, 2048), (9000, 2560), (28641, 4096)])
 def test_8_bit_rows_have_the_bits_of_the_rows_unpacked(tiled, n, k):
-    """Up to 16 rows, where the order of the sums does not depend on x's type."""
+    """The order of the sums does not depend on x's type."""
     dev = device()
     announce(f"matvec of 8-bit rows and of the rows unpacked, tiled {tiled} {n} x {k}")
     w = Weights("mx", n, k, tiled, dev, 5)
     args = w.call()
-    x = draw((16, k), 3, BF, 5.0).to(dev)
+    x = draw((64, k), 3, BF, 5.0).to(dev)
     v = B.fp4_unpack8(*B.fp4_pack8(x))
-    for m in (1, 3, 5, 8, 12, 16):
+    for m in (1, 3, 5, 8, 12, 16, 17, 24, 32, 40, 48, 64):
         assert torch.equal(product(w, x[:m], args, x8=True), product(w, v[:m], args)), m
