@@ -476,7 +476,8 @@ void run_matvec(const Matvec &a, uint32_t most, hipStream_t st)
 template <Format kFormat, bool kX8, int kMQ, int kP, int kR>
 void pick_rows(const Matvec &a, uint32_t r, uint32_t most, hipStream_t st)
 {
-    if constexpr (kR > (kMQ == 16 ? 2 : 1)) {  // (16 rows of W alone get at most 32 of x)
+    // with fewer rows of W to a unit, x's are in groups of 32 at most (group_rows)
+    if constexpr (kR > (kMQ < 16 ? 1 : kFormat == kMx ? 4 : 3)) {
         if (r < (uint32_t)kR) return pick_rows<kFormat, kX8, kMQ, kP, kR - 1>(a, r, most, st);
     }
     run_matvec<kFormat, kX8, kMQ, kR, kP>(a, most, st);
@@ -518,7 +519,7 @@ void pick_waves(const Matvec &a, uint32_t units, hipStream_t st)
         run_matvec<kFormat, kX8, 1, 1, kP>(a, waves, st);
     } else {
         const uint32_t groups = (each + kMost - 1u) / kMost, r = (each + groups - 1u) / groups;
-        const bool eight = groups == 1u && ((kMQ == 8 && r * kP > 4u) || (kMQ == 16 && r <= 3u));
+        const bool eight = groups == 1u && ((kMQ == 8 && r * kP > 4u) || (kMQ == 16 && r == 3u));
         pick_rows<kFormat, kX8, kMQ, kP, kMost>(a, r, eight ? 8u : waves, st);
     }
 }
