@@ -24,8 +24,8 @@
 // fifths of those are the products of codes and scales, twice MXFP4's); 28672 x
 // 4096 MXFP4 with 16 rows 12.9, 32 8-bit rows 15.3, 64 rows 23.0 (x's way from
 // the L2 through LDS, the converts and the MFMAs, 5 to 7 us each, overlap in
-// part); 32 rows, 4096 x 14336 14.3 (where a compute unit reads as much of x as
-// of W).  The first kernel, whose lanes loaded x in the MFMA's layout
+// part); 32 rows, 4096 x 14336 14.3 (where a compute unit reads 448 KiB of x and
+// 238 of W).  The first kernel, whose lanes loaded x in the MFMA's layout
 // instead of whole lines, took 33 us for the 32 rows and 81 for the 64.
 #pragma once
 
@@ -493,22 +493,21 @@ void pick_rows(const Matvec &a, uint32_t r, uint32_t most, hipStream_t st)
 // rows of W, whose loads are all that is under way.  The waves, and so the
 // order of the sums, do not depend on x's rows up to 16.
 //   Measured in us on weights from memory, K = 4096, MXFP4 tiled unless named.
-// Rows of W to a wave: 64 rows of x, 28672 rows of W, two workgroups of 64 /
-// one of 112 with four waves 26.4 / 23.1 (in rows 35.5 / 27.8, NVFP4 tiles 32
-// / 112 41.2 / 29.9); 32 rows of x, W in rows, 64 / 112 24.6 / 21.6 (NVFP4
-// tiles 80 / 112 21.5 / 22.9); 16 rows of x, in rows 64 / 112 19.2 / 18.2.
-//   At a lower clock: 16 rows of x, 16 / 32 / 48 / 64 / 80 / 112 rows of W to a
-// wave: 8192 rows of W 14 / 11.6 / 12.5, 11008 - / 16.6 / 13.2 / 14.1 / 16.3,
-// 28672 - / - / 28.8 / 24.6 / 26.8 / 23.1, 40000 (80 each for two workgroups) -
-// / - / - / 33.7 / 29.9 / 34.8.  One row of x, 16 / 32: 11008 11.1 / 12.1, 28672
-// 20.7 / 21.6, 60000 38.2 / 38.3.
-//   Waves: 64 rows of x in one workgroup, eight / four with one step in flight,
-// 4096 rows of W 11.3 / 13.0, 8192 12.3 / 13.7.  At the lower clock four of two steps / eight
-// of two / eight of one, 16 rows of x: 8192 11.6 / 12.0 / 12.5, 14336 14.7 / 15.6
-// / 15.8, 28672 23.1 / 24.3 / 23.3; 32 rows of x: 14336 18.5 / 19.3 / 19.4, but
-// 28672 30.1 / 33.3 / 27.7; 4096 rows of W: 9.8 / 9.5 / 10.5, and with K = 14336
-// 23.3 / 21.5 / 23.3 and sixteen of two 21.7; one row of x there 19.4 / 14.1 / -
-// / 13.3.
+// Rows of W to a wave: 16 rows of x, 16 / 32 / 48 / 64 / 80 / 112: 8192 rows of W
+// 8.0 / 6.4, 11008 10.7 / 9.7 / 7.3 / 8.0, 28672 - / 17.2 / 16.5 / 14.3 / 16.1 /
+// 12.9 (in rows - / - / - / 19.3 / 22.5 / 18.5), 40000, 80 each for two workgroups
+// and one of 112 for a first and most of a second round, - / - / - / 19.8 / 17.5
+// / 20.4; 28672 rows of W, 64 / 80 / 112: 32 rows of x 18.8 / 22.2 / 16.2, in rows
+// 27.4 / 31.3 / 21.7 (NVFP4 tiles 21.7 / 24.5, and 112, not kept, 22.9); 64 rows
+// of x 26.0 / 36.4 / 23.5, in rows 35.5 / 40.1 / 27.7, NVFP4 tiles 42.4 / 46.8 / 30.0.  One row
+// of x, 16 / 32: 11008 6.5 / 7.2, 28672 12.1 / 12.3, 60000 22.4 / 21.7; four rows,
+// 28672 13.0 / 12.5.
+//   Waves, four / eight: 16 rows of x 4096 rows of W 5.7 / 5.4, 8192 7.3 / 7.4, 14336
+// 8.4 / 8.9, 28672 12.9 / 13.2; 32 rows of x, two steps in flight, 14336 10.9 /
+// 11.2, one step, 20480 14.0 / 13.1, 28672 16.8 / 16.2; 64 rows of x, 12000 NVFP4
+// 16.7 / 15.1.  Four / eight / sixteen, one row of x, 4096 rows of W 5.1 / 4.3 / 4.3,
+// with K = 14336 12.0 / 8.4 / 7.9 (16 rows of x 13.2 / 12.6 / 12.7: they keep one
+// row's waves).
 template <Format kFormat, bool kX8, int kMQ, int kP>
 void pick_waves(const Matvec &a, uint32_t units, hipStream_t st)
 {

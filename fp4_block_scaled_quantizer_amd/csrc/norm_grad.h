@@ -24,6 +24,13 @@
 // 19: 4096 rows 145 us, 4.6 TB/s), four chunks up to 16 for bf16 and 63 for
 // binary32, ragged 131 (4096 x 24000 bf16 199 us, 4096 x 24001 508: there the
 // rows' kernel moves more than three times its rows' bytes).
+// Two chunks of 8-bit rows beside bf16 dy (two rows in flight, each with a
+// scale register a chunk) spill more than bf16 rows: with sums, dres 15 against
+// 7, dropout 17 / 2, both 31 / 19; walked without sums, both 17 / 1 (binary32 dy,
+// with sums, dropout 18 / 12, both 10 / 4).  4096 x 16384, RMS norm, 8-bit / own
+// rows, us: bf16 72 / 83, dres 103 / 104, dropout 115 / 105, both 155 / 136, so that
+// with dropout the bytes saved do not pay; binary32 117 / 154, 166 / 207, 218 /
+// 231, 232 / 255.
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -403,9 +410,13 @@ __global__ __launch_bounds__(1024) void norm_weight_sums_kernel(const NormGradAr
 // (kRowsWalked), whose loads then never pause; up to 3 * 2^20 elements, where
 // there is little to walk, each workgroup has its first rows only (kNoSums).
 // Walked / not, us, bf16: 8192 x 4096 36.2 / 50.7, 2048 x 4096 11.8 / 14.7,
-// 365 x 8192 6.8 / 7.1 (with dres and dropout 9.4 / 8.8), 2048 x 1024 5.5 /
-// 4.7, 10000 x 256 6.2 / 5.9; two chunks a thread 400 x 9000 7.4 / 8.3, 219 x
-// 14336 7.6 / 5.9; binary32 512 x 4096 8.0 / 7.7, 768 x 4096 10.9 / 11.7.
+// 365 x 8192 6.8 / 7.1 (with dres and dropout 9.4 / 8.8), 2048 x 1024 5.4 /
+// 4.5, but 3000 x 1024 6.0 / 7.3 (with dres and dropout 8.6 / 9.1), 10000 x 256
+// 6.0 / 5.7; two chunks a thread 400 x 9000 7.4 / 8.3, 219 x 14336 7.6 / 5.6;
+// binary32 512 x 4096 7.5 / 7.1, 768 x 4096 11.0 / 11.8.  The limit is between
+// the calls' kinds: with one to two workgroups a unit, 22
+// widths of 8 to 16384, walked takes 0.80 to 1.06 of the other's time, with
+// dres and dropout 0.88 to 1.21 (8-bit rows 0.79 to 1.05, and 0.88 to 1.74).
 enum How { kNoSums, kRowsWalked, kInRows, kBeside, kApart };
 struct GradPlan {
     How sums;
