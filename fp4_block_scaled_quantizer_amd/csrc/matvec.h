@@ -17,12 +17,12 @@
 // take the columns' steps in turn and join their sums through LDS in a fixed
 // order.
 //   Weights from memory (where a copy reads and writes 6.3 TB/s), us a call:
-// one row of x, MXFP4 tiled 4096 x 4096 4.7 (launch), 28672 x 4096 12.1 (5.2
-// TB/s, HBM; in rows 14.6, NVFP4 tiles 14.6), 4096 x 14336 8.0; 5 rows, NVFP4 4096
-// x 14336 tiled 10.2, in rows 12.0 (a compute unit has 16 rows of W, whose start,
+// one row of x, MXFP4 tiled 4096 x 4096 4.6 (launch), 28672 x 4096 12.1 (5.2
+// TB/s, HBM; in rows 14.7, NVFP4 tiles 14.4), 4096 x 14336 8.0; 5 rows, NVFP4 4096
+// x 14336 tiled 10.1, in rows 12.0 (a compute unit has 16 rows of W, whose start,
 // 85 vector instructions a step of 128 columns and join are not hidden: four
 // fifths of those are the products of codes and scales, twice MXFP4's); 28672 x
-// 4096 MXFP4 with 16 rows 12.9, 32 8-bit rows 15.3, 64 rows 23.0 (x's way from
+// 4096 MXFP4 with 16 rows 12.9, 32 8-bit rows 15.3, 64 rows 23.2 (x's way from
 // the L2 through LDS, the converts and the MFMAs, 5 to 7 us each, overlap in
 // part); 32 rows, 4096 x 14336 14.3 (where a compute unit reads 448 KiB of x and
 // 238 of W).  The first kernel, whose lanes loaded x in the MFMA's layout

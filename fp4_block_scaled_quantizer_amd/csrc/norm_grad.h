@@ -413,10 +413,10 @@ __global__ __launch_bounds__(1024) void norm_weight_sums_kernel(const NormGradAr
 // 365 x 8192 6.8 / 7.1 (with dres and dropout 9.4 / 8.8), 2048 x 1024 5.4 /
 // 4.5, but 3000 x 1024 6.0 / 7.3 (with dres and dropout 8.6 / 9.1), 10000 x 256
 // 6.0 / 5.7; two chunks a thread 400 x 9000 7.4 / 8.3, 219 x 14336 7.6 / 5.6;
-// binary32 512 x 4096 7.5 / 7.1, 768 x 4096 11.0 / 11.8.  The limit is between
-// the calls' kinds: with one to two workgroups a unit, 22
-// widths of 8 to 16384, walked takes 0.80 to 1.06 of the other's time, with
-// dres and dropout 0.88 to 1.21 (8-bit rows 0.79 to 1.05, and 0.88 to 1.74).
+// binary32 512 x 4096 7.5 / 7.1, 768 x 4096 11.0 / 11.8.  The limit lies between
+// the calls' kinds: with one to two workgroups a unit, 22 widths of 8 to 16384,
+// walked takes 0.80 to 1.06 of the other's time, with dres and dropout 0.88 to
+// 1.21 (8-bit rows 0.79 to 1.05, and 0.88 to 1.74).
 enum How { kNoSums, kRowsWalked, kInRows, kBeside, kApart };
 struct GradPlan {
     How sums;
