@@ -15,6 +15,19 @@ FORMATS = ["mx", "nv", "nv tile"]
 U = 2.0 ** -24
 
 
+@pytest.fixture(scope="module", autouse=True)
+def products_on_the_gpu():
+    """The oracle's products run on the GPU, and torch keeps the memory that its matrix library works in: made before
+    there is a large block that it could be cut from, it lets go of those when they are free."""
+    if torch.cuda.is_available():
+        torch.cuda.empty_cache()
+        one = torch.ones((8, 8), dtype=F64, device="cuda")
+        assert float((one @ one.t()).sum()) == 512
+    yield
+    if torch.cuda.is_available():
+        torch.cuda.empty_cache()
+
+
 class Weights:
     """Random codes and scales (few binary orders apart, so that no product is lost in a sum), in a layout."""
 

@@ -8,6 +8,14 @@ from tests.gpu_common import B, announce, device
 pytestmark = pytest.mark.gpu
 
 
+@pytest.fixture(autouse=True)
+def give_back():
+    """Some 45 GB, which later tests neither need nor expect in torch's cache."""
+    yield
+    if torch.cuda.is_available():
+        torch.cuda.empty_cache()
+
+
 def test_unpack_in_more_than_one_part():
     """Rows of 2^13 pieces of four binary32 elements: 2^18 rows in the first part, three in the second."""
     dev = device()
